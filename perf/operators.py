@@ -168,12 +168,13 @@ def _scan_time(a, u):
 
 
 def _scan_back(a, u, last):
-    """g_t = u_t + a_{t+1} g_{t+1} along axis 1, g_{L-1} = u_{L-1} + last; overwrites u."""
+    """g_t = u_t + a_{t+1} g_{t+1} along axis 1, g_{L-1} = u_{L-1} + last."""
+    u = u.flip(1)
     if last is not None:
-        u[:, -1] += last
+        u[:, 0] += last
     step = torch.zeros_like(a)
     step[:, 1:] = a[:, 1:].flip(1)
-    return _scan_time(step, u.flip(1)).flip(1)
+    return _scan_time(step, u).flip(1)
 
 
 def _gates(r, i, lam, reset):
