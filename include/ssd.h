@@ -309,6 +309,91 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A,
                               ssd_stream stream);
 
 /*
+ * A gated linear recurrence with one state per channel: the diagonal
+ * recurrence of the selective scan ("精读笔记 #12：Mamba", section 3.5: the
+ * discretised step acts as a gate) with the state expansion removed and the
+ * decay and the input gated per token and channel:
+ *
+ *     s_t = -c softplus(lam_d) sigmoid(r_t)     a_t = exp(s_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t
+ *
+ * A token whose reset byte is nonzero begins a new sequence: its a_t is 0 (so
+ * that h_t = sigmoid(i_t) x_t), and nothing passes from the tokens before it,
+ * in either direction. dims->nheads is the number of channels D; headdim,
+ * dstate and ngroups must be 1. dims->dtype is the type of x, r, i, y and of
+ * their gradients; states and parameters are fp32, sums are held in fp32.
+ *
+ *   x, r, i   (batch, seqlen, D)  I/O type: input, and the raw gates
+ *   lam       (D) fp32
+ *   c         > 0, finite
+ *   reset     (batch, seqlen) bytes, or NULL for none
+ *   h0        (batch, D) fp32, or NULL for zeros
+ *   y         (batch, seqlen, D)  I/O type, written
+ *   h_final   (batch, D) fp32, written, or NULL; may alias h0
+ *   states    (batch, nblocks, D) fp32, written, or NULL: the state entering
+ *             each block of SSD_GATED_BLOCK tokens, nblocks = the blocks of
+ *             seqlen rounded up. The backward pass starts from them.
+ *   ckpt_q, ckpt_e
+ *             both or neither: the inputs in 8 bits for the backward pass.
+ *             ckpt_q (3, batch, seqlen, D) int8 and ckpt_e (3, batch, nblocks,
+ *             D) bytes, x, r and i in this order. A channel's values of one
+ *             block share a step, the least power of two 2^e (e >= -126) whose
+ *             127-fold reaches the largest magnitude: value = q 2^e, q rounded
+ *             to nearest (ties to even), and the byte holds e + 127. A block
+ *             that holds an infinity or a NaN has the byte 255 and q = 0 and
+ *             reads as NaN.
+ *   workspace, workspace_bytes as for ssd_forward, sized by
+ *             ssd_gated_scan_workspace_size
+ *
+ * Tensors need the alignment of their element type; 16-byte alignment and an
+ * even D (fp32) or D a multiple of 2 (bf16) are faster. Outputs may not alias
+ * inputs, but for h_final and h0. seqlen 0 copies h0 to h_final.
+ */
+#define SSD_GATED_BLOCK 64
+
+size_t ssd_gated_scan_workspace_size(const ssd_dims *dims);
+ssd_status ssd_gated_scan(const void *x, const void *r, const void *i, const float *lam, float c,
+                          const uint8_t *reset, const float *h0, void *y, float *h_final,
+                          float *states, int8_t *ckpt_q, uint8_t *ckpt_e, const ssd_dims *dims,
+                          void *workspace, size_t workspace_bytes, ssd_stream stream);
+
+/*
+ * Backward pass of ssd_gated_scan for the scalar loss
+ * sum dy . y + sum dh_final . h_final, from the inputs x, r and i, or from
+ * their 8-bit copies (x, r and i NULL, ckpt_q and ckpt_e given): the gradients
+ * are then those of the recurrence on the values that the copies stand for,
+ * each block entered with its saved state, passed straight through the
+ * rounding.
+ *
+ *   states    (batch, nblocks, D) fp32 from ssd_gated_scan
+ *   dy        (batch, seqlen, D) I/O type
+ *   dh_final  (batch, D) fp32, or NULL for zeros
+ *   dx, dr, di (batch, seqlen, D) I/O type, written
+ *   dlam      (D) fp32, written: summed over batch and tokens, in an order
+ *             that does not change between calls
+ *   dh0       (batch, D) fp32, written, or NULL; may alias dh_final
+ *
+ * c and reset as in the forward. Outputs may not alias inputs, but for dh0 and
+ * dh_final. seqlen 0 gives dlam = 0 and dh0 = dh_final.
+ */
+size_t ssd_gated_scan_backward_workspace_size(const ssd_dims *dims);
+ssd_status ssd_gated_scan_backward(const void *x, const void *r, const void *i,
+                                   const int8_t *ckpt_q, const uint8_t *ckpt_e, const float *lam,
+                                   float c, const uint8_t *reset, const float *states,
+                                   const void *dy, const float *dh_final, void *dx, void *dr,
+                                   void *di, float *dlam, float *dh0, const ssd_dims *dims,
+                                   void *workspace, size_t workspace_bytes, ssd_stream stream);
+
+/*
+ * One token of the gated recurrence, in place, for generation: h (batch, D)
+ * fp32 is read and overwritten, y (batch, D) written in the I/O type; x, r, i
+ * (batch, D). dims as for ssd_gated_scan, seqlen ignored. y may not alias h or
+ * an input.
+ */
+ssd_status ssd_gated_step(float *h, const void *x, const void *r, const void *i, const float *lam,
+                          float c, void *y, const ssd_dims *dims, ssd_stream stream);
+
+/*
  * Backward pass of the layer (the plain forward of ssd_forward: decay
  * exp(dt A_h), input weight dt; step options are not differentiated), by the
  * chunked decomposition with the chunk states recomputed ("精读笔记 #12：

@@ -33,6 +33,8 @@ class Dims(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+SSD_GATED_BLOCK = 64
+
 SSD_DISC_EULER = 0
 SSD_DISC_ZOH = 1
 
@@ -74,6 +76,13 @@ _SIGNATURES = {
                                        ctypes.POINTER(Dims), _VP]),
     "ssd_selective_scan": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                           ctypes.POINTER(Dims), ctypes.POINTER(Options), _VP]),
+    "ssd_gated_scan_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
+    "ssd_gated_scan": (ctypes.c_int, [_VP] * 4 + [ctypes.c_float] + [_VP] * 7 +
+                       [ctypes.POINTER(Dims), _VP, ctypes.c_size_t, _VP]),
+    "ssd_gated_scan_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
+    "ssd_gated_scan_backward": (ctypes.c_int, [_VP] * 6 + [ctypes.c_float] + [_VP] * 9 +
+                                [ctypes.POINTER(Dims), _VP, ctypes.c_size_t, _VP]),
+    "ssd_gated_step": (ctypes.c_int, [_VP] * 5 + [ctypes.c_float, _VP, ctypes.POINTER(Dims), _VP]),
     "ssd_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
     "ssd_backward": (ctypes.c_int, [_VP] * 16 + [ctypes.POINTER(Dims), _VP, ctypes.c_size_t,
                                                  _VP]),

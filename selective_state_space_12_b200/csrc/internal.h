@@ -118,6 +118,33 @@ ssd_status scan_launch(const Problem &pr, const void *x, const void *dt, const f
                        const void *B, const void *C, const float *Dskip, const float *h0,
                        void *y, float *h_final, const DtPre &pre, cudaStream_t st);
 
+// --- gated linear recurrence (one state per channel; nheads = channels), see gated.cu ---
+struct GatedArgs {
+    const void *x = nullptr, *r = nullptr, *i = nullptr;  // or, in the backward pass,
+    int8_t *q = nullptr;                                  // their 8-bit copies (3, b, L, D)
+    uint8_t *e = nullptr;                                 // and step codes (3, b, nb, D)
+    const float *lam = nullptr;
+    float c = 0.f;
+    const uint8_t *reset = nullptr;
+    float *states = nullptr;  // (b, nb, D): the state entering each block
+    void *y = nullptr;
+    const void *dy = nullptr;
+    void *dx = nullptr, *dr = nullptr, *di = nullptr;
+    // set by the launchers
+    int64_t batch = 0, L = 0, D = 0, nb = 0, dblocks = 0;
+    float2 *sums = nullptr;      // (b, nb, D): each block's map
+    float *grads = nullptr;      // (b, nb, D): the gradient entering each block from its right
+    float *dlam_part = nullptr;  // (b, nb, D)
+};
+int64_t gated_blocks(const Problem &pr);
+size_t gated_workspace_bytes(const Problem &pr, bool back);
+ssd_status gated_forward_launch(const Problem &pr, GatedArgs a, const float *h0, float *h_final,
+                                void *ws, cudaStream_t st);
+ssd_status gated_backward_launch(const Problem &pr, GatedArgs a, const float *dh_final,
+                                 float *dlam, float *dh0, void *ws, cudaStream_t st);
+ssd_status gated_step_launch(const Problem &pr, float *h, const void *x, const void *r,
+                             const void *i, const float *lam, float c, void *y, cudaStream_t st);
+
 // --- decode step ---
 ssd_status step_launch(const Problem &pr, float *h, const void *x, const void *dt,
                        const float *A, const void *B, const void *C, const float *D,

@@ -120,6 +120,88 @@ ssd_status read_options(const ssd_options *o, DtPre *pre) {
     return SSD_OK;
 }
 
+// Sizes of the gated recurrence: nheads = channels, one state each.
+ssd_status check_gated_dims(const ssd_dims *d, bool need_seq) {
+    if (!d) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    if (d->reserved != 0) return fail(SSD_ERR_INVALID_ARG, "dims.reserved must be 0");
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "dims.dtype %d is not SSD_F32 or SSD_BF16", d->dtype);
+    if (d->batch < 1 || d->nheads < 1 || (need_seq && d->seqlen < 0))
+        return fail(SSD_ERR_INVALID_ARG, "sizes must be positive (seqlen >= 0)");
+    if (d->headdim != 1 || d->dstate != 1 || d->ngroups != 1)
+        return fail(SSD_ERR_INVALID_ARG, "gated scan: headdim, dstate and ngroups must be 1 (one "
+                                         "state per channel), got %lld, %lld, %lld",
+                    (long long)d->headdim, (long long)d->dstate, (long long)d->ngroups);
+    const int64_t blocks = need_seq ? (d->seqlen + SSD_GATED_BLOCK - 1) / SSD_GATED_BLOCK : 1;
+    if (d->batch > 65535 || d->nheads > (int64_t)1 << 24 ||
+        (need_seq && d->seqlen > (int64_t)1 << 30) ||
+        (double)d->batch * (double)((d->nheads + 31) / 32) * (double)blocks > 2.0e9)
+        return fail(SSD_ERR_UNSUPPORTED, "gated scan: batch above 65535, channels above 2^24, "
+                                         "seqlen above 2^30, or all three too large together");
+    return SSD_OK;
+}
+
+// Takes `need` bytes of workspace on the stream where the caller gave none.
+ssd_status take_workspace(void *given, size_t given_bytes, size_t need, cudaStream_t st, void **ws,
+                          bool *owned) {
+    *ws = given;
+    *owned = false;
+    if (given) {
+        if (given_bytes < need)
+            return fail(SSD_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", given_bytes,
+                        need);
+        if (!aligned(given, 256))
+            return fail(SSD_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    } else if (need > 0) {
+        const cudaError_t e = cudaMallocAsync(ws, need, st);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(SSD_ERR_NO_MEMORY, "cudaMallocAsync of %zu workspace bytes: %s", need,
+                        cudaGetErrorString(e));
+        }
+        *owned = true;
+    }
+    return SSD_OK;
+}
+
+ssd_status give_back(void *ws, bool owned, cudaStream_t st, ssd_status s) {
+    if (owned) {
+        const cudaError_t e = cudaFreeAsync(ws, st);
+        if (e != cudaSuccess && s == SSD_OK) s = cuda_fail(e, "cudaFreeAsync of the workspace");
+    }
+    return s;
+}
+
+struct Named {
+    const void *p;
+    const char *name;
+};
+
+// No output may be one of the inputs (NULLs aside).
+template <int NO, int NI>
+ssd_status check_aliases(const Named (&outs)[NO], const Named (&ins)[NI]) {
+    for (const Named &o : outs)
+        for (const Named &i : ins)
+            if (o.p && o.p == i.p)
+                return fail(SSD_ERR_INVALID_ARG, "%s aliases %s", o.name, i.name);
+    return SSD_OK;
+}
+
+template <int N>
+ssd_status check_aligned(const Named (&ps)[N], size_t a) {
+    for (const Named &p : ps)
+        if (p.p && !aligned(p.p, a))
+            return fail(SSD_ERR_INVALID_ARG, "%s is not %zu-byte aligned", p.name, a);
+    return SSD_OK;
+}
+
+ssd_status check_gate_power(float c) {
+    if (!(c > 0.f) || !(c < 3.0e38f))
+        return fail(SSD_ERR_INVALID_ARG, "gated scan: c must be positive and finite (got %g)",
+                    (double)c);
+    return SSD_OK;
+}
+
 }  // namespace
 
 ssd_status fail(ssd_status s, const char *fmt, ...) {
@@ -396,6 +478,127 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A, con
         return fail(SSD_ERR_INVALID_ARG, "y aliases an input");
     return scan_launch(pr, x, dt, A, B, C, Dskip, h0, y, h_final, pre,
                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t ssd_gated_scan_workspace_size(const ssd_dims *dims) {
+    if (check_gated_dims(dims, true) != SSD_OK) return 0;
+    return gated_workspace_bytes(make_problem(dims, 0), false);
+}
+
+size_t ssd_gated_scan_backward_workspace_size(const ssd_dims *dims) {
+    if (check_gated_dims(dims, true) != SSD_OK) return 0;
+    return gated_workspace_bytes(make_problem(dims, 0), true);
+}
+
+ssd_status ssd_gated_scan(const void *x, const void *r, const void *i, const float *lam, float c,
+                          const uint8_t *reset, const float *h0, void *y, float *h_final,
+                          float *states, int8_t *ckpt_q, uint8_t *ckpt_e, const ssd_dims *dims,
+                          void *workspace, size_t workspace_bytes_given, ssd_stream stream) {
+    ssd_status s = check_gated_dims(dims, true);
+    if (s != SSD_OK || (s = check_gate_power(c)) != SSD_OK) return s;
+    const Problem pr = make_problem(dims, 0);
+    const size_t esz = pr.dtype == SSD_F32 ? 4 : 2;
+    if (!lam) return fail(SSD_ERR_INVALID_ARG, "lam is NULL");
+    if (pr.seqlen > 0 && (!x || !r || !i || !y))
+        return fail(SSD_ERR_INVALID_ARG, "x, r, i and y must be non-NULL");
+    if ((ckpt_q == nullptr) != (ckpt_e == nullptr))
+        return fail(SSD_ERR_INVALID_ARG, "ckpt_q and ckpt_e go together");
+    const Named io[] = {{x, "x"}, {r, "r"}, {i, "i"}, {y, "y"}};
+    const Named f4[] = {{lam, "lam"}, {h0, "h0"}, {h_final, "h_final"}, {states, "states"}};
+    if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
+    const Named outs[] = {{y, "y"}, {states, "states"}, {ckpt_q, "ckpt_q"}, {ckpt_e, "ckpt_e"}};
+    const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {h0, "h0"}, {reset, "reset"}};
+    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void *ws;
+    bool owned;
+    s = take_workspace(workspace, workspace_bytes_given, gated_workspace_bytes(pr, false), st, &ws,
+                       &owned);
+    if (s != SSD_OK) return s;
+    GatedArgs a;
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.q = ckpt_q;
+    a.e = ckpt_e;
+    a.lam = lam;
+    a.c = c;
+    a.reset = reset;
+    a.states = states;
+    a.y = y;
+    s = gated_forward_launch(pr, a, h0, h_final, ws, st);
+    return give_back(ws, owned, st, s);
+}
+
+ssd_status ssd_gated_scan_backward(const void *x, const void *r, const void *i,
+                                   const int8_t *ckpt_q, const uint8_t *ckpt_e, const float *lam,
+                                   float c, const uint8_t *reset, const float *states,
+                                   const void *dy, const float *dh_final, void *dx, void *dr,
+                                   void *di, float *dlam, float *dh0, const ssd_dims *dims,
+                                   void *workspace, size_t workspace_bytes_given,
+                                   ssd_stream stream) {
+    ssd_status s = check_gated_dims(dims, true);
+    if (s != SSD_OK || (s = check_gate_power(c)) != SSD_OK) return s;
+    const Problem pr = make_problem(dims, 0);
+    const size_t esz = pr.dtype == SSD_F32 ? 4 : 2;
+    if (!lam || !dlam) return fail(SSD_ERR_INVALID_ARG, "lam and dlam are required");
+    if ((ckpt_q == nullptr) != (ckpt_e == nullptr))
+        return fail(SSD_ERR_INVALID_ARG, "ckpt_q and ckpt_e go together");
+    if (ckpt_q && (x || r || i))
+        return fail(SSD_ERR_INVALID_ARG, "give x, r and i, or their 8-bit copies, not both");
+    if (pr.seqlen > 0 && ((!ckpt_q && (!x || !r || !i)) || !states || !dy || !dx || !dr || !di))
+        return fail(SSD_ERR_INVALID_ARG, "x, r, i (or their 8-bit copies), states, dy, dx, dr and "
+                                         "di must be non-NULL");
+    const Named io[] = {{x, "x"}, {r, "r"}, {i, "i"}, {dy, "dy"}, {dx, "dx"}, {dr, "dr"},
+                        {di, "di"}};
+    const Named f4[] = {{lam, "lam"}, {states, "states"}, {dh_final, "dh_final"}, {dlam, "dlam"},
+                        {dh0, "dh0"}};
+    if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
+    const Named outs[] = {{dx, "dx"}, {dr, "dr"}, {di, "di"}, {dlam, "dlam"}};
+    const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {ckpt_q, "ckpt_q"}, {ckpt_e, "ckpt_e"},
+                         {lam, "lam"}, {states, "states"}, {dy, "dy"}, {dh_final, "dh_final"},
+                         {reset, "reset"}};
+    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void *ws;
+    bool owned;
+    s = take_workspace(workspace, workspace_bytes_given, gated_workspace_bytes(pr, true), st, &ws,
+                       &owned);
+    if (s != SSD_OK) return s;
+    GatedArgs a;
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.q = const_cast<int8_t *>(ckpt_q);
+    a.e = const_cast<uint8_t *>(ckpt_e);
+    a.lam = lam;
+    a.c = c;
+    a.reset = reset;
+    a.states = const_cast<float *>(states);
+    a.dy = dy;
+    a.dx = dx;
+    a.dr = dr;
+    a.di = di;
+    s = gated_backward_launch(pr, a, dh_final, dlam, dh0, ws, st);
+    return give_back(ws, owned, st, s);
+}
+
+ssd_status ssd_gated_step(float *h, const void *x, const void *r, const void *i, const float *lam,
+                          float c, void *y, const ssd_dims *dims, ssd_stream stream) {
+    ssd_status s = check_gated_dims(dims, false);
+    if (s != SSD_OK || (s = check_gate_power(c)) != SSD_OK) return s;
+    const Problem pr = make_problem(dims, 0);
+    const size_t esz = pr.dtype == SSD_F32 ? 4 : 2;
+    if (!h || !x || !r || !i || !lam || !y)
+        return fail(SSD_ERR_INVALID_ARG, "h, x, r, i, lam and y must be non-NULL");
+    const Named io[] = {{x, "x"}, {r, "r"}, {i, "i"}, {y, "y"}};
+    const Named f4[] = {{h, "h"}, {lam, "lam"}};
+    if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
+    const Named outs[] = {{y, "y"}, {h, "h"}};
+    const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}};
+    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    if (y == (void *)h) return fail(SSD_ERR_INVALID_ARG, "y aliases h");
+    return gated_step_launch(pr, h, x, r, i, lam, c, y, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t ssd_backward_workspace_size(const ssd_dims *dims) {

@@ -324,6 +324,201 @@ def ssd_selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     return y, h_final
 
 
+def _gated_dims(batch, L, D, dtype) -> _lib.Dims:
+    return make_dims(batch, L, D, 1, 1, 1, dtype)
+
+
+def gated_blocks(seqlen: int) -> int:
+    """Blocks of SSD_GATED_BLOCK tokens in a sequence: the saved states, and
+    the steps of 8-bit checkpoints, of the gated scan."""
+    return -(-int(seqlen) // _lib.SSD_GATED_BLOCK)
+
+
+class GatedCheckpoint8:
+    """What ssd_gated_scan saves for a backward pass from 8-bit inputs.
+
+    ``q`` (3,b,L,D) int8 and ``e`` (3,b,nblocks,D) uint8: x, r and i as steps
+    of 2^(e - 127), one step for each channel and block of 64 tokens; and
+    ``states`` (b,nblocks,D) float32, the state entering each block. About
+    3.1 bytes for each token and channel, against 6 for the bf16 inputs."""
+
+    def __init__(self, batch: int, seqlen: int, channels: int, device="cuda"):
+        nb = gated_blocks(seqlen)
+        self.q = torch.empty((3, batch, seqlen, channels), dtype=torch.int8, device=device)
+        self.e = torch.empty((3, batch, nb, channels), dtype=torch.uint8, device=device)
+        self.states = torch.empty((batch, nb, channels), dtype=torch.float32, device=device)
+
+    def values(self) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """x, r and i (b,L,D) float32 as the backward pass reads them."""
+        L = self.q.shape[2]
+        step = torch.ldexp(torch.ones_like(self.e, dtype=torch.float32), self.e.int() - 127)
+        step = step.masked_fill(self.e == 255, float("nan"))
+        step = step.repeat_interleave(_lib.SSD_GATED_BLOCK, 2)[:, :, :L]
+        return tuple(self.q.float() * step)
+
+
+def _check_reset(reset, batch, L, dev):
+    if reset is not None:
+        if reset.dtype == torch.bool:
+            raise TypeError("reset must be uint8 (use reset.view(torch.uint8))")
+        _check_tensor("reset", reset, (batch, L), torch.uint8, dev)
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], dev):
+    """(tensor or None, bytes): the caller's workspace, or one from torch's allocator."""
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def ssd_gated_scan(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor,
+                   c: float = 8.0, reset: Optional[torch.Tensor] = None,
+                   h0: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   h_final: Optional[torch.Tensor] = None, want_final: bool = True,
+                   states: Optional[torch.Tensor] = None,
+                   checkpoint: Optional[GatedCheckpoint8] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """y, h_final of the gated recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2)
+    sigmoid(i_t) x_t, a_t = exp(-c softplus(lam) sigmoid(r_t)).
+
+    x, r, i, y (b,L,D) share one dtype (float32 or bfloat16); lam (D,), h0 and
+    h_final (b,D) are float32; reset (b,L) uint8, nonzero where a new sequence
+    begins. For training, ``states`` (b,gated_blocks(L),D) float32 receives the
+    state entering each block of 64 tokens, and ``checkpoint`` the inputs in 8
+    bits together with those states."""
+    lib = _lib.load()
+    batch, L, D = x.shape
+    dev, io = x.device, x.dtype
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        _check_tensor(name, t, (batch, L, D), io, dev)
+    _check_tensor("lam", lam, (D,), torch.float32, dev)
+    _check_reset(reset, batch, L, dev)
+    if h0 is not None:
+        _check_tensor("h0", h0, (batch, D), torch.float32, dev)
+    dims = _gated_dims(batch, L, D, io)
+    nb = gated_blocks(L)
+    q = e = None
+    if checkpoint is not None:
+        if states is not None:
+            raise ValueError("give states or a checkpoint (which holds them), not both")
+        states, q, e = checkpoint.states, checkpoint.q, checkpoint.e
+        _check_tensor("checkpoint.q", q, (3, batch, L, D), torch.int8, dev)
+        _check_tensor("checkpoint.e", e, (3, batch, nb, D), torch.uint8, dev)
+    if states is not None:
+        _check_tensor("states", states, (batch, nb, D), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    _check_tensor("y", y, (batch, L, D), io, dev)
+    if h_final is None and want_final:
+        h_final = torch.empty((batch, D), dtype=torch.float32, device=dev)
+    if h_final is not None:
+        _check_tensor("h_final", h_final, (batch, D), torch.float32, dev)
+    need = int(lib.ssd_gated_scan_workspace_size(ctypes.byref(dims)))
+    workspace, ws_given = _workspace(need, workspace, dev)
+    with torch.cuda.device(dev):
+        st = lib.ssd_gated_scan(_ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(c), _ptr(reset),
+                                _ptr(h0), _ptr(y), _ptr(h_final), _ptr(states), _ptr(q), _ptr(e),
+                                ctypes.byref(dims), _ptr(workspace), ws_given,
+                                _stream_handle(stream, dev))
+    if st != _lib.SSD_OK:
+        raise SSDError(st, "ssd_gated_scan")
+    return y, h_final
+
+
+def _gated_backward(x, r, i, ckpt, lam, states, dy, dh_final, c, reset, want_dh0, workspace,
+                    stream, where) -> dict:
+    lib = _lib.load()
+    batch, L, D = dy.shape
+    dev, io = dy.device, dy.dtype
+    nb = gated_blocks(L)
+    q = e = None
+    if ckpt is None:
+        for name, t in (("x", x), ("r", r), ("i", i)):
+            _check_tensor(name, t, (batch, L, D), io, dev)
+    else:
+        states, q, e = ckpt.states, ckpt.q, ckpt.e
+        _check_tensor("checkpoint.q", q, (3, batch, L, D), torch.int8, dev)
+        _check_tensor("checkpoint.e", e, (3, batch, nb, D), torch.uint8, dev)
+    _check_tensor("states", states, (batch, nb, D), torch.float32, dev)
+    _check_tensor("dy", dy, (batch, L, D), io, dev)
+    _check_tensor("lam", lam, (D,), torch.float32, dev)
+    _check_reset(reset, batch, L, dev)
+    if dh_final is not None:
+        _check_tensor("dh_final", dh_final, (batch, D), torch.float32, dev)
+    dims = _gated_dims(batch, L, D, io)
+    out = dict(dx=torch.empty_like(dy), dr=torch.empty_like(dy), di=torch.empty_like(dy),
+               dlam=torch.empty_like(lam),
+               dh0=torch.empty((batch, D), dtype=torch.float32, device=dev) if want_dh0 else None)
+    need = int(lib.ssd_gated_scan_backward_workspace_size(ctypes.byref(dims)))
+    workspace, ws_given = _workspace(need, workspace, dev)
+    with torch.cuda.device(dev):
+        st = lib.ssd_gated_scan_backward(_ptr(x), _ptr(r), _ptr(i), _ptr(q), _ptr(e), _ptr(lam),
+                                         float(c), _ptr(reset), _ptr(states), _ptr(dy),
+                                         _ptr(dh_final), _ptr(out["dx"]), _ptr(out["dr"]),
+                                         _ptr(out["di"]), _ptr(out["dlam"]), _ptr(out["dh0"]),
+                                         ctypes.byref(dims), _ptr(workspace), ws_given,
+                                         _stream_handle(stream, dev))
+    if st != _lib.SSD_OK:
+        raise SSDError(st, where)
+    return out
+
+
+def ssd_gated_scan_backward(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor,
+                            states: torch.Tensor, dy: torch.Tensor,
+                            dh_final: Optional[torch.Tensor] = None, c: float = 8.0,
+                            reset: Optional[torch.Tensor] = None, want_dh0: bool = True,
+                            workspace: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of sum dy . y + sum dh_final . h_final for ssd_gated_scan: a
+    dict of dx, dr, di (b,L,D) in the inputs' dtype and dlam (D,), dh0 (b,D)
+    in float32. ``states`` are the forward's; c and reset as given to it."""
+    return _gated_backward(x, r, i, None, lam, states, dy, dh_final, c, reset, want_dh0, workspace,
+                           stream, "ssd_gated_scan_backward")
+
+
+def ssd_gated_scan_backward_ckpt8(checkpoint: GatedCheckpoint8, lam: torch.Tensor,
+                                  dy: torch.Tensor, dh_final: Optional[torch.Tensor] = None,
+                                  c: float = 8.0, reset: Optional[torch.Tensor] = None,
+                                  want_dh0: bool = True,
+                                  workspace: Optional[torch.Tensor] = None,
+                                  stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """ssd_gated_scan_backward from the 8-bit checkpoint that the forward wrote:
+    the gradients of the recurrence on checkpoint.values(), each block entered
+    with its saved state, in dy's dtype."""
+    return _gated_backward(None, None, None, checkpoint, lam, None, dy, dh_final, c, reset,
+                           want_dh0, workspace, stream, "ssd_gated_scan_backward")
+
+
+def ssd_gated_step(h: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.Tensor,
+                   lam: torch.Tensor, c: float = 8.0, y: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One token of the gated recurrence: updates h (b,D) float32 in place,
+    returns y (b,D) in the dtype of x, r, i (b,D)."""
+    lib = _lib.load()
+    batch, D = h.shape
+    dev, io = x.device, x.dtype
+    _check_tensor("h", h, (batch, D), torch.float32, dev)
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        _check_tensor(name, t, (batch, D), io, dev)
+    _check_tensor("lam", lam, (D,), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    _check_tensor("y", y, (batch, D), io, dev)
+    dims = _gated_dims(batch, 1, D, io)
+    with torch.cuda.device(dev):
+        st = lib.ssd_gated_step(_ptr(h), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(c), _ptr(y),
+                                ctypes.byref(dims), _stream_handle(stream, dev))
+    if st != _lib.SSD_OK:
+        raise SSDError(st, "ssd_gated_step")
+    return y
+
+
 def ssd_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                  C: torch.Tensor, D: Optional[torch.Tensor], h0: Optional[torch.Tensor],
                  dy: torch.Tensor, dh_final: Optional[torch.Tensor] = None,
