@@ -309,6 +309,38 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A,
                               ssd_stream stream);
 
 /*
+ * Backward pass of ssd_selective_scan with its step options, for the scalar
+ * loss sum dy . y + sum dh_final . h_final; states are recomputed, not stored
+ * ("精读笔记 #12：Mamba", section 3.3).
+ *
+ *   x, dt, A, B, C, Dskip, h0, opts   the scan's inputs; dt the raw steps
+ *   dy       (batch, seqlen, D)       I/O type
+ *   dh_final (batch, D, dstate) fp32, or NULL for zeros
+ *   dx, ddt (batch, seqlen, D), dA (D, dstate), dB, dC (batch, seqlen,
+ *            ngroups, dstate): fp32, written; dx, ddt, dB and dC may be NULL
+ *            only when seqlen is 0. ddt is the gradient of the RAW step: a
+ *            clamped step passes none, one on a bound does
+ *   dD (D), ddt_bias (D), dh0 (batch, D, dstate): fp32, written, or NULL;
+ *            dh0 may alias dh_final
+ *   workspace, workspace_bytes as for ssd_forward, sized by
+ *            ssd_selective_scan_backward_workspace_size
+ *
+ * Tensors need the alignment of their element type; no output may alias an
+ * input, but for dh0 and dh_final. Sums over tokens, batch and channels are
+ * fp32, in an order that does not change between calls. seqlen 0 gives zeros,
+ * and dh0 = dh_final.
+ */
+size_t ssd_selective_scan_backward_workspace_size(const ssd_dims *dims);
+ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const float *A,
+                                       const void *B, const void *C, const float *Dskip,
+                                       const float *h0, const void *dy, const float *dh_final,
+                                       float *dx, float *ddt, float *dA, float *dB, float *dC,
+                                       float *dD, float *ddt_bias, float *dh0,
+                                       const ssd_dims *dims, const ssd_options *opts,
+                                       void *workspace, size_t workspace_bytes,
+                                       ssd_stream stream);
+
+/*
  * A gated linear recurrence with one state per channel: the diagonal
  * recurrence of the selective scan ("精读笔记 #12：Mamba", section 3.5: the
  * discretised step acts as a gate) with the state expansion removed and the

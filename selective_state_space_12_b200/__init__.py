@@ -11,6 +11,7 @@ from .ssd import (CHUNKS, GatedCheckpoint8, HostForward, PreparedCall, SSDError,
                   ssd_backward, ssd_device_status, ssd_forward, ssd_forward_ex, ssd_forward_state,
                   ssd_forward_workspace_size, ssd_gated_scan, ssd_gated_scan_backward,
                   ssd_gated_scan_backward_ckpt8, ssd_gated_step, ssd_last_error, ssd_selective_scan,
+                  ssd_selective_scan_backward,
                   ssd_set_wait_limit, ssd_state_chain, ssd_step,
                   ssd_step_ex)
 
@@ -20,5 +21,6 @@ __all__ = ["CHUNKS", "GatedCheckpoint8", "HostForward", "PreparedCall", "SSDErro
            "ssd_device_status", "ssd_forward", "ssd_forward_ex", "ssd_forward_state",
            "ssd_forward_workspace_size", "ssd_gated_scan", "ssd_gated_scan_backward",
            "ssd_gated_scan_backward_ckpt8", "ssd_gated_step", "ssd_last_error", "ssd_selective_scan",
+           "ssd_selective_scan_backward",
            "ssd_set_wait_limit", "ssd_state_chain", "sp_forward",
            "ssd_step", "ssd_step_ex"]

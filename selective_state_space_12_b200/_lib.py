@@ -76,6 +76,9 @@ _SIGNATURES = {
                                        ctypes.POINTER(Dims), _VP]),
     "ssd_selective_scan": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                           ctypes.POINTER(Dims), ctypes.POINTER(Options), _VP]),
+    "ssd_selective_scan_backward_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
+    "ssd_selective_scan_backward": (ctypes.c_int, [_VP] * 17 + [
+        ctypes.POINTER(Dims), ctypes.POINTER(Options), _VP, ctypes.c_size_t, _VP]),
     "ssd_gated_scan_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
     "ssd_gated_scan": (ctypes.c_int, [_VP] * 4 + [ctypes.c_float] + [_VP] * 7 +
                        [ctypes.POINTER(Dims), _VP, ctypes.c_size_t, _VP]),

@@ -118,6 +118,14 @@ ssd_status scan_launch(const Problem &pr, const void *x, const void *dt, const f
                        const void *B, const void *C, const float *Dskip, const float *h0,
                        void *y, float *h_final, const DtPre &pre, cudaStream_t st);
 
+// Its backward pass, see scan_backward.cu. dD, ddt_bias and dh0 may be NULL.
+size_t scan_backward_workspace_bytes(const Problem &pr);
+ssd_status scan_backward_launch(const Problem &pr, const void *x, const void *dt, const float *A,
+                                const void *B, const void *C, const float *Dskip, const float *h0,
+                                const void *dy, const float *dh_final, float *dx, float *ddt,
+                                float *dA, float *dB, float *dC, float *dD, float *ddt_bias,
+                                float *dh0, void *ws, const DtPre &pre, cudaStream_t st);
+
 // --- gated linear recurrence (one state per channel; nheads = channels), see gated.cu ---
 struct GatedArgs {
     const void *x = nullptr, *r = nullptr, *i = nullptr;  // or, in the backward pass,

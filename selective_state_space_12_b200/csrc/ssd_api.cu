@@ -480,6 +480,83 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A, con
                        reinterpret_cast<cudaStream_t>(stream));
 }
 
+static ssd_status check_scan_backward_dims(const ssd_dims *dims) {
+    if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    if (dims->reserved != 0) return fail(SSD_ERR_INVALID_ARG, "dims.reserved must be 0");
+    if (dims->dtype != SSD_F32 && dims->dtype != SSD_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "dims.dtype %d is not SSD_F32 or SSD_BF16", dims->dtype);
+    if (dims->batch < 1 || dims->nheads < 1 || dims->ngroups < 1 || dims->seqlen < 0)
+        return fail(SSD_ERR_INVALID_ARG, "sizes must be positive (seqlen >= 0)");
+    if (dims->headdim != 1)
+        return fail(SSD_ERR_INVALID_ARG, "selective scan: headdim must be 1 (one channel per "
+                                         "head), got %lld", (long long)dims->headdim);
+    if (dims->nheads % dims->ngroups != 0)
+        return fail(SSD_ERR_INVALID_ARG, "channels %lld not a multiple of ngroups %lld",
+                    (long long)dims->nheads, (long long)dims->ngroups);
+    if (!scan_supported_dstate(dims->dstate))
+        return fail(SSD_ERR_UNSUPPORTED, "selective scan: dstate %lld: supported 4, 8, 16",
+                    (long long)dims->dstate);
+    // 32-bit grids over (batch, chunks, groups, channel tiles) and over states
+    const double chunks = (double)((dims->seqlen + 63) / 64);
+    const double gch = (double)(dims->nheads / dims->ngroups);
+    if (dims->batch > 65535 || dims->seqlen > (int64_t)1 << 30 ||
+        dims->nheads > (int64_t)1 << 24 ||
+        (double)dims->batch * chunks * (double)dims->ngroups * (gch / 32 + 1) > 2.0e9 ||
+        (double)dims->batch * (double)dims->nheads * (double)dims->dstate > 1.0e11 ||
+        (double)dims->batch * (double)dims->seqlen * (double)dims->ngroups *
+                (double)dims->dstate > 1.0e11)
+        return fail(SSD_ERR_UNSUPPORTED, "selective scan backward: batch above 65535, channels "
+                                         "above 2^24, seqlen above 2^30, or together too large");
+    return SSD_OK;
+}
+
+size_t ssd_selective_scan_backward_workspace_size(const ssd_dims *dims) {
+    if (check_scan_backward_dims(dims) != SSD_OK) return 0;
+    return scan_backward_workspace_bytes(make_problem(dims, 0));
+}
+
+ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const float *A,
+                                       const void *B, const void *C, const float *Dskip,
+                                       const float *h0, const void *dy, const float *dh_final,
+                                       float *dx, float *ddt, float *dA, float *dB, float *dC,
+                                       float *dD, float *ddt_bias, float *dh0,
+                                       const ssd_dims *dims, const ssd_options *opts,
+                                       void *workspace, size_t workspace_bytes_given,
+                                       ssd_stream stream) {
+    ssd_status s = check_scan_backward_dims(dims);
+    if (s != SSD_OK) return s;
+    DtPre pre;
+    if ((s = read_options(opts, &pre)) != SSD_OK) return s;
+    const Problem pr = make_problem(dims, 0);
+    const size_t esz = pr.dtype == SSD_F32 ? 4 : 2;
+    if (!A || !dA) return fail(SSD_ERR_INVALID_ARG, "A and dA are required");
+    if (pr.seqlen > 0 && (!x || !dt || !B || !C || !dy || !dx || !ddt || !dB || !dC))
+        return fail(SSD_ERR_INVALID_ARG, "x, dt, B, C, dy and the gradients dx, ddt, dB, dC must "
+                                         "be non-NULL");
+    const Named io[] = {{x, "x"}, {dt, "dt"}, {B, "B"}, {C, "C"}, {dy, "dy"}};
+    const Named f4[] = {{A, "A"}, {Dskip, "Dskip"}, {h0, "h0"}, {dh_final, "dh_final"},
+                        {dx, "dx"}, {ddt, "ddt"}, {dA, "dA"}, {dB, "dB"}, {dC, "dC"}, {dD, "dD"},
+                        {ddt_bias, "ddt_bias"}, {dh0, "dh0"}};
+    if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
+    const Named outs[] = {{dx, "dx"}, {ddt, "ddt"}, {dA, "dA"}, {dB, "dB"}, {dC, "dC"},
+                          {dD, "dD"}, {ddt_bias, "ddt_bias"}};
+    const Named ins[] = {{x, "x"}, {dt, "dt"}, {A, "A"}, {B, "B"}, {C, "C"}, {Dskip, "Dskip"},
+                         {h0, "h0"}, {dy, "dy"}, {dh_final, "dh_final"},
+                         {pre.bias, "options.dt_bias"}};
+    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    if (dh0 && (dh0 == h0 || dh0 == A))
+        return fail(SSD_ERR_INVALID_ARG, "dh0 aliases an input");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void *ws;
+    bool owned;
+    s = take_workspace(workspace, workspace_bytes_given, scan_backward_workspace_bytes(pr), st,
+                       &ws, &owned);
+    if (s != SSD_OK) return s;
+    s = scan_backward_launch(pr, x, dt, A, B, C, Dskip, h0, dy, dh_final, dx, ddt, dA, dB, dC, dD,
+                             ddt_bias, dh0, ws, pre, st);
+    return give_back(ws, owned, st, s);
+}
+
 size_t ssd_gated_scan_workspace_size(const ssd_dims *dims) {
     if (check_gated_dims(dims, true) != SSD_OK) return 0;
     return gated_workspace_bytes(make_problem(dims, 0), false);

@@ -324,6 +324,55 @@ def ssd_selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     return y, h_final
 
 
+def ssd_selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
+                                B: torch.Tensor, C: torch.Tensor, Dskip: Optional[torch.Tensor],
+                                h0: Optional[torch.Tensor], dy: torch.Tensor,
+                                dh_final: Optional[torch.Tensor] = None,
+                                dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                                dt_limit: Optional[Tuple[float, float]] = None, zoh: bool = False,
+                                want_dh0: bool = True, workspace: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of sum dy . y + sum dh_final . h_final for ssd_selective_scan
+    with its step options: a dict of fp32 tensors dx, ddt (of the raw step),
+    dA, dB, dC, dD, ddt_bias, dh0."""
+    lib = _lib.load()
+    batch, L, Dc = x.shape
+    N = A.shape[1]
+    G = B.shape[2]
+    dev, io = x.device, x.dtype
+    for name, t, shape, dtype in (("x", x, (batch, L, Dc), io), ("dt", dt, (batch, L, Dc), io),
+                                  ("A", A, (Dc, N), torch.float32),
+                                  ("B", B, (batch, L, G, N), io), ("C", C, (batch, L, G, N), io),
+                                  ("dy", dy, (batch, L, Dc), io)):
+        _check_tensor(name, t, shape, dtype, dev)
+    for name, t in (("Dskip", Dskip), ("dt_bias", dt_bias)):
+        if t is not None:
+            _check_tensor(name, t, (Dc,), torch.float32, dev)
+    for name, t in (("h0", h0), ("dh_final", dh_final)):
+        if t is not None:
+            _check_tensor(name, t, (batch, Dc, N), torch.float32, dev)
+    f = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty((batch, L, Dc), **f), ddt=torch.empty((batch, L, Dc), **f),
+               dA=torch.empty((Dc, N), **f), dB=torch.empty((batch, L, G, N), **f),
+               dC=torch.empty((batch, L, G, N), **f), dD=torch.empty((Dc,), **f),
+               ddt_bias=torch.empty((Dc,), **f),
+               dh0=torch.empty((batch, Dc, N), **f) if want_dh0 else None)
+    dims = make_dims(batch, L, Dc, 1, N, G, io)
+    opts = make_options(dt_bias, dt_softplus, dt_limit, zoh)
+    need = int(lib.ssd_selective_scan_backward_workspace_size(ctypes.byref(dims)))
+    workspace, ws_given = _workspace(need, workspace, dev)
+    with torch.cuda.device(dev):
+        st = lib.ssd_selective_scan_backward(
+            _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(h0), _ptr(dy),
+            _ptr(dh_final), *[_ptr(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD",
+                                                     "ddt_bias", "dh0")],
+            ctypes.byref(dims), ctypes.byref(opts), _ptr(workspace), ws_given,
+            _stream_handle(stream, dev))
+    if st != _lib.SSD_OK:
+        raise SSDError(st, "ssd_selective_scan_backward")
+    return out
+
+
 def _gated_dims(batch, L, D, dtype) -> _lib.Dims:
     return make_dims(batch, L, D, 1, 1, 1, dtype)
 

@@ -1,0 +1,290 @@
+"""The selective scan's backward pass on the GPU against the adjoint of its
+definition in 64 bits, token after token.
+
+An output's error is |got - ref| as a share of the larger of the value and the
+rms, held to 2e-4: one decay is within 2^-22.5 (1.7e-7) of its value by the
+hardware's exp2, whose errors may share a sign over the tokens that a state
+remembers, at most about 1000 here (steps of 1e-3, |A| >= 1): 1.7e-4."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TOL = 2e-4
+F32, BF16 = torch.float32, torch.bfloat16
+LIMIT = (2.0 ** -8, 3 * 2.0 ** -6)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from selective_state_space_12_b200 import build
+
+    build.build()
+
+
+def make(b, L, D, N, G=1, dtype=F32, softplus=True, h0=True, seed=0, Dskip=True):
+    g = np.random.default_rng(seed)
+
+    def t(a, dt=F32):
+        return torch.from_numpy(np.asarray(a, dtype=np.float32)).cuda().to(dt)
+
+    step = np.exp(g.uniform(np.log(1e-3), np.log(1e-1), D))
+    s = dict(x=t(g.standard_normal((b, L, D)), dtype), dy=t(g.standard_normal((b, L, D)), dtype),
+             A=t(-np.exp(g.uniform(0, np.log(16), (D, N)))),
+             B=t(g.standard_normal((b, L, G, N)) / np.sqrt(N), dtype),
+             C=t(g.standard_normal((b, L, G, N)) / np.sqrt(N), dtype),
+             Dskip=t(1 + 0.1 * g.standard_normal(D)) if Dskip else None, bias=None, h0=None,
+             dhf=None)
+    if softplus:
+        s["dt"], s["bias"] = t(0.5 * g.standard_normal((b, L, D)), dtype), t(np.log(np.expm1(step)))
+    else:
+        s["dt"] = t(step * np.exp(g.uniform(-0.7, 0.7, (b, L, D))), dtype)
+    if h0:
+        s["h0"], s["dhf"] = t(g.standard_normal((b, D, N))), t(g.standard_normal((b, D, N)))
+    return s
+
+
+def f64(v):
+    return None if v is None else v.detach().double().cpu().numpy()
+
+
+def prepared(s, softplus, limit):
+    pre = f64(s["dt"]) + (0 if s["bias"] is None else f64(s["bias"]))
+    v = np.logaddexp(pre, 0) if softplus else pre
+    slope = 1 / (1 + np.exp(-pre)) if softplus else np.ones_like(pre)
+    if limit is None:
+        return v, slope
+    return np.clip(v, *limit), slope * ((v >= limit[0]) & (v <= limit[1]))
+
+
+def expand(v, D):
+    return np.repeat(v, D // v.shape[1], axis=1)  # (b, G, N) -> (b, D, N)
+
+
+def weight(dt, A, zoh):
+    z = dt[..., None] * A
+    safe = np.where(A == 0, 1, A)
+    return np.exp(z), np.where(A == 0, dt[..., None], np.expm1(z) / safe) if zoh else \
+        np.broadcast_to(dt[..., None], z.shape)
+
+
+def forward(s, softplus=False, limit=None, zoh=False, **change):
+    s = {**s, **change}
+    x, A, B, C = (f64(s[k]) for k in ("x", "A", "B", "C"))
+    b, L, D = x.shape
+    dt, _ = prepared(s, softplus, limit)
+    h = np.zeros((b, D, A.shape[1])) if s["h0"] is None else f64(s["h0"])
+    y = np.zeros((b, L, D))
+    for t in range(L):
+        a, w = weight(dt[:, t], A, zoh)
+        h = a * h + w * x[:, t, :, None] * expand(B[:, t], D)
+        y[:, t] = (h * expand(C[:, t], D)).sum(2)
+    return y + (0 if s["Dskip"] is None else f64(s["Dskip"]) * x), h
+
+
+def reference(s, softplus=False, limit=None, zoh=False):
+    x, A, B, C, dy = (f64(s[k]) for k in ("x", "A", "B", "C", "dy"))
+    b, L, D = x.shape
+    G, N = B.shape[2:]
+    dt, slope = prepared(s, softplus, limit)
+    H = np.zeros((L + 1, b, D, N))
+    if s["h0"] is not None:
+        H[0] = f64(s["h0"])
+    for t in range(L):
+        a, w = weight(dt[:, t], A, zoh)
+        H[t + 1] = a * H[t] + w * x[:, t, :, None] * expand(B[:, t], D)
+    dx, ddt, dB, dC, dA = (np.zeros_like(v) for v in (x, dt, B, C, A))
+    r = np.zeros((b, D, N)) if s["dhf"] is None else f64(s["dhf"])
+    for t in range(L - 1, -1, -1):
+        a, w = weight(dt[:, t], A, zoh)
+        d, xt, Bt = dt[:, t, :, None], x[:, t, :, None], expand(B[:, t], D)
+        r = r + dy[:, t, :, None] * expand(C[:, t], D)
+        dC[:, t] = (dy[:, t, :, None] * H[t + 1]).reshape(b, G, D // G, N).sum(2)
+        dB[:, t] = (r * w * xt).reshape(b, G, D // G, N).sum(2)
+        dx[:, t] = (r * w * Bt).sum(2)
+        ddt[:, t] = (r * (A * a * H[t] + (a if zoh else 1) * xt * Bt)).sum(2)
+        dA += (r * d * a * H[t]).sum(0)
+        if zoh:
+            z = d * A
+            near = 0.5 + z / 3 + z ** 2 / 8 + z ** 3 / 30 + z ** 4 / 144 + z ** 5 / 840
+            with np.errstate(divide="ignore", invalid="ignore"):
+                far = (z * np.exp(z) - np.expm1(z)) / z ** 2
+            dA += (r * xt * Bt * d * d * np.where(np.abs(z) < 0.02, near, far)).sum(0)
+        r = a * r
+    if s["Dskip"] is not None:
+        dx += f64(s["Dskip"]) * dy
+    ddt = ddt * slope
+    return dict(dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=(x * dy).sum((0, 1)),
+                ddt_bias=ddt.sum((0, 1)), dh0=r)
+
+
+def run(s, softplus=False, limit=None, zoh=False, **kw):
+    import selective_state_space_12_b200 as ssd
+
+    g = ssd.ssd_selective_scan_backward(s["x"], s["dt"], s["A"], s["B"], s["C"], s["Dskip"],
+                                        s["h0"], s["dy"], s["dhf"], dt_bias=s["bias"],
+                                        dt_softplus=softplus, dt_limit=limit, zoh=zoh, **kw)
+    assert ssd.ssd_device_status() == 0, ssd.ssd_last_error()
+    return g
+
+
+def off(got, ref):
+    got = f64(got)
+    assert got.shape == ref.shape
+    if not ref.size:
+        return 0.0
+    size = np.maximum(np.abs(ref), max(np.sqrt(np.mean(ref * ref)), 1e-300))
+    return float(np.max(np.abs(got - ref) / size))
+
+
+def check(s, **o):
+    g, ref = run(s, **o), reference(s, **o)
+    far = {k: off(g[k], v) for k, v in ref.items() if np.any(v)}
+    assert all(v <= TOL for v in far.values()), far
+    assert all(not g[k].any() for k, v in ref.items() if not np.any(v))
+
+
+OPTIONS = {"euler": dict(), "euler_softplus": dict(softplus=True), "zoh": dict(zoh=True),
+           "zoh_softplus": dict(softplus=True, zoh=True),
+           "zoh_clamp": dict(softplus=True, zoh=True, limit=LIMIT),
+           "euler_clamp": dict(limit=LIMIT)}
+SHAPES = [(1, 1, 1, 16, 1), (1, 3, 33, 4, 1), (2, 64, 32, 16, 1), (1, 65, 40, 8, 2),
+          (2, 130, 96, 16, 3), (1, 255, 257, 16, 1), (3, 63, 31, 8, 1), (1, 700, 64, 4, 2)]
+
+
+@pytest.mark.parametrize("o", sorted(OPTIONS))
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients_f32(shape, o):
+    check(make(*shape, softplus=OPTIONS[o].get("softplus", False), seed=sum(shape)), **OPTIONS[o])
+
+
+@pytest.mark.parametrize("o", sorted(OPTIONS))
+@pytest.mark.parametrize("shape", [(1, 1, 8, 16, 1), (2, 130, 96, 16, 3), (1, 333, 320, 16, 1),
+                                   (2, 100, 72, 8, 2)])
+def test_gradients_bf16(shape, o):
+    check(make(*shape, dtype=BF16, softplus=OPTIONS[o].get("softplus", False), h0=False,
+               seed=7 + sum(shape)), **OPTIONS[o])
+
+
+def test_bias_without_softplus_and_no_skip():
+    s = make(1, 90, 50, 16, softplus=False, Dskip=False, seed=3)
+    s["bias"] = torch.full((50,), 0.01, device="cuda")
+    check(s)
+    check(s, zoh=True, limit=LIMIT)
+
+
+@pytest.mark.parametrize("zoh", [False, True])
+def test_far_decays(zoh):
+    """A = 0, A > 0, A of -1e-6 and of -1e4 (one token forgets everything)."""
+    s = make(2, 100, 40, 16, softplus=False, seed=11)
+    s["A"][:, 0], s["A"][:, 1], s["A"][:, 2], s["A"][:, 3] = 0.0, 0.1, -1e-6, -1e4
+    check(s, zoh=zoh)
+
+
+def test_a_step_on_a_bound_passes_its_gradient():
+    s = make(1, 70, 32, 16, softplus=False, seed=13)
+    lo, hi = LIMIT
+    s["dt"][0, 10], s["dt"][0, 20] = lo, hi
+    s["dt"][0, 30], s["dt"][0, 40] = lo * (1 - 2.0 ** -23), hi * (1 + 2.0 ** -23)
+    g = run(s, limit=LIMIT)["ddt"]
+    assert g[0, 10].all() and g[0, 20].all() and not g[0, 30].any() and not g[0, 40].any()
+    check(s, limit=LIMIT)
+
+
+def test_against_differences():
+    """Central differences of the 64-bit forward in random directions."""
+    s = make(1, 75, 12, 8, 2, seed=17)
+    o = dict(softplus=True, zoh=True)
+    g = run(s, **o)
+    rng = np.random.default_rng(18)
+    dy, dhf = f64(s["dy"]), f64(s["dhf"])
+
+    def loss(**change):
+        y, h = forward(s, **o, **change)
+        return float((dy * y).sum() + (dhf * h).sum())
+
+    for k, grad in (("x", "dx"), ("dt", "ddt"), ("A", "dA"), ("B", "dB"), ("C", "dC"),
+                    ("Dskip", "dD"), ("bias", "ddt_bias"), ("h0", "dh0")):
+        base = s[k].double().cpu()
+        v = torch.from_numpy(rng.standard_normal(tuple(base.shape)))
+        eps = 1e-5
+        num = (loss(**{k: base + eps * v}) - loss(**{k: base - eps * v})) / (2 * eps)
+        got = g[grad].double().cpu()
+        # central differences leave about eps^2 of the third derivative
+        assert abs(float((got * v).sum()) - num) <= TOL * float(got.norm() * v.norm()), k
+
+
+def test_gradient_of_the_librarys_forward():
+    """A run of both: the forward's outputs move as its backward pass says."""
+    import selective_state_space_12_b200 as ssd
+
+    s = make(2, 200, 64, 16, seed=19)
+    kw = dict(dt_bias=s["bias"], dt_softplus=True, zoh=True)
+    y, hf = ssd.ssd_selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], s["Dskip"], s["h0"],
+                                   **kw)
+    g = run(s, softplus=True, zoh=True)
+    v = torch.randn_like(s["x"])
+    y2, hf2 = ssd.ssd_selective_scan(s["x"] + 0.5 * v, s["dt"], s["A"], s["B"], s["C"],
+                                     s["Dskip"], s["h0"], **kw)
+    # linear in x: exact but for rounding, 1e-4 of the forward's rms bound
+    num = float((s["dy"].double() * (y2.double() - y.double())).sum()
+                + (s["dhf"].double() * (hf2.double() - hf.double())).sum())
+    got = 0.5 * float((g["dx"].double() * v.double()).sum())
+    scale = float(s["dy"].norm() * y.norm()) * 1e-4
+    assert abs(num - got) <= scale
+
+
+def test_empty_sequence():
+    import selective_state_space_12_b200 as ssd
+
+    s = make(2, 0, 24, 16, seed=23)
+    g = run(s, softplus=True)
+    assert torch.equal(g["dh0"], s["dhf"]) and g["dx"].shape == (2, 0, 24)
+    assert not any(g[k].any() for k in ("dA", "dD", "ddt_bias"))
+    s["dhf"] = None
+    assert not run(s)["dh0"].any()
+    assert ssd.ssd_selective_scan_backward(
+        s["x"], s["dt"], s["A"], s["B"], s["C"], None, None, s["dy"], want_dh0=False)["dh0"] is None
+
+
+def test_unaligned_inputs_another_stream_graph_and_bits():
+    import selective_state_space_12_b200 as ssd
+
+    s = make(2, 300, 100, 16, dtype=BF16, seed=29)
+    o = dict(softplus=True, zoh=True)
+    want = run(s, **o)
+    for k in ("x", "dt", "B", "C", "dy"):
+        buf = torch.empty(s[k].numel() + 1, dtype=BF16, device="cuda")[1:].view(s[k].shape)
+        s[k] = buf.copy_(s[k])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = run(s, **o, stream=side)
+    side.synchronize()
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    keep = {k: s[k].clone() for k in ("x", "dt", "dy")}
+    for k in keep:
+        s[k].zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ssd.ssd_selective_scan_backward(
+            s["x"], s["dt"], s["A"], s["B"], s["C"], s["Dskip"], s["h0"], s["dy"], s["dhf"],
+            dt_bias=s["bias"], dt_softplus=True, zoh=True)
+    for _ in range(2):
+        for k in keep:
+            s[k].copy_(keep[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(out[k], want[k]), k
+        for k in keep:
+            s[k].zero_()
+        graph.replay()
+
+
+def test_many_blocks_of_channels():
+    """Wide enough that a CUDA block walks several tiles of channels."""
+    check(make(2, 200, 5120, 16, dtype=BF16, h0=False, seed=31), softplus=True, zoh=True)
