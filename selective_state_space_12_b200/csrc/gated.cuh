@@ -77,31 +77,94 @@ __device__ __forceinline__ float expm1_neg(float s) {
 }
 
 // A reset's decay is written -0: it passes nothing on, whatever stands before
-// it (an infinity or a NaN times 0 would). Products of decays keep the mark,
-// as decays are >= +0.
+// it (an infinity or a NaN times 0 would). Products of decays from a reset on
+// keep the mark, as decays are >= +0.
 constexpr uint32_t kResetBits = 0x80000000u;
 __device__ __forceinline__ float reset_decay() { return __uint_as_float(kResetBits); }
 __device__ __forceinline__ float carry_on(float a, float h, float u) {  // a h + u
     return __float_as_uint(a) == kResetBits ? u : fmaf(a, h, u);
 }
 
-struct Gate {
-    float sr, si;  // sigmoids
-    float s;       // log a
-    float a, m2;   // decay and m^2
-    float rm;      // 1 / m (large where m = 0, with m2 * rm = 0 there)
-    __device__ __forceinline__ float m() const { return m2 * rm; }
-};
+__device__ __forceinline__ float chain_decay(float first, float next) {
+    return __float_as_uint(next) == kResetBits ? next : first * next;
+}
 
-template <bool FAST>
+// One token's gate values (the step kernel).
+struct Gate {
+    float a, m, si;
+};
 __device__ __forceinline__ Gate gate(float r, float i, float k) {
     Gate g;
-    two_sigmoids(r, i, g.sr, g.si);
-    g.s = k * g.sr;
-    const float E = expm1_neg<FAST>(g.s);
+    float sr;
+    two_sigmoids(r, i, sr, g.si);
+    const float E = expm1_neg<false>(k * sr);
     g.a = 1.f + E;
-    g.m2 = -E * (2.f + E);
-    g.rm = rsqrt_approx(g.m2 < 1e-36f ? 1e-36f : g.m2);
+    const float m2 = -E * (2.f + E);
+    g.m = m2 * rsqrt_approx(m2 < 1e-36f ? 1e-36f : m2);
+    return g;
+}
+
+// The same for two channels at once in packed fp32 (half the instructions).
+using tc::f2;
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_mul;
+using tc::f2_pack;
+using tc::f2_unpack;
+
+__device__ __forceinline__ f2 f2_both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ f2 f2_neg(f2 v) { return v ^ 0x8000000080000000ull; }
+
+struct Gate2 {
+    f2 sr, si;  // sigmoids
+    f2 a;       // decay
+    f2 m, rm;   // sqrt(1 - a^2) and its reciprocal (large where m = 0)
+};
+
+__device__ __forceinline__ f2 exp2_gate2(f2 v) {  // exp2(min(-v log2 e, 63))
+    float lo, hi;
+    f2_unpack(f2_mul(v, f2_both(-kLog2e)), lo, hi);
+    return f2_pack(tc::fast_exp2(min_nan(lo, 63.f)), tc::fast_exp2(min_nan(hi, 63.f)));
+}
+__device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si) {
+    const f2 one = f2_both(1.f);
+    const f2 p = f2_add(one, exp2_gate2(r)), q = f2_add(one, exp2_gate2(i));
+    float lo, hi;
+    f2_unpack(f2_mul(p, q), lo, hi);
+    const f2 R = f2_pack(rcp_approx(lo), rcp_approx(hi));
+    sr = f2_mul(q, R);
+    si = f2_mul(p, R);
+}
+template <bool FAST>
+__device__ __forceinline__ f2 expm1_neg2(f2 s) {
+    f2 p = f2_both(1.f / 720.f);
+    p = f2_fma(p, s, f2_both(1.f / 120.f));
+    p = f2_fma(p, s, f2_both(1.f / 24.f));
+    p = f2_fma(p, s, f2_both(1.f / 6.f));
+    p = f2_fma(p, s, f2_both(0.5f));
+    p = f2_fma(p, s, f2_both(1.f));
+    const f2 series = f2_mul(s, p);
+    if (FAST) return series;
+    float e0, e1, s0, s1;
+    f2_unpack(series, e0, e1);
+    f2_unpack(s, s0, s1);
+    return f2_pack(s0 >= kSeries ? e0 : tc::fast_exp2(s0 * kLog2e) - 1.f,
+                   s1 >= kSeries ? e1 : tc::fast_exp2(s1 * kLog2e) - 1.f);
+}
+// a, m and 1 / m from E = a - 1.
+__device__ __forceinline__ void decay_from2(f2 E, Gate2 &g) {
+    g.a = f2_add(f2_both(1.f), E);
+    const f2 m2 = f2_mul(f2_neg(E), f2_add(f2_both(2.f), E));
+    float lo, hi;
+    f2_unpack(m2, lo, hi);
+    g.rm = f2_pack(rsqrt_approx(lo < 1e-36f ? 1e-36f : lo), rsqrt_approx(hi < 1e-36f ? 1e-36f : hi));
+    g.m = f2_mul(m2, g.rm);
+}
+template <bool FAST>
+__device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
+    Gate2 g;
+    two_sigmoids2(r, i, g.sr, g.si);
+    decay_from2(expm1_neg2<FAST>(f2_mul(k, g.sr)), g);
     return g;
 }
 

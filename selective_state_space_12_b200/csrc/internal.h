@@ -139,10 +139,13 @@ struct GatedArgs {
     const void *dy = nullptr;
     void *dx = nullptr, *dr = nullptr, *di = nullptr;
     // set by the launchers
-    int64_t batch = 0, L = 0, D = 0, nb = 0, dblocks = 0;
-    float2 *sums = nullptr;      // (b, nb, D): each block's map
-    float *grads = nullptr;      // (b, nb, D): the gradient entering each block from its right
-    float *dlam_part = nullptr;  // (b, nb, D)
+    int64_t batch = 0, L = 0, D = 0, nb = 0, dblocks = 0;  // nb blocks of tokens, tiles of channels
+    const float *first = nullptr;  // h0, or dh_final
+    float *last = nullptr;         // h_final, or dh0
+    float *dlam_part = nullptr;    // (b, nb, D)
+    unsigned *counter = nullptr, *abort = nullptr, *err = nullptr;
+    unsigned long long *ends = nullptr, *maps = nullptr;  // what tiles publish
+    long long wait = 0;
 };
 int64_t gated_blocks(const Problem &pr);
 size_t gated_workspace_bytes(const Problem &pr, bool back);
