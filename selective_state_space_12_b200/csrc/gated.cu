@@ -41,7 +41,7 @@ constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;    // and the one that folds and looks back
 constexpr int kRun = kBlock / kWarps;  // tokens of a warp
 constexpr int kTileCh = 64;            // channels of a tile, two a lane
-constexpr int kWindow = 8;             // tiles that a look reaches back
+constexpr int kWindow = 4;             // tiles that a look reaches back
 
 // Barriers of the compute warps and the chain warp.
 enum { kMapsReady = 1, kEntryReady = 2 };
@@ -95,16 +95,17 @@ __device__ __forceinline__ Tile tile_of(const GatedArgs &a, unsigned ticket) {
 
 // ------------------------------------------------------------ two channels
 
-// A lane's two channels: adjacent with VEC (one load; D even, aligned), else
-// 32 apart (two loads that neighbouring lanes continue).
-template <bool VEC>
+// A lane's two channels: adjacent where rows are 16-byte aligned (ALIGNED: one
+// load of shared memory, one store of global memory), else 32 apart (two, which
+// neighbouring lanes continue).
+template <bool ALIGNED>
 __device__ __forceinline__ int channel(int j) {
     const int lane = threadIdx.x & 31;
-    return VEC ? 2 * lane + j : lane + 32 * j;
+    return ALIGNED ? 2 * lane + j : lane + 32 * j;
 }
 
 template <typename T>
-struct Pair;  // storage of two adjacent elements
+struct Pair;  // two elements as stored
 template <>
 struct Pair<float> {
     using type = float2;
@@ -117,79 +118,126 @@ __device__ __forceinline__ f2 widen(float2 v) { return f2_pack(v.x, v.y); }
 __device__ __forceinline__ f2 widen(uint32_t v) {
     return f2_pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
+__device__ __forceinline__ f2 widen(char2 v) { return f2_pack((float)v.x, (float)v.y); }
 
-template <typename T>
-__device__ __forceinline__ typename Pair<T>::type raw_pair(const void *p, int64_t row,
-                                                           const GatedArgs &a, int d0) {
-    const T *v = static_cast<const T *>(p) + row;
-    const int c0 = d0 + channel<false>(0), c1 = d0 + channel<false>(1);
-    const T lo = c0 < a.D ? v[c0] : from_f<T>(0.f), hi = c1 < a.D ? v[c1] : from_f<T>(0.f);
-    if constexpr (sizeof(T) == 4)
-        return make_float2(lo, hi);
-    else
-        return (uint32_t)__bfloat16_as_ushort(lo) | (uint32_t)__bfloat16_as_ushort(hi) << 16;
-}
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_pair(void *p, int64_t row, const GatedArgs &a, int d0,
-                                           f2 val) {
-    T *v = static_cast<T *>(p) + row;
-    float lo, hi;
-    f2_unpack(val, lo, hi);
-    const int c0 = d0 + channel<VEC>(0), c1 = d0 + channel<VEC>(1);
-    if constexpr (VEC) {
-        if (c0 >= a.D) return;
-        if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float2 *>(v + c0) = make_float2(lo, hi);
-        else
-            *reinterpret_cast<uint32_t *>(v + c0) = tc::pack_bf16(lo, hi);
-    } else {
-        if (c0 < a.D) v[c0] = from_f<T>(lo);
-        if (c1 < a.D) v[c1] = from_f<T>(hi);
+// An output's rows for this lane: stores its two channels of one token.
+template <typename T, bool ALIGNED>
+struct Rows {
+    T *p;
+    bool has0, has1;
+    __device__ __forceinline__ Rows(void *base, int64_t row, int d0, int64_t D)
+        : p(static_cast<T *>(base) + row + d0 + channel<ALIGNED>(0)),
+          has0(d0 + channel<ALIGNED>(0) < D),
+          has1(d0 + channel<ALIGNED>(1) < D) {}
+    __device__ __forceinline__ void put(int64_t off, f2 val) const {
+        float lo, hi;
+        f2_unpack(val, lo, hi);
+        if constexpr (ALIGNED) {
+            if (!has0) return;
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float2 *>(p + off) = make_float2(lo, hi);
+            else
+                *reinterpret_cast<uint32_t *>(p + off) = tc::pack_bf16(lo, hi);
+        } else {
+            if (has0) p[off] = from_f<T>(lo);
+            if (has1) p[off + 32] = from_f<T>(hi);
+        }
     }
-}
+};
 
 // ------------------------------------------------------------ staged inputs
 
-// With VEC, each thread copies the pairs it will read itself, a tile ahead
-// and asynchronously, to its own words of shared memory: no registers and no
-// barriers are spent on them.
-template <typename T, bool VEC, int TENSORS>
+// Each warp brings its own eight tokens' rows of every input tensor to shared
+// memory a tile ahead, by one bulk copy a row (a lane each), counted by a
+// barrier of its own: no registers, no address arithmetic in the loop, and no
+// waiting for other warps. A copy starts and ends on 16 bytes: where rows do
+// not, it takes the 16-byte windows that cover the row (at most 16 bytes more),
+// and the lanes read from the row's place in it; a window that would leave the
+// tensor (its first and last rows only) is replaced by plain loads.
+template <typename T, bool ALIGNED, int TENSORS>
 struct Stage {
     using P = typename Pair<T>::type;
-    static constexpr size_t kBytes = VEC ? sizeof(P) * TENSORS * kRun * kCompute : 16;
+    static constexpr int kPitch = kTileCh * (int)sizeof(T) + 16;
+    static constexpr int kWarpBytes = TENSORS * kRun * kPitch;
+    static constexpr size_t kBytes = (size_t)kWarps * kWarpBytes;
 
-    static __device__ __forceinline__ P *own(unsigned char *s, int w, int t) {
-        return reinterpret_cast<P *>(s) + (w * kRun + t) * kCompute + threadIdx.x;
-    }
-    static __device__ __forceinline__ void request(unsigned char *s, const GatedArgs &a,
-                                                   const Tile &t, const void *const (&src)[TENSORS]) {
-        if constexpr (VEC) {
-            const int tok0 = (threadIdx.x >> 5) * kRun, c = t.d0 + channel<true>(0);
+    unsigned char *buf;  // this warp's rows
+    uint64_t *bar;
+    uint32_t parity;
+
+    __device__ __forceinline__ Stage(unsigned char *all, uint64_t *bars)
+        : buf(all + (threadIdx.x >> 5) * kWarpBytes), bar(bars + (threadIdx.x >> 5)), parity(0) {}
+
+    __device__ __forceinline__ void request(const GatedArgs &a, const Tile &t,
+                                            const void *const (&src)[TENSORS]) const {
+        const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
+        const int w = lane / kRun, j = lane % kRun;
+        const int64_t left = a.D - t.d0;
+        const int len = (int)(left < kTileCh ? left : kTileCh) * (int)sizeof(T);
+        const char *base = nullptr, *row = nullptr, *from = nullptr;
+        uint32_t bytes = 0;
+        bool plain = false;
+        if (w < TENSORS && tok0 + j < t.n) {
 #pragma unroll
-            for (int w = 0; w < TENSORS; ++w)
-#pragma unroll
-                for (int j = 0; j < kRun; ++j) {
-                    const bool ok = tok0 + j < t.n && c < a.D;
-                    const T *from = static_cast<const T *>(src[w]) +
-                                    (ok ? t.row0 + (tok0 + j) * a.D + c : 0);
-                    const uint32_t to = (uint32_t)__cvta_generic_to_shared(own(s, w, j));
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from),
-                                 "n"((int)sizeof(P)), "r"(ok ? (int)sizeof(P) : 0)
-                                 : "memory");
-                }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            for (int k = 0; k < TENSORS; ++k)
+                if (k == w) base = static_cast<const char *>(src[k]);
+            row = base + (t.row0 + (tok0 + j) * a.D + t.d0) * (int64_t)sizeof(T);
+            from = row;
+            bytes = (uint32_t)len;
+            if constexpr (!ALIGNED) {
+                const uintptr_t lo = reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15);
+                const uintptr_t hi = (reinterpret_cast<uintptr_t>(row) + len + 15) & ~uintptr_t(15);
+                const uintptr_t end = reinterpret_cast<uintptr_t>(base) +
+                                      (uintptr_t)(a.batch * a.L * a.D) * sizeof(T);
+                plain = lo < reinterpret_cast<uintptr_t>(base) || hi > end;
+                from = reinterpret_cast<const char *>(lo);
+                bytes = plain ? 0u : (uint32_t)(hi - lo);
+            }
         }
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        unsigned char *to = buf + lane * kPitch;
+        if constexpr (!ALIGNED) {
+            if (plain) {
+                T *dst = reinterpret_cast<T *>(to + (row - from));
+                for (int c = 0; c < len / (int)sizeof(T); ++c)
+                    dst[c] = reinterpret_cast<const T *>(row)[c];
+            }
+        }
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, total);
+        __syncwarp();
+        if (bytes > 0)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+                "[%3];" ::"r"(tc::smem_u32(to)),
+                "l"(from), "r"(bytes), "r"(tc::smem_u32(bar))
+                : "memory");
     }
-    static __device__ __forceinline__ void wait() {
-        if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // False when the wait ran out.
+    __device__ __forceinline__ bool wait(long long limit) {
+        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
+        if (ok) parity ^= 1;
+        return ok;
     }
-    static __device__ __forceinline__ P raw(unsigned char *s, const GatedArgs &a, const Tile &t,
-                                            const void *src, int w, int j) {
-        if constexpr (VEC) {
-            return *own(s, w, j);
+    // Where in its window token 0's row of a tensor lies, and how far on the next.
+    static __device__ __forceinline__ uint32_t place(const GatedArgs &a, const Tile &t,
+                                                     const void *src) {
+        if (ALIGNED) return 0;
+        return (uint32_t)reinterpret_cast<uintptr_t>(
+            static_cast<const char *>(src) +
+            (t.row0 + (int64_t)((threadIdx.x >> 5) * kRun) * a.D + t.d0) * (int64_t)sizeof(T));
+    }
+    __device__ __forceinline__ P get(int w, int j, uint32_t place0, uint32_t rowbytes) const {
+        const unsigned char *row = buf + (w * kRun + j) * kPitch;
+        if constexpr (ALIGNED) {
+            return reinterpret_cast<const P *>(row)[threadIdx.x & 31];
         } else {
-            const int tok = (threadIdx.x >> 5) * kRun + j;
-            return tok < t.n ? raw_pair<T>(src, t.row0 + tok * a.D, a, t.d0) : P{};
+            const T *v = reinterpret_cast<const T *>(row + ((place0 + j * rowbytes) & 15u)) +
+                         (threadIdx.x & 31);
+            if constexpr (sizeof(T) == 4)
+                return make_float2(v[0], v[32]);
+            else
+                return (uint32_t)__bfloat16_as_ushort(v[0]) |
+                       (uint32_t)__bfloat16_as_ushort(v[32]) << 16;
         }
     }
 };
@@ -277,14 +325,14 @@ __device__ __forceinline__ bool look_back(const GatedArgs &a, int64_t id, unsign
     }
 }
 
-template <bool VEC>
+template <bool ALIGNED>
 __device__ __forceinline__ f2 read_state(const float *p, int64_t row, int d0, int64_t D) {
-    const int c0 = d0 + channel<VEC>(0), c1 = d0 + channel<VEC>(1);
+    const int c0 = d0 + channel<ALIGNED>(0), c1 = d0 + channel<ALIGNED>(1);
     return f2_pack(p && c0 < D ? p[row + c0] : 0.f, p && c1 < D ? p[row + c1] : 0.f);
 }
-template <bool VEC>
+template <bool ALIGNED>
 __device__ __forceinline__ void write_state(float *p, int64_t row, int d0, int64_t D, f2 v) {
-    const int c0 = d0 + channel<VEC>(0), c1 = d0 + channel<VEC>(1);
+    const int c0 = d0 + channel<ALIGNED>(0), c1 = d0 + channel<ALIGNED>(1);
     float lo, hi;
     f2_unpack(v, lo, hi);
     if (c0 < D) p[row + c0] = lo;
@@ -300,16 +348,25 @@ struct Shared {
     float dlam[2][kWarps][kTileCh];
     unsigned top[2][3][kTileCh];  // 8-bit copies: largest magnitudes
     unsigned code[3][kTileCh];
+    uint64_t bars[kWarps];
     unsigned ticket[2];        // of this and the next tile
-    int stop;
+    int stop[2];
 };
 
-template <bool VEC>
+template <bool ALIGNED>
 __device__ __forceinline__ void gate_scales(const GatedArgs &a, int d0, float *k) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int c = channel<VEC>(j);
-        k[c] = d0 + c < a.D ? -a.c * softplus_full(a.lam[d0 + c]) : 0.f;
+        const int c = channel<ALIGNED>(j);
+        k[c] = d0 + c < a.D ? a.scale[d0 + c] : 0.f;
+    }
+}
+// A wait of a compute warp ran out.
+__device__ __forceinline__ void give_up(const GatedArgs &a, int *stop) {
+    if ((threadIdx.x & 31) == 0) {
+        atomicExch(a.err, 0x6a7ed002u);
+        if (a.abort) atomicExch(a.abort, 1u);
+        *stop = 1;
     }
 }
 __device__ __forceinline__ bool all_fast(f2 k) {
@@ -338,7 +395,7 @@ __device__ __forceinline__ int8_t in_steps(float v, uint32_t code) {
 // finds what enters it, hands every run what enters that, and publishes what
 // leaves. While the others compute a tile it fetches the next ticket and
 // prepares the next tile's gate scales.
-template <bool VEC, bool CK, bool BACK>
+template <bool ALIGNED, bool CK, bool BACK>
 __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsigned tiles,
                                            int64_t lanes) {
     const int lane = threadIdx.x & 31;
@@ -349,7 +406,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
     auto flush = [&](int slot) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int c = channel<VEC>(j);
+            const int c = channel<ALIGNED>(j);
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sum += s.dlam[slot][w][c];
@@ -362,15 +419,19 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         unsigned after = tiles;
         if (next < tiles) {
             if (lane == 0) after = atomicAdd(a.counter, 1u);
-            gate_scales<VEC>(a, tile_of<BACK>(a, next).d0, s.k[(n + 1) & 1]);
+            gate_scales<ALIGNED>(a, tile_of<BACK>(a, next).d0, s.k[(n + 1) & 1]);
             after = __shfl_sync(0xffffffffu, after, 0);
         }
         f2 in = 0, h = 0;
         word before = kEmpty;
-        if (step == 0) in = read_state<VEC>(a.first, t.b * a.D, t.d0, a.D);
+        if (step == 0) in = read_state<ALIGNED>(a.first, t.b * a.D, t.d0, a.D);
         else before = load_word(&a.ends[(t.id - lanes) * 32 + lane]);
-        if (BACK) h = read_state<VEC>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D);
+        if (BACK) h = read_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D);
         bar_sync(kMapsReady);
+        if (s.stop[n & 1]) {
+            bar_arrive(kEntryReady);
+            return;
+        }
         if (BACK && last_row >= 0) flush((n + 1) & 1);
         float4 m[kWarps];
 #pragma unroll
@@ -388,7 +449,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = then(all, m[BACK ? kWarps - 1 - w : w]);
         if (step > 0 && !look_back(a, t.id, step, lanes, all, before, in)) {
-            if (lane == 0) s.stop = 1;
+            if (lane == 0) s.stop[n & 1] = 1;
             __syncwarp();
             bar_arrive(kEntryReady);
             return;
@@ -411,7 +472,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
             for (int w = 0; w < 3; ++w)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const int c = channel<VEC>(j);
+                    const int c = channel<ALIGNED>(j);
                     const uint32_t code = step_code(s.top[n & 1][w][c]);
                     s.code[w][c] = code;
                     s.top[n & 1][w][c] = 0;
@@ -423,8 +484,8 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         __syncwarp();
         bar_arrive(kEntryReady);
         if (!BACK && a.states)
-            write_state<VEC>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D, in);
-        if (a.last && step + 1 == a.nb) write_state<VEC>(a.last, t.b * a.D, t.d0, a.D, out);
+            write_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D, in);
+        if (a.last && step + 1 == a.nb) write_state<ALIGNED>(a.last, t.b * a.D, t.d0, a.D, out);
         last_row = (t.b * a.nb + t.blk) * a.D;
         last_d0 = t.d0;
         now = next;
@@ -436,11 +497,11 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
     }
 }
 
-// The first two tickets of this thread block, and its first gate scales.
-template <bool VEC, bool BACK>
+// The first two tickets of this thread block, its barriers and first gate scales.
+template <bool ALIGNED, bool BACK>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
     if (threadIdx.x == 0) {
-        s.stop = 0;
+        s.stop[0] = s.stop[1] = 0;
         if (a.nb > 1) {
             s.ticket[0] = atomicAdd(a.counter, 1u);
             s.ticket[1] = atomicAdd(a.counter, 1u);
@@ -448,68 +509,84 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
             s.ticket[0] = blockIdx.x;
             s.ticket[1] = tiles;
         }
+        for (int w = 0; w < kWarps; ++w) tc::mbar_init(&s.bars[w], 1);
+        tc::fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 2 * 3 * kTileCh; i += kThreads) (&s.top[0][0][0])[i] = 0;
     __syncthreads();
     if (threadIdx.x >= kCompute && s.ticket[0] < tiles)
-        gate_scales<VEC>(a, tile_of<BACK>(a, s.ticket[0]).d0, s.k[0]);
+        gate_scales<ALIGNED>(a, tile_of<BACK>(a, s.ticket[0]).d0, s.k[0]);
     __syncthreads();
 }
 
+// The plain case of a warp's eight tokens (all there, no reset, slow decays) is
+// straight code; every other case runs a general copy with a branch a token.
+struct PlainRun : std::true_type {};
+struct AnyRun : std::false_type {};
+
 // ------------------------------------------------------------ forward
 
-template <typename T, bool VEC, bool CK>
+template <typename T, bool ALIGNED, bool CK>
 __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(const GatedArgs a) {
-    extern __shared__ __align__(16) unsigned char staged[];
+    extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
-    using In = Stage<T, VEC, 3>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<VEC, false>(a, s, tiles);
+    open_block<ALIGNED, false>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<VEC, CK, false>(a, s, tiles, lanes);
+        chain_warp<ALIGNED, CK, false>(a, s, tiles, lanes);
         return;
     }
+    Stage<T, ALIGNED, 3> in(staged, s.bars);
     const void *const src[3] = {a.x, a.r, a.i};
-    unsigned now = s.ticket[0], next = s.ticket[1];
-    if (now >= tiles) return;
-    Tile t = tile_of<false>(a, now);
-    In::request(staged, a, t, src);
+    const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
+    unsigned next = s.ticket[1];
+    if (s.ticket[0] >= tiles) return;
+    Tile t = tile_of<false>(a, s.ticket[0]);
+    in.request(a, t, src);
     unsigned mark = reset_byte(a, t);
     const int tok0 = warp * kRun;
+    bool ahead = false;  // copies are on their way
     for (int n = 0;; ++n) {
-        const f2 k = f2_pack(s.k[n & 1][channel<VEC>(0)], s.k[n & 1][channel<VEC>(1)]);
-        const bool fast = all_fast(k);
+        const f2 k = f2_pack(s.k[n & 1][channel<ALIGNED>(0)], s.k[n & 1][channel<ALIGNED>(1)]);
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
-        In::wait();
+        const bool plain = all_fast(k) && marks == 0 && left >= kRun;
+        uint32_t at[3];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) at[w] = in.place(a, t, src[w]);
+        const bool here = in.wait(a.wait);
+        if (!here) give_up(a, &s.stop[n & 1]);
         typename Pair<T>::type v[3][kRun];
         f2 av[kRun], u[kRun];
         f2 P = f2_both(1.f), H = f2_both(0.f);
-        auto gates = [&](auto is_fast) {
+        auto gates = [&](auto run) {
+            constexpr bool kPlain = decltype(run)::value;
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
 #pragma unroll
-                for (int w = 0; w < 3; ++w) v[w][j] = In::raw(staged, a, t, src[w], w, j);
-                const Gate2 g = gate2<decltype(is_fast)::value>(widen(v[1][j]), widen(v[2][j]), k);
+                for (int w = 0; w < 3; ++w) v[w][j] = in.get(w, j, at[w], rowbytes);
+                const Gate2 g = gate2<kPlain>(widen(v[1][j]), widen(v[2][j]), k);
                 const f2 ix = f2_mul(g.si, widen(v[0][j]));
-                if (marks >> j & 1) {
-                    av[j] = P = f2_both(reset_decay());
-                    H = u[j] = ix;
-                } else if (j < left) {
+                if (kPlain || (j < left && !(marks >> j & 1))) {
                     av[j] = g.a;
                     u[j] = f2_mul(g.m, ix);
-                    H = f2_fma(g.a, H, u[j]);
-                    P = f2_mul(P, g.a);
+                    H = j == 0 ? u[j] : f2_fma(g.a, H, u[j]);
+                    P = j == 0 ? g.a : f2_mul(P, g.a);
+                } else if (j < left) {
+                    av[j] = P = f2_both(reset_decay());
+                    H = u[j] = ix;
                 } else {
                     av[j] = f2_both(1.f);
                     u[j] = f2_both(0.f);
+#pragma unroll
+                    for (int w = 0; w < 3; ++w) v[w][j] = {};
                 }
             }
         };
-        if (fast) gates(std::true_type{});
-        else gates(std::false_type{});
+        if (plain) gates(PlainRun());
+        else gates(AnyRun());
         if (CK) {
 #pragma unroll
             for (int w = 0; w < 3; ++w) {
@@ -520,92 +597,104 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(con
                     m0 = max(m0, (uint32_t)f & 0x7fffffffu);
                     m1 = max(m1, (uint32_t)(f >> 32) & 0x7fffffffu);
                 }
-                atomicMax(&s.top[n & 1][w][channel<VEC>(0)], m0);
-                atomicMax(&s.top[n & 1][w][channel<VEC>(1)], m1);
+                atomicMax(&s.top[n & 1][w][channel<ALIGNED>(0)], m0);
+                atomicMax(&s.top[n & 1][w][channel<ALIGNED>(1)], m1);
             }
         }
         s.maps[warp][lane] = as_map(P, H);
         bar_arrive(kMapsReady);
         Tile tn = t;
-        if (next < tiles) {  // the next tile's inputs are on their way while this one waits
+        ahead = here && next < tiles;
+        if (ahead) {  // the next tile's inputs are on their way while this one waits
             tn = tile_of<false>(a, next);
-            In::request(staged, a, tn, src);
+            in.request(a, tn, src);
             mark = reset_byte(a, tn);
         }
         bar_sync(kEntryReady);
-        if (s.stop) break;
+        if (s.stop[n & 1]) {
+            if (!here) in.wait(a.wait);
+            break;
+        }
         const unsigned after = s.ticket[n & 1];
         f2 h = s.entry[warp][lane];
+        const Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
+        if (plain) {
+            int64_t off = 0;
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) {
-            h = (marks >> j & 1) ? u[j] : f2_fma(av[j], h, u[j]);
-            if (j < left) store_pair<T, VEC>(a.y, t.row0 + (tok0 + j) * a.D, a, t.d0, h);
+            for (int j = 0; j < kRun; ++j, off += a.D) {
+                h = f2_fma(av[j], h, u[j]);
+                y.put(off, h);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                h = (marks >> j & 1) ? u[j] : f2_fma(av[j], h, u[j]);
+                if (j < left) y.put(j * a.D, h);
+            }
         }
         if (CK) {
 #pragma unroll
             for (int w = 0; w < 3; ++w) {
-                const int c0 = channel<VEC>(0), c1 = channel<VEC>(1);
+                const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
                 const uint32_t k0 = s.code[w][c0], k1 = s.code[w][c1];
-                int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + t.d0;
+                int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok0 * a.D + t.d0;
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) {
+                for (int j = 0; j < kRun; ++j, q += a.D) {
+                    if (j >= left) break;
                     float lo, hi;
                     f2_unpack(widen(v[w][j]), lo, hi);
                     const int8_t q0 = in_steps(lo, k0), q1 = in_steps(hi, k1);
-                    int8_t *to = q + (tok0 + j) * a.D;
-                    if (j >= left) continue;
-                    if (VEC && t.d0 + c0 < a.D) {
-                        *reinterpret_cast<char2 *>(to + c0) = make_char2(q0, q1);
-                    } else if (!VEC) {
-                        if (t.d0 + c0 < a.D) to[c0] = q0;
-                        if (t.d0 + c1 < a.D) to[c1] = q1;
+                    if (ALIGNED) {  // q is 2-byte aligned and D even
+                        if (y.has0) *reinterpret_cast<char2 *>(q + c0) = make_char2(q0, q1);
+                    } else {
+                        if (y.has0) q[c0] = q0;
+                        if (y.has1) q[c1] = q1;
                     }
                 }
             }
         }
-        if (next >= tiles) break;
+        if (!ahead) break;
         t = tn;
         next = after;
     }
-    In::wait();  // nothing may be in flight to shared memory at the end
+    if (ahead) in.wait(a.wait);  // nothing may be in flight to shared memory at the end
 }
 
 // ------------------------------------------------------------ backward
 
 // A pair of an 8-bit copy: int8 steps.
-template <bool VEC>
+template <bool ALIGNED>
 __device__ __forceinline__ char2 copy_pair(const GatedArgs &a, const Tile &t, int w, int tok) {
     if (tok >= t.n) return make_char2(0, 0);
     const int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok * a.D + t.d0;
-    const int c0 = channel<VEC>(0), c1 = channel<VEC>(1);
-    if (VEC)
+    const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
+    if (ALIGNED)
         return t.d0 + c0 < a.D ? *reinterpret_cast<const char2 *>(q + c0) : make_char2(0, 0);
     return make_char2(t.d0 + c0 < a.D ? q[c0] : 0, t.d0 + c1 < a.D ? q[c1] : 0);
 }
-template <bool VEC>
+template <bool ALIGNED>
 __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w) {
     const uint8_t *e = a.e + ((w * a.batch + t.b) * a.nb + t.blk) * a.D + t.d0;
-    const int c0 = channel<VEC>(0), c1 = channel<VEC>(1);
+    const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
     return f2_pack(t.d0 + c0 < a.D ? __uint_as_float((uint32_t)e[c0] << 23) : 0.f,
                    t.d0 + c1 < a.D ? __uint_as_float((uint32_t)e[c1] << 23) : 0.f);
 }
-__device__ __forceinline__ f2 widen(char2 v) { return f2_pack((float)v.x, (float)v.y); }
 
-template <typename T, bool VEC, bool CK>
+template <typename T, bool ALIGNED, bool CK>
 __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const GatedArgs a) {
-    extern __shared__ __align__(16) unsigned char staged[];
+    extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
     constexpr int kIn = CK ? 1 : 4;
-    using In = Stage<T, VEC, kIn>;
     using P2 = typename Pair<T>::type;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<VEC, true>(a, s, tiles);
+    open_block<ALIGNED, true>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<VEC, CK, true>(a, s, tiles, lanes);
+        chain_warp<ALIGNED, CK, true>(a, s, tiles, lanes);
         return;
     }
+    Stage<T, ALIGNED, kIn> in(staged, s.bars);
     const void *src[kIn];
     src[0] = a.dy;
     if constexpr (!CK) {
@@ -613,123 +702,143 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const Gated
         src[2] = a.i;
         src[3] = a.x;
     }
-    unsigned now = s.ticket[0], next = s.ticket[1];
-    if (now >= tiles) return;
-    Tile t = tile_of<true>(a, now);
-    In::request(staged, a, t, src);
+    const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
+    unsigned next = s.ticket[1];
+    if (s.ticket[0] >= tiles) return;
+    Tile t = tile_of<true>(a, s.ticket[0]);
+    in.request(a, t, src);
     unsigned mark = reset_byte(a, t);
     const int tok0 = warp * kRun;
-    const f2 one = f2_both(1.f), none = f2_both(0.f);
+    const f2 none = f2_both(0.f);
+    bool ahead = false;
     for (int n = 0;; ++n) {
-        const f2 k = f2_pack(s.k[n & 1][channel<VEC>(0)], s.k[n & 1][channel<VEC>(1)]);
-        const bool fast = all_fast(k);
+        const f2 k = f2_pack(s.k[n & 1][channel<ALIGNED>(0)], s.k[n & 1][channel<ALIGNED>(1)]);
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
+        const bool plain = all_fast(k) && marks == 0 && left >= kRun;
         // kept until the gradients: dy, x (as stored) and the two sigmoids
         std::conditional_t<CK, char2, P2> xr[kRun];
         P2 dyr[kRun];
         f2 sr[kRun], si[kRun], steps[3];
         if (CK) {
 #pragma unroll
-            for (int w = 0; w < 3; ++w) steps[w] = copy_step<VEC>(a, t, w);
+            for (int w = 0; w < 3; ++w) steps[w] = copy_step<ALIGNED>(a, t, w);
         }
-        auto xv = [&](int j) { return CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]); };
-        In::wait();
+        uint32_t at[kIn];
+#pragma unroll
+        for (int w = 0; w < kIn; ++w) at[w] = in.place(a, t, src[w]);
+        const bool here = in.wait(a.wait);
+        if (!here) give_up(a, &s.stop[n & 1]);
         f2 P = f2_both(1.f), H = none, R = none;
-        auto gates = [&](auto is_fast) {
+        auto gates = [&](auto run) {
+            constexpr bool kPlain = decltype(run)::value;
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                f2 rv, iv;
-                dyr[j] = In::raw(staged, a, t, src[0], 0, j);
+                f2 rv, iv, x;
+                dyr[j] = in.get(0, j, at[0], rowbytes);
                 if constexpr (CK) {
-                    xr[j] = copy_pair<VEC>(a, t, 0, tok0 + j);
-                    rv = f2_mul(widen(copy_pair<VEC>(a, t, 1, tok0 + j)), steps[1]);
-                    iv = f2_mul(widen(copy_pair<VEC>(a, t, 2, tok0 + j)), steps[2]);
+                    xr[j] = copy_pair<ALIGNED>(a, t, 0, tok0 + j);
+                    x = f2_mul(widen(xr[j]), steps[0]);
+                    rv = f2_mul(widen(copy_pair<ALIGNED>(a, t, 1, tok0 + j)), steps[1]);
+                    iv = f2_mul(widen(copy_pair<ALIGNED>(a, t, 2, tok0 + j)), steps[2]);
                 } else {
-                    rv = widen(In::raw(staged, a, t, src[1], 1, j));
-                    iv = widen(In::raw(staged, a, t, src[2], 2, j));
-                    xr[j] = In::raw(staged, a, t, src[3], 3, j);
+                    rv = widen(in.get(1, j, at[1], rowbytes));
+                    iv = widen(in.get(2, j, at[2], rowbytes));
+                    xr[j] = in.get(3, j, at[3], rowbytes);
+                    x = widen(xr[j]);
                 }
-                const Gate2 g = gate2<decltype(is_fast)::value>(rv, iv, k);
+                const Gate2 g = gate2<kPlain>(rv, iv, k);
                 sr[j] = g.sr;
                 si[j] = g.si;
-                const f2 vx = f2_mul(g.si, xv(j));
-                if (marks >> j & 1) {
+                const f2 vx = f2_mul(g.si, x);
+                if (kPlain || (j < left && !(marks >> j & 1))) {
+                    H = j == 0 ? f2_mul(g.m, vx) : f2_fma(g.a, H, f2_mul(g.m, vx));
+                    P = j == 0 ? g.a : f2_mul(P, g.a);
+                    // R: dy times the decays up to and with its own, before any reset
+                    if (kPlain || (marks & ((1u << j) - 1)) == 0)
+                        R = f2_fma(P, widen(dyr[j]), R);
+                } else if (j < left) {
                     P = f2_both(reset_decay());
                     H = vx;
-                } else if (j < left) {
-                    H = f2_fma(g.a, H, f2_mul(g.m, vx));
-                    P = f2_mul(P, g.a);
-                    // R: dy times the decays up to and with its own, before any reset
-                    if ((marks & ((1u << j) - 1)) == 0) R = f2_fma(P, widen(dyr[j]), R);
                 }
             }
         };
-        if (fast) gates(std::true_type{});
-        else gates(std::false_type{});
+        if (plain) gates(PlainRun());
+        else gates(AnyRun());
         s.maps[warp][lane] = as_map(P, H);
         float2 Rw;
         f2_unpack(R, Rw.x, Rw.y);
         s.right[warp][lane] = Rw;
         bar_arrive(kMapsReady);
         Tile tn = t;
-        if (next < tiles) {
+        ahead = here && next < tiles;
+        if (ahead) {
             tn = tile_of<true>(a, next);
-            In::request(staged, a, tn, src);
+            in.request(a, tn, src);
             mark = reset_byte(a, tn);
         }
         bar_sync(kEntryReady);
-        if (s.stop) break;
+        if (s.stop[n & 1]) {
+            if (!here) in.wait(a.wait);
+            break;
+        }
         const unsigned after = s.ticket[n & 1];
         f2 dl = none;
-        auto grads = [&](auto is_fast) {
-            constexpr bool kFast = decltype(is_fast)::value;
+        auto grads = [&](auto run) {
+            constexpr bool kPlain = decltype(run)::value;
+            const int64_t row = t.row0 + tok0 * a.D;
+            const Rows<T, ALIGNED> dx(a.dx, row, t.d0, a.D), dr(a.dr, row, t.d0, a.D),
+                di(a.di, row, t.d0, a.D);
             f2 E[kRun], G[kRun];
             f2 c = s.grad[warp][lane];
 #pragma unroll
             for (int j = kRun - 1; j >= 0; --j) {
-                E[j] = j < left ? expm1_neg2<kFast>(f2_mul(k, sr[j])) : none;  // a = 1 + E
-                G[j] = f2_add(j < left ? widen(dyr[j]) : none, c);
-                c = (marks >> j & 1) ? none : f2_fma(E[j], G[j], G[j]);
+                if (kPlain || j < left) {
+                    E[j] = expm1_neg2<kPlain>(f2_mul(k, sr[j]));  // a = 1 + E
+                    G[j] = f2_add(widen(dyr[j]), c);
+                    c = (!kPlain && (marks >> j & 1)) ? none : f2_fma(E[j], G[j], G[j]);
+                } else {
+                    E[j] = G[j] = none;
+                }
             }
             f2 h = s.entry[warp][lane];
+            int64_t off = 0;
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) {
-                const bool cut = marks >> j & 1;
+            for (int j = 0; j < kRun; ++j, off += a.D) {
+                if (!kPlain && j >= left) break;
+                const bool cut = !kPlain && (marks >> j & 1);
                 Gate2 g;
                 decay_from2(E[j], g);
-                const f2 vx = f2_mul(si[j], xv(j));  // sigmoid(i) x
+                const f2 x = CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]);
+                const f2 vx = f2_mul(si[j], x);  // sigmoid(i) x
                 const f2 gm = cut ? G[j] : f2_mul(G[j], g.m);
                 // s dm/ds = -s a^2 / m: finite where s -> 0
                 const f2 sa = f2_mul(f2_mul(k, sr[j]), g.a);
                 const f2 e = cut ? none
                                  : f2_mul(f2_mul(G[j], sa),
                                           f2_fma(f2_neg(f2_mul(g.a, g.rm)), vx, h));
-                if (j < left) {
-                    dl = f2_add(dl, e);
-                    const int64_t row = t.row0 + (tok0 + j) * a.D;
-                    store_pair<T, VEC>(a.dx, row, a, t.d0, f2_mul(gm, si[j]));
-                    store_pair<T, VEC>(a.dr, row, a, t.d0, f2_fma(f2_neg(e), sr[j], e));
-                    const f2 gv = f2_mul(gm, vx);
-                    store_pair<T, VEC>(a.di, row, a, t.d0, f2_fma(f2_neg(gv), si[j], gv));
-                }
+                dl = f2_add(dl, e);
+                const f2 gv = f2_mul(gm, vx);
+                dx.put(off, f2_mul(gm, si[j]));
+                dr.put(off, f2_fma(f2_neg(e), sr[j], e));
+                di.put(off, f2_fma(f2_neg(gv), si[j], gv));
                 h = cut ? vx : f2_fma(g.a, h, f2_mul(g.m, vx));
             }
         };
-        if (fast) grads(std::true_type{});
-        else grads(std::false_type{});
+        if (plain) grads(PlainRun());
+        else grads(AnyRun());
         float2 dw;
         f2_unpack(dl, dw.x, dw.y);
-        s.dlam[n & 1][warp][channel<VEC>(0)] = dw.x;
-        s.dlam[n & 1][warp][channel<VEC>(1)] = dw.y;
-        if (next >= tiles) {
+        s.dlam[n & 1][warp][channel<ALIGNED>(0)] = dw.x;
+        s.dlam[n & 1][warp][channel<ALIGNED>(1)] = dw.y;
+        if (!ahead) {
             bar_arrive(kMapsReady);  // the chain warp takes the last tile's dlam
             break;
         }
         t = tn;
         next = after;
     }
-    In::wait();
+    if (ahead) in.wait(a.wait);
 }
 
 // dlam: the blocks' sums over batch and blocks, times the channel's factor.
@@ -763,8 +872,18 @@ __global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x
 
 // ------------------------------------------------------------ host
 
+// Clears the words that tiles publish and the counter, and prepares the gate
+// scales k = -c softplus(lam).
+__global__ void gated_open_kernel(const GatedArgs a, int64_t words) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i == 0) *a.counter = *a.abort = 0;
+    if (i < a.D) a.scale[i] = -a.c * softplus_full(a.lam[i]);
+    // ends and maps are neighbours, each a multiple of 16 bytes
+    if (2 * i < words) reinterpret_cast<ulonglong2 *>(a.ends)[i] = make_ulonglong2(kEmpty, kEmpty);
+}
+
 // Thread blocks of a persistent kernel: as many as fit, fewer where there are
-// fewer tiles; without a chain one per tile.
+// fewer tiles; with one block of tokens one per tile.
 template <typename F>
 cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -772,51 +891,52 @@ cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, 
     int per_sm = 1, dev = 0, sms = 0;
     const int64_t tiles = a.batch * a.dblocks * a.nb;
     int64_t grid = tiles;
+    const int64_t words = a.nb > 1 ? tiles * 32 * 3 : 0;
     if (e == cudaSuccess && a.nb > 1) {
         if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
             (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
         if (e == cudaSuccess && (int64_t)per_sm * sms < grid) grid = (int64_t)per_sm * sms;
-        if (e == cudaSuccess) e = cudaMemsetAsync(a.counter, 0, 256, st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(a.ends, 0xff, (size_t)tiles * 32 * 24, st);
     }
     if (e != cudaSuccess) return e;
+    const int64_t n = words / 2 > a.D ? words / 2 : a.D;
+    launch_begin("gated_open", st);
+    gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, words);
+    launch_end(st);
     launch_begin(name, st);
     kernel<<<(unsigned)grid, kThreads, smem, st>>>(a);
     launch_end(st);
     return cudaGetLastError();
 }
 
-bool even(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <typename T, bool VEC>
+template <typename T, bool ALIGNED>
 cudaError_t forward_t(const GatedArgs &a, cudaStream_t st) {
-    const size_t smem = Stage<T, VEC, 3>::kBytes;
-    return a.q ? start("gated_forward", gated_forward_kernel<T, VEC, true>, smem, a, st)
-               : start("gated_forward", gated_forward_kernel<T, VEC, false>, smem, a, st);
+    const size_t smem = Stage<T, ALIGNED, 3>::kBytes;
+    return a.q ? start("gated_forward", gated_forward_kernel<T, ALIGNED, true>, smem, a, st)
+               : start("gated_forward", gated_forward_kernel<T, ALIGNED, false>, smem, a, st);
 }
 template <typename T>
 cudaError_t forward_v(const GatedArgs &a, cudaStream_t st) {
-    const size_t two = 2 * sizeof(T);
-    const bool vec = a.D % 2 == 0 && even(a.x, two) && even(a.r, two) && even(a.i, two) &&
-                     even(a.y, two) && even(a.q, 2);
-    return vec ? forward_t<T, true>(a, st) : forward_t<T, false>(a, st);
+    const bool aligned = a.D * (int64_t)sizeof(T) % 16 == 0 && on(a.x, 16) && on(a.r, 16) &&
+                         on(a.i, 16) && on(a.y, 8) && on(a.q, 2);
+    return aligned ? forward_t<T, true>(a, st) : forward_t<T, false>(a, st);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool ALIGNED>
 cudaError_t backward_t(const GatedArgs &a, cudaStream_t st) {
-    return a.q ? start("gated_backward", gated_backward_kernel<T, VEC, true>,
-                       Stage<T, VEC, 1>::kBytes, a, st)
-               : start("gated_backward", gated_backward_kernel<T, VEC, false>,
-                       Stage<T, VEC, 4>::kBytes, a, st);
+    return a.q ? start("gated_backward", gated_backward_kernel<T, ALIGNED, true>,
+                       Stage<T, ALIGNED, 1>::kBytes, a, st)
+               : start("gated_backward", gated_backward_kernel<T, ALIGNED, false>,
+                       Stage<T, ALIGNED, 4>::kBytes, a, st);
 }
 template <typename T>
 cudaError_t backward_v(const GatedArgs &a, float *dlam, cudaStream_t st) {
-    const size_t two = 2 * sizeof(T);
-    const bool vec = a.D % 2 == 0 && even(a.x, two) && even(a.r, two) && even(a.i, two) &&
-                     even(a.dy, two) && even(a.dx, two) && even(a.dr, two) && even(a.di, two) &&
-                     even(a.q, 2);
-    cudaError_t e = vec ? backward_t<T, true>(a, st) : backward_t<T, false>(a, st);
+    const bool aligned = a.D * (int64_t)sizeof(T) % 16 == 0 && on(a.x, 16) && on(a.r, 16) &&
+                         on(a.i, 16) && on(a.dy, 16) && on(a.dx, 8) && on(a.dr, 8) &&
+                         on(a.di, 8) && on(a.q, 2);
+    cudaError_t e = aligned ? backward_t<T, true>(a, st) : backward_t<T, false>(a, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
     gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 8), 0, st>>>(
@@ -841,9 +961,10 @@ size_t carve(const Problem &pr, GatedArgs &a, void *ws, bool back) {
         at += align256(bytes);
         return here;
     };
+    a.counter = reinterpret_cast<unsigned *>(take(256));
+    a.abort = a.counter + 32;
+    a.scale = reinterpret_cast<float *>(take((size_t)a.D * sizeof(float)));
     if (a.nb > 1) {
-        a.counter = reinterpret_cast<unsigned *>(take(256));
-        a.abort = a.counter + 32;
         a.ends = reinterpret_cast<unsigned long long *>(take(tiles * 32 * 8));
         a.maps = reinterpret_cast<unsigned long long *>(take(tiles * 32 * 16));
     }

@@ -8,8 +8,8 @@
 // a is close to 1 for channels that remember long, and an error of a is
 // multiplied by that memory, so nothing here forms 1 - a by subtraction:
 // with E = exp(s) - 1, a = 1 + E (one rounding) and m^2 = -E (2 + E). For
-// s >= kSeries, E is its Taylor series s (1 + s/2 + ... + s^5/720), whose
-// remainder is below s^6/5040 < 1e-9 relative; below, exp2 of the
+// s >= kSeries, E is its Taylor series s (1 + s/2 + ... + s^4/120), whose
+// remainder is below s^5/720 < 5e-8 relative; below, exp2 of the
 // special-function unit (relative error about 2^-22) minus one, where
 // |E| > 0.11. The series takes no special-function operation; those bind these
 // kernels beside the memory (16 a clock and SM), so both sigmoids also share
@@ -65,8 +65,7 @@ __device__ __forceinline__ void two_sigmoids(float r, float i, float &sr, float 
 // E = exp(s) - 1 for s <= 0. FAST: the caller knows that s >= kSeries.
 template <bool FAST>
 __device__ __forceinline__ float expm1_neg(float s) {
-    float p = 1.f / 720.f;
-    p = fmaf(p, s, 1.f / 120.f);
+    float p = 1.f / 120.f;
     p = fmaf(p, s, 1.f / 24.f);
     p = fmaf(p, s, 1.f / 6.f);
     p = fmaf(p, s, 0.5f);
@@ -137,8 +136,7 @@ __device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si) {
 }
 template <bool FAST>
 __device__ __forceinline__ f2 expm1_neg2(f2 s) {
-    f2 p = f2_both(1.f / 720.f);
-    p = f2_fma(p, s, f2_both(1.f / 120.f));
+    f2 p = f2_both(1.f / 120.f);
     p = f2_fma(p, s, f2_both(1.f / 24.f));
     p = f2_fma(p, s, f2_both(1.f / 6.f));
     p = f2_fma(p, s, f2_both(0.5f));
@@ -151,14 +149,14 @@ __device__ __forceinline__ f2 expm1_neg2(f2 s) {
     return f2_pack(s0 >= kSeries ? e0 : tc::fast_exp2(s0 * kLog2e) - 1.f,
                    s1 >= kSeries ? e1 : tc::fast_exp2(s1 * kLog2e) - 1.f);
 }
-// a, m and 1 / m from E = a - 1.
+// a, m and 1 / m from E = a - 1: m^2 = -E (1 + a) = -(E + E a).
 __device__ __forceinline__ void decay_from2(f2 E, Gate2 &g) {
     g.a = f2_add(f2_both(1.f), E);
-    const f2 m2 = f2_mul(f2_neg(E), f2_add(f2_both(2.f), E));
     float lo, hi;
-    f2_unpack(m2, lo, hi);
-    g.rm = f2_pack(rsqrt_approx(lo < 1e-36f ? 1e-36f : lo), rsqrt_approx(hi < 1e-36f ? 1e-36f : hi));
-    g.m = f2_mul(m2, g.rm);
+    f2_unpack(f2_fma(E, g.a, E), lo, hi);
+    const float l = fmaxf(-lo, 1e-36f), h = fmaxf(-hi, 1e-36f);
+    g.rm = f2_pack(rsqrt_approx(l), rsqrt_approx(h));
+    g.m = f2_mul(f2_pack(-lo, -hi), g.rm);
 }
 template <bool FAST>
 __device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
