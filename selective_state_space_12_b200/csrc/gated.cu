@@ -26,6 +26,8 @@
 // kernel, and is complete once it differs from that: readers poll the data
 // itself, one trip to L2, and no fence stands between data and flag. Waits are
 // bounded; one that runs out tells the others and all return.
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "gated.cuh"
@@ -148,16 +150,21 @@ struct Rows {
 // ------------------------------------------------------------ staged inputs
 
 // Each warp brings its own eight tokens' rows of every input tensor to shared
-// memory a tile ahead, by one bulk copy a row (a lane each), counted by a
-// barrier of its own: no registers, no address arithmetic in the loop, and no
-// waiting for other warps. A copy starts and ends on 16 bytes: where rows do
-// not, it takes the 16-byte windows that cover the row (at most 16 bytes more),
-// and the lanes read from the row's place in it; a window that would leave the
-// tensor (its first and last rows only) is replaced by plain loads.
+// memory a tile ahead and waits for nobody else's. Where rows are 16-byte
+// aligned, one TMA load a tensor does it, counted by the warp's own barrier;
+// past the last token and channel it fills zeros. Elsewhere the lanes copy the
+// 4-byte words that cover each row (33 for bf16 rows that start inside one)
+// asynchronously, and read from the row's place in them. Words that may leave
+// the tensor (the last tile's; a bf16 tensor that starts inside a word) are
+// replaced by plain loads.
+struct Maps {
+    CUtensorMap m[4];
+};
+
 template <typename T, bool ALIGNED, int TENSORS>
 struct Stage {
     using P = typename Pair<T>::type;
-    static constexpr int kPitch = kTileCh * (int)sizeof(T) + 16;
+    static constexpr int kPitch = kTileCh * (int)sizeof(T) + (ALIGNED ? 0 : 16);
     static constexpr int kWarpBytes = TENSORS * kRun * kPitch;
     static constexpr size_t kBytes = (size_t)kWarps * kWarpBytes;
 
@@ -168,60 +175,92 @@ struct Stage {
     __device__ __forceinline__ Stage(unsigned char *all, uint64_t *bars)
         : buf(all + (threadIdx.x >> 5) * kWarpBytes), bar(bars + (threadIdx.x >> 5)), parity(0) {}
 
-    __device__ __forceinline__ void request(const GatedArgs &a, const Tile &t,
+    __device__ __forceinline__ void request(const GatedArgs &a, const Maps &maps, const Tile &t,
                                             const void *const (&src)[TENSORS]) const {
         const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
-        const int w = lane / kRun, j = lane % kRun;
-        const int64_t left = a.D - t.d0;
-        const int len = (int)(left < kTileCh ? left : kTileCh) * (int)sizeof(T);
-        const char *base = nullptr, *row = nullptr, *from = nullptr;
-        uint32_t bytes = 0;
-        bool plain = false;
-        if (w < TENSORS && tok0 + j < t.n) {
+        __syncwarp();  // the rows have been read
+        if constexpr (ALIGNED) {
+            if (lane == 0) {
+                const bool any = tok0 < t.n;
+                tc::mbar_arrive_expect_tx(bar, any ? kWarpBytes : 0);
+                if (any) {
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k)
-                if (k == w) base = static_cast<const char *>(src[k]);
-            row = base + (t.row0 + (tok0 + j) * a.D + t.d0) * (int64_t)sizeof(T);
-            from = row;
-            bytes = (uint32_t)len;
-            if constexpr (!ALIGNED) {
-                const uintptr_t lo = reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15);
-                const uintptr_t hi = (reinterpret_cast<uintptr_t>(row) + len + 15) & ~uintptr_t(15);
-                const uintptr_t end = reinterpret_cast<uintptr_t>(base) +
-                                      (uintptr_t)(a.batch * a.L * a.D) * sizeof(T);
-                plain = lo < reinterpret_cast<uintptr_t>(base) || hi > end;
-                from = reinterpret_cast<const char *>(lo);
-                bytes = plain ? 0u : (uint32_t)(hi - lo);
+                    for (int w = 0; w < TENSORS; ++w)
+                        tc::tma_load_4d(buf + w * kRun * kPitch, &maps.m[w], bar, t.d0,
+                                        (int)(t.blk * kBlock) + tok0, (int)t.b, 0);
+                }
             }
-        }
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-        unsigned char *to = buf + lane * kPitch;
-        if constexpr (!ALIGNED) {
-            if (plain) {
-                T *dst = reinterpret_cast<T *>(to + (row - from));
-                for (int c = 0; c < len / (int)sizeof(T); ++c)
-                    dst[c] = reinterpret_cast<const T *>(row)[c];
+        } else {
+            const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
+            const bool last = t.b == a.batch - 1 && t.blk == a.nb - 1 && t.d0 + kTileCh >= a.D;
+            const int64_t row0 = t.row0 + (int64_t)tok0 * a.D + t.d0;
+            if (sizeof(T) == 4 || last || !a.words) {
+#pragma unroll
+                for (int w = 0; w < TENSORS; ++w)
+#pragma unroll
+                    for (int j = 0; j < kRun; ++j) {
+                        if (tok0 + j >= t.n) break;
+                        const T *row = static_cast<const T *>(src[w]) + row0 + j * a.D;
+                        unsigned char *to = buf + (w * kRun + j) * kPitch +
+                                            (sizeof(T) == 4 ? 0u : ((uint32_t)(uintptr_t)row & 3u));
+#pragma unroll
+                        for (int c = lane; c < kTileCh; c += 32) {
+                            if (c >= len) continue;
+                            if constexpr (sizeof(T) == 4)
+                                copy4(to + 4 * c, row + c);
+                            else
+                                reinterpret_cast<T *>(to)[c] = row[c];
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int w = 0; w < TENSORS; ++w) {
+                    const uintptr_t row = reinterpret_cast<uintptr_t>(src[w]) + 2 * row0;
+#pragma unroll
+                    for (int j = 0; j < kRun; ++j) {
+                        if (tok0 + j >= t.n) break;
+                        const uintptr_t r = row + 2 * (uintptr_t)(j * a.D);
+                        const int words = ((int)(r & 3) + 2 * len + 3) / 4;
+                        if (lane < words)
+                            copy4(buf + (w * kRun + j) * kPitch + 4 * lane,
+                                  reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * lane));
+                    }
+                }
+                // the 33rd words: lane w kRun + j
+                const int w = lane / kRun, j = lane % kRun;
+                if (w < TENSORS && tok0 + j < t.n) {
+                    uintptr_t row = 0;
+#pragma unroll
+                    for (int v = 0; v < TENSORS; ++v)
+                        if (v == w) row = reinterpret_cast<uintptr_t>(src[v]) + 2 * (row0 + j * a.D);
+                    if ((int)(row & 3) + 2 * len > 128)
+                        copy4(buf + lane * kPitch + 128,
+                              reinterpret_cast<const void *>((row & ~uintptr_t(3)) + 128));
+                }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, total);
-        __syncwarp();
-        if (bytes > 0)
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-                "[%3];" ::"r"(tc::smem_u32(to)),
-                "l"(from), "r"(bytes), "r"(tc::smem_u32(bar))
-                : "memory");
+    }
+    static __device__ __forceinline__ void copy4(void *to, const void *from) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from)
+                     : "memory");
     }
     // False when the wait ran out.
     __device__ __forceinline__ bool wait(long long limit) {
-        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
-        if (ok) parity ^= 1;
-        return ok;
+        if constexpr (ALIGNED) {
+            const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
+            if (ok) parity ^= 1;
+            return ok;
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            return true;
+        }
     }
-    // Where in its window token 0's row of a tensor lies, and how far on the next.
+    // The address, in its low bits, of this warp's first row of a tensor.
     static __device__ __forceinline__ uint32_t place(const GatedArgs &a, const Tile &t,
                                                      const void *src) {
-        if (ALIGNED) return 0;
+        if (ALIGNED || sizeof(T) == 4) return 0;
         return (uint32_t)reinterpret_cast<uintptr_t>(
             static_cast<const char *>(src) +
             (t.row0 + (int64_t)((threadIdx.x >> 5) * kRun) * a.D + t.d0) * (int64_t)sizeof(T));
@@ -231,7 +270,8 @@ struct Stage {
         if constexpr (ALIGNED) {
             return reinterpret_cast<const P *>(row)[threadIdx.x & 31];
         } else {
-            const T *v = reinterpret_cast<const T *>(row + ((place0 + j * rowbytes) & 15u)) +
+            const T *v = reinterpret_cast<const T *>(
+                             row + (sizeof(T) == 4 ? 0u : ((place0 + j * rowbytes) & 3u))) +
                          (threadIdx.x & 31);
             if constexpr (sizeof(T) == 4)
                 return make_float2(v[0], v[32]);
@@ -344,7 +384,7 @@ struct Shared {
     float2 right[kWarps][32];  // backward: R of each run
     f2 entry[kWarps][32];      // the state entering each run
     f2 grad[kWarps][32];       // backward: the gradient entering it from its right
-    float k[2][kTileCh];       // -c softplus(lam), of this and the next tile
+    float k[2][kTileCh];       // c softplus(lam), of this and the next tile
     float dlam[2][kWarps][kTileCh];
     unsigned top[2][3][kTileCh];  // 8-bit copies: largest magnitudes
     unsigned code[3][kTileCh];
@@ -372,7 +412,7 @@ __device__ __forceinline__ void give_up(const GatedArgs &a, int *stop) {
 __device__ __forceinline__ bool all_fast(f2 k) {
     float lo, hi;
     f2_unpack(k, lo, hi);
-    return __all_sync(0xffffffffu, lo >= kSeries && hi >= kSeries);
+    return __all_sync(0xffffffffu, lo <= kSeries && hi <= kSeries);
 }
 
 // ------------------------------------------------------------ 8-bit copies
@@ -527,7 +567,8 @@ struct AnyRun : std::false_type {};
 // ------------------------------------------------------------ forward
 
 template <typename T, bool ALIGNED, bool CK>
-__global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
+    const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -544,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(con
     unsigned next = s.ticket[1];
     if (s.ticket[0] >= tiles) return;
     Tile t = tile_of<false>(a, s.ticket[0]);
-    in.request(a, t, src);
+    in.request(a, maps, t, src);
     unsigned mark = reset_byte(a, t);
     const int tok0 = warp * kRun;
     bool ahead = false;  // copies are on their way
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(con
         ahead = here && next < tiles;
         if (ahead) {  // the next tile's inputs are on their way while this one waits
             tn = tile_of<false>(a, next);
-            in.request(a, tn, src);
+            in.request(a, maps, tn, src);
             mark = reset_byte(a, tn);
         }
         bar_sync(kEntryReady);
@@ -681,7 +722,8 @@ __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w
 }
 
 template <typename T, bool ALIGNED, bool CK>
-__global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const GatedArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
+    const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
     constexpr int kIn = CK ? 1 : 4;
@@ -706,10 +748,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const Gated
     unsigned next = s.ticket[1];
     if (s.ticket[0] >= tiles) return;
     Tile t = tile_of<true>(a, s.ticket[0]);
-    in.request(a, t, src);
+    in.request(a, maps, t, src);
     unsigned mark = reset_byte(a, t);
     const int tok0 = warp * kRun;
-    const f2 none = f2_both(0.f);
+    const f2 none = f2_both(0.f), one = f2_both(1.f);
     bool ahead = false;
     for (int n = 0;; ++n) {
         const f2 k = f2_pack(s.k[n & 1][channel<ALIGNED>(0)], s.k[n & 1][channel<ALIGNED>(1)]);
@@ -774,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const Gated
         ahead = here && next < tiles;
         if (ahead) {
             tn = tile_of<true>(a, next);
-            in.request(a, tn, src);
+            in.request(a, maps, tn, src);
             mark = reset_byte(a, tn);
         }
         bar_sync(kEntryReady);
@@ -789,16 +831,16 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const Gated
             const int64_t row = t.row0 + tok0 * a.D;
             const Rows<T, ALIGNED> dx(a.dx, row, t.d0, a.D), dr(a.dr, row, t.d0, a.D),
                 di(a.di, row, t.d0, a.D);
-            f2 E[kRun], G[kRun];
+            f2 F[kRun], G[kRun];
             f2 c = s.grad[warp][lane];
 #pragma unroll
             for (int j = kRun - 1; j >= 0; --j) {
                 if (kPlain || j < left) {
-                    E[j] = expm1_neg2<kPlain>(f2_mul(k, sr[j]));  // a = 1 + E
+                    F[j] = forget2<kPlain>(f2_mul(k, sr[j]));  // a = 1 - F
                     G[j] = f2_add(widen(dyr[j]), c);
-                    c = (!kPlain && (marks >> j & 1)) ? none : f2_fma(E[j], G[j], G[j]);
+                    c = (!kPlain && (marks >> j & 1)) ? none : f2_mul(f2_sub(one, F[j]), G[j]);
                 } else {
-                    E[j] = G[j] = none;
+                    F[j] = G[j] = none;
                 }
             }
             f2 h = s.entry[warp][lane];
@@ -808,20 +850,20 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(const Gated
                 if (!kPlain && j >= left) break;
                 const bool cut = !kPlain && (marks >> j & 1);
                 Gate2 g;
-                decay_from2(E[j], g);
+                decay_from2(F[j], g);
                 const f2 x = CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]);
                 const f2 vx = f2_mul(si[j], x);  // sigmoid(i) x
                 const f2 gm = cut ? G[j] : f2_mul(G[j], g.m);
-                // s dm/ds = -s a^2 / m: finite where s -> 0
-                const f2 sa = f2_mul(f2_mul(k, sr[j]), g.a);
+                // q dm/dq = q a^2 / m: finite where q -> 0
+                const f2 qa = f2_mul(f2_mul(k, sr[j]), g.a);
                 const f2 e = cut ? none
-                                 : f2_mul(f2_mul(G[j], sa),
-                                          f2_fma(f2_neg(f2_mul(g.a, g.rm)), vx, h));
+                                 : f2_mul(f2_mul(G[j], qa),
+                                          f2_sub(f2_mul(f2_mul(g.a, g.rm), vx), h));
                 dl = f2_add(dl, e);
                 const f2 gv = f2_mul(gm, vx);
                 dx.put(off, f2_mul(gm, si[j]));
-                dr.put(off, f2_fma(f2_neg(e), sr[j], e));
-                di.put(off, f2_fma(f2_neg(gv), si[j], gv));
+                dr.put(off, f2_mul(e, f2_sub(one, sr[j])));
+                di.put(off, f2_mul(gv, f2_sub(one, si[j])));
                 h = cut ? vx : f2_fma(g.a, h, f2_mul(g.m, vx));
             }
         };
@@ -864,7 +906,7 @@ __global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x
                                   int64_t D, int64_t n) {
     const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (at >= n) return;
-    const Gate g = gate(to_f(r[at]), to_f(i[at]), -c * softplus_full(lam[at % D]));
+    const Gate g = gate(to_f(r[at]), to_f(i[at]), c * softplus_full(lam[at % D]));
     const float v = fmaf(g.a, h[at], g.m * g.si * to_f(x[at]));
     h[at] = v;
     y[at] = from_f<T>(v);
@@ -873,11 +915,11 @@ __global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x
 // ------------------------------------------------------------ host
 
 // Clears the words that tiles publish and the counter, and prepares the gate
-// scales k = -c softplus(lam).
+// scales k = c softplus(lam).
 __global__ void gated_open_kernel(const GatedArgs a, int64_t words) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i == 0) *a.counter = *a.abort = 0;
-    if (i < a.D) a.scale[i] = -a.c * softplus_full(a.lam[i]);
+    if (i < a.D) a.scale[i] = a.c * softplus_full(a.lam[i]);
     // ends and maps are neighbours, each a multiple of 16 bytes
     if (2 * i < words) reinterpret_cast<ulonglong2 *>(a.ends)[i] = make_ulonglong2(kEmpty, kEmpty);
 }
@@ -885,7 +927,8 @@ __global__ void gated_open_kernel(const GatedArgs a, int64_t words) {
 // Thread blocks of a persistent kernel: as many as fit, fewer where there are
 // fewer tiles; with one block of tokens one per tile.
 template <typename F>
-cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, cudaStream_t st) {
+cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, const Maps &maps,
+                  cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     int per_sm = 1, dev = 0, sms = 0;
@@ -904,39 +947,73 @@ cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, 
     gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, words);
     launch_end(st);
     launch_begin(name, st);
-    kernel<<<(unsigned)grid, kThreads, smem, st>>>(a);
+    kernel<<<(unsigned)grid, kThreads, smem, st>>>(a, maps);
     launch_end(st);
     return cudaGetLastError();
 }
 
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <typename T, bool ALIGNED>
-cudaError_t forward_t(const GatedArgs &a, cudaStream_t st) {
-    const size_t smem = Stage<T, ALIGNED, 3>::kBytes;
-    return a.q ? start("gated_forward", gated_forward_kernel<T, ALIGNED, true>, smem, a, st)
-               : start("gated_forward", gated_forward_kernel<T, ALIGNED, false>, smem, a, st);
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault,
+                                                &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
 }
+
+// A map over a (b, L, D) tensor whose box is one warp's rows of a tile. False
+// where the tensor's layout has none (the unaligned path then serves it).
 template <typename T>
-cudaError_t forward_v(const GatedArgs &a, cudaStream_t st) {
-    const bool aligned = a.D * (int64_t)sizeof(T) % 16 == 0 && on(a.x, 16) && on(a.r, 16) &&
-                         on(a.i, 16) && on(a.y, 8) && on(a.q, 2);
-    return aligned ? forward_t<T, true>(a, st) : forward_t<T, false>(a, st);
+bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
+    const uint64_t row = (uint64_t)a.D * sizeof(T);
+    if (!encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1};
+    const cuuint64_t strides[3] = {row, row * (uint64_t)a.L, row * (uint64_t)a.L};
+    const cuuint32_t box[4] = {kTileCh, kRun, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return encoder()(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     4, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, bool ALIGNED>
-cudaError_t backward_t(const GatedArgs &a, cudaStream_t st) {
-    return a.q ? start("gated_backward", gated_backward_kernel<T, ALIGNED, true>,
-                       Stage<T, ALIGNED, 1>::kBytes, a, st)
-               : start("gated_backward", gated_backward_kernel<T, ALIGNED, false>,
-                       Stage<T, ALIGNED, 4>::kBytes, a, st);
+cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
+    const size_t smem = Stage<T, ALIGNED, 3>::kBytes;
+    return a.q ? start("gated_forward", gated_forward_kernel<T, ALIGNED, true>, smem, a, maps, st)
+               : start("gated_forward", gated_forward_kernel<T, ALIGNED, false>, smem, a, maps, st);
 }
 template <typename T>
-cudaError_t backward_v(const GatedArgs &a, float *dlam, cudaStream_t st) {
-    const bool aligned = a.D * (int64_t)sizeof(T) % 16 == 0 && on(a.x, 16) && on(a.r, 16) &&
-                         on(a.i, 16) && on(a.dy, 16) && on(a.dx, 8) && on(a.dr, 8) &&
-                         on(a.di, 8) && on(a.q, 2);
-    cudaError_t e = aligned ? backward_t<T, true>(a, st) : backward_t<T, false>(a, st);
+cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
+    Maps maps;
+    const bool aligned = on(a.y, 8) && on(a.q, 2) && make_map<T>(&maps.m[0], a.x, a) &&
+                         make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a);
+    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4);
+    return aligned ? forward_t<T, true>(a, maps, st) : forward_t<T, false>(a, maps, st);
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
+    return a.q ? start("gated_backward", gated_backward_kernel<T, ALIGNED, true>,
+                       Stage<T, ALIGNED, 1>::kBytes, a, maps, st)
+               : start("gated_backward", gated_backward_kernel<T, ALIGNED, false>,
+                       Stage<T, ALIGNED, 4>::kBytes, a, maps, st);
+}
+template <typename T>
+cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
+    Maps maps;
+    const bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && on(a.q, 2) &&
+                         make_map<T>(&maps.m[0], a.dy, a) &&
+                         (a.q || (make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a) &&
+                                  make_map<T>(&maps.m[3], a.x, a)));
+    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4) && on(a.dy, 4);
+    cudaError_t e = aligned ? backward_t<T, true>(a, maps, st) : backward_t<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
     gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 8), 0, st>>>(

@@ -1,19 +1,18 @@
 // Arithmetic of the gated linear recurrence, shared by its kernels (gated.cu).
 //
-// For one channel with k = -c softplus(lam) <= 0, and gates r, i of a token:
+// For one channel with k = c softplus(lam) >= 0, and gates r, i of a token:
 //
-//   s = k sigmoid(r)      a = exp(s)      m = sqrt(1 - a^2)
-//   h <- a h + m sigmoid(i) x             (a reset token: a = 0, m = 1)
+//   q = k sigmoid(r)      a = exp(-q)      m = sqrt(1 - a^2)
+//   h <- a h + m sigmoid(i) x              (a reset token: a = 0, m = 1)
 //
 // a is close to 1 for channels that remember long, and an error of a is
 // multiplied by that memory, so nothing here forms 1 - a by subtraction:
-// with E = exp(s) - 1, a = 1 + E (one rounding) and m^2 = -E (2 + E). For
-// s >= kSeries, E is its Taylor series s (1 + s/2 + ... + s^4/120), whose
-// remainder is below s^5/720 < 5e-8 relative; below, exp2 of the
-// special-function unit (relative error about 2^-22) minus one, where
-// |E| > 0.11. The series takes no special-function operation; those bind these
-// kernels beside the memory (16 a clock and SM), so both sigmoids also share
-// one reciprocal.
+// with F = 1 - exp(-q), a = 1 - F (one rounding) and m^2 = F (1 + a). For
+// q <= kSeries, F is its Taylor series q (1 - q/2 + ... + q^4/120), whose
+// remainder is below q^5/720 < 5e-8 relative; above, one minus exp2 of the
+// special-function unit (relative error about 2^-22), where F > 0.11. The
+// series takes no special-function operation; those bind these kernels beside
+// the memory (16 a clock and SM), so both sigmoids also share one reciprocal.
 #pragma once
 
 #include "common.cuh"
@@ -23,7 +22,7 @@ namespace ssd {
 namespace gated {
 
 constexpr int kBlock = 64;          // SSD_GATED_BLOCK: tokens per saved state and 8-bit scale
-constexpr float kSeries = -0.125f;
+constexpr float kSeries = 0.125f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float rcp_approx(float v) {
@@ -42,7 +41,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
     return y;
 }
 
-// k = -c softplus(lam), and sigmoid(lam) / softplus(lam) (its limit 1 where
+// softplus(lam), and sigmoid(lam) / softplus(lam) (its limit 1 where
 // softplus underflows), by which the gradient of lam follows from that of log a.
 __device__ __forceinline__ float softplus_full(float v) {
     return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
@@ -62,17 +61,14 @@ __device__ __forceinline__ void two_sigmoids(float r, float i, float &sr, float 
     si = p * R;
 }
 
-// E = exp(s) - 1 for s <= 0. FAST: the caller knows that s >= kSeries.
-template <bool FAST>
-__device__ __forceinline__ float expm1_neg(float s) {
+// F = 1 - exp(-q) for q = -log a >= 0.
+__device__ __forceinline__ float forget(float q) {
     float p = 1.f / 120.f;
-    p = fmaf(p, s, 1.f / 24.f);
-    p = fmaf(p, s, 1.f / 6.f);
-    p = fmaf(p, s, 0.5f);
-    p = fmaf(p, s, 1.f);
-    const float series = s * p;
-    if (FAST) return series;
-    return s >= kSeries ? series : tc::fast_exp2(s * kLog2e) - 1.f;
+    p = fmaf(p, q, -1.f / 24.f);
+    p = fmaf(p, q, 1.f / 6.f);
+    p = fmaf(p, q, -0.5f);
+    p = fmaf(p, q, 1.f);
+    return q <= kSeries ? q * p : 1.f - tc::fast_exp2(-q * kLog2e);
 }
 
 // A reset's decay is written -0: it passes nothing on, whatever stands before
@@ -96,10 +92,10 @@ __device__ __forceinline__ Gate gate(float r, float i, float k) {
     Gate g;
     float sr;
     two_sigmoids(r, i, sr, g.si);
-    const float E = expm1_neg<false>(k * sr);
-    g.a = 1.f + E;
-    const float m2 = -E * (2.f + E);
-    g.m = m2 * rsqrt_approx(m2 < 1e-36f ? 1e-36f : m2);
+    const float F = forget(k * sr);
+    g.a = 1.f - F;
+    const float m2 = fmaf(F, g.a, F) + 1e-36f;
+    g.m = m2 * rsqrt_approx(m2);
     return g;
 }
 
@@ -109,10 +105,10 @@ using tc::f2_add;
 using tc::f2_fma;
 using tc::f2_mul;
 using tc::f2_pack;
+using tc::f2_sub;
 using tc::f2_unpack;
 
 __device__ __forceinline__ f2 f2_both(float v) { return f2_pack(v, v); }
-__device__ __forceinline__ f2 f2_neg(f2 v) { return v ^ 0x8000000080000000ull; }
 
 struct Gate2 {
     f2 sr, si;  // sigmoids
@@ -134,35 +130,37 @@ __device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si) {
     sr = f2_mul(q, R);
     si = f2_mul(p, R);
 }
+// F = 1 - exp(-q), q = -log a >= 0.
 template <bool FAST>
-__device__ __forceinline__ f2 expm1_neg2(f2 s) {
+__device__ __forceinline__ f2 forget2(f2 q) {
     f2 p = f2_both(1.f / 120.f);
-    p = f2_fma(p, s, f2_both(1.f / 24.f));
-    p = f2_fma(p, s, f2_both(1.f / 6.f));
-    p = f2_fma(p, s, f2_both(0.5f));
-    p = f2_fma(p, s, f2_both(1.f));
-    const f2 series = f2_mul(s, p);
+    p = f2_fma(p, q, f2_both(-1.f / 24.f));
+    p = f2_fma(p, q, f2_both(1.f / 6.f));
+    p = f2_fma(p, q, f2_both(-0.5f));
+    p = f2_fma(p, q, f2_both(1.f));
+    const f2 series = f2_mul(q, p);
     if (FAST) return series;
-    float e0, e1, s0, s1;
-    f2_unpack(series, e0, e1);
-    f2_unpack(s, s0, s1);
-    return f2_pack(s0 >= kSeries ? e0 : tc::fast_exp2(s0 * kLog2e) - 1.f,
-                   s1 >= kSeries ? e1 : tc::fast_exp2(s1 * kLog2e) - 1.f);
+    float f0, f1, q0, q1;
+    f2_unpack(series, f0, f1);
+    f2_unpack(q, q0, q1);
+    return f2_pack(q0 <= kSeries ? f0 : 1.f - tc::fast_exp2(-q0 * kLog2e),
+                   q1 <= kSeries ? f1 : 1.f - tc::fast_exp2(-q1 * kLog2e));
 }
-// a, m and 1 / m from E = a - 1: m^2 = -E (1 + a) = -(E + E a).
-__device__ __forceinline__ void decay_from2(f2 E, Gate2 &g) {
-    g.a = f2_add(f2_both(1.f), E);
+// a, m and 1 / m from F = 1 - a: m^2 = F (1 + a) = F + F a, kept off zero by
+// 1e-36 (m = 1e-18 where a = 1).
+__device__ __forceinline__ void decay_from2(f2 F, Gate2 &g) {
+    g.a = f2_sub(f2_both(1.f), F);
+    const f2 m2 = f2_add(f2_fma(F, g.a, F), f2_both(1e-36f));
     float lo, hi;
-    f2_unpack(f2_fma(E, g.a, E), lo, hi);
-    const float l = fmaxf(-lo, 1e-36f), h = fmaxf(-hi, 1e-36f);
-    g.rm = f2_pack(rsqrt_approx(l), rsqrt_approx(h));
-    g.m = f2_mul(f2_pack(-lo, -hi), g.rm);
+    f2_unpack(m2, lo, hi);
+    g.rm = f2_pack(rsqrt_approx(lo), rsqrt_approx(hi));
+    g.m = f2_mul(m2, g.rm);
 }
 template <bool FAST>
 __device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
     Gate2 g;
     two_sigmoids2(r, i, g.sr, g.si);
-    decay_from2(expm1_neg2<FAST>(f2_mul(k, g.sr)), g);
+    decay_from2(forget2<FAST>(f2_mul(k, g.sr)), g);
     return g;
 }
 

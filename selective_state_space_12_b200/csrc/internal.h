@@ -143,7 +143,8 @@ struct GatedArgs {
     const float *first = nullptr;  // h0, or dh_final
     float *last = nullptr;         // h_final, or dh0
     float *dlam_part = nullptr;    // (b, nb, D)
-    float *scale = nullptr;        // (D): -c softplus(lam)
+    float *scale = nullptr;        // (D): c softplus(lam)
+    bool words = false;            // input tensors start on 4 bytes
     unsigned *counter = nullptr, *abort = nullptr, *err = nullptr;
     unsigned long long *ends = nullptr, *maps = nullptr;  // what tiles publish
     long long wait = 0;
