@@ -14,18 +14,29 @@
 // with a_{t+1} G_{t+1} as what a tile receives from its right; the states
 // before its tokens it recomputes from the saved one, at the tile's start.
 //
-// Looking back. Tiles are handed out by a counter, all channels of a block of
-// tokens before the next block, so that whoever holds a tile knows that the
-// tiles before it are done or held by a running thread block. A ninth warp
-// folds the maps of a tile's eight runs. If the tile before has published what
-// leaves it, that is what enters; if not, the warp publishes its own (P, H),
-// and waits for some tile among the kWindow before it that has published its
-// end, all between them their (P, H), and folds these in order. What enters a
-// tile is the same fold whichever tile it starts from: results do not depend on
-// the timing. A published word is 64 bits, cleared to all ones before the
-// kernel, and is complete once it differs from that: readers poll the data
-// itself, one trip to L2, and no fence stands between data and flag. Waits are
-// bounded; one that runs out tells the others and all return.
+// Tiles are handed out by a counter, all channels of a block of tokens before
+// the next block, so that whoever holds a tile knows that the tiles before it
+// are done or held by a running thread block; a ninth warp folds the maps of a
+// tile's eight runs and finds what enters the tile. There are two ways, by the
+// number of lanes (batch times tiles of channels), each with one fixed order of
+// sums:
+//
+//  - many lanes (at least one for each thread block): a tile waits for what
+//    leaves the tile before, which was handed out a whole round earlier and is
+//    hardly ever late. Thread blocks hold a ticket ahead, so that the next
+//    tile's inputs arrive meanwhile.
+//  - few lanes: thread blocks work on many consecutive tiles of a lane at once,
+//    and a chain of waits from tile to tile would be the whole time (0.4 us a
+//    step). Tiles form groups of kGroup; each publishes its (P, H), folds those
+//    before it in its group, and waits only for what leaves the group before,
+//    so the chain has one step a group. A ticket held ahead could then block
+//    the chain behind its holder's wait, so none is: the inputs that the next
+//    round of tiles needs are brought to L2 instead.
+//
+// A published word is 64 bits, cleared to all ones before the kernel, and is
+// complete once it differs from that: readers poll the data itself, and no
+// fence stands between data and flag. Waits are bounded; one that runs out
+// tells the others and all return.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -43,10 +54,10 @@ constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;    // and the one that folds and looks back
 constexpr int kRun = kBlock / kWarps;  // tokens of a warp
 constexpr int kTileCh = 64;            // channels of a tile, two a lane
-constexpr int kWindow = 4;             // tiles that a look reaches back
+constexpr int kGroup = 8;              // consecutive tiles that fold each other's maps
 
 // Barriers of the compute warps and the chain warp.
-enum { kMapsReady = 1, kEntryReady = 2 };
+enum { kMapsReady = 1, kEntryReady = 2, kTicketReady = 3 };
 __device__ __forceinline__ void bar_sync(int id) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
 }
@@ -241,6 +252,35 @@ struct Stage {
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
+    // Without tickets ahead: brings the rows of the tile that comes one round of
+    // thread blocks later to L2, whoever will take it.
+    __device__ __forceinline__ void prefetch(const GatedArgs &a, const Maps &maps, unsigned tiles,
+                                             const Tile &now, const void *const (&src)[TENSORS],
+                                             bool back) const {
+        const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
+        const unsigned later = (unsigned)now.id + gridDim.x;
+        if (later >= tiles || later < gridDim.x) return;
+        const Tile t = back ? tile_of<true>(a, later) : tile_of<false>(a, later);
+        if constexpr (ALIGNED) {
+            if (lane == 0 && tok0 < t.n) {
+#pragma unroll
+                for (int w = 0; w < TENSORS; ++w)
+                    tc::tma_prefetch_l2_4d(&maps.m[w], t.d0, (int)(t.blk * kBlock) + tok0, (int)t.b, 0);
+            }
+        } else {
+            const int w = lane / kRun, j = lane % kRun;
+            if (w < TENSORS && tok0 + j < t.n) {
+                const T *row = nullptr;
+#pragma unroll
+                for (int v = 0; v < TENSORS; ++v)
+                    if (v == w) row = static_cast<const T *>(src[v]);
+                row += t.row0 + (tok0 + j) * a.D + t.d0;
+                const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
+                for (int c = 0; c < len; c += 64 / (int)sizeof(T))
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+            }
+        }
+    }
     static __device__ __forceinline__ void copy4(void *to, const void *from) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from)
                      : "memory");
@@ -308,61 +348,72 @@ __device__ __forceinline__ float4 then(float4 first, float4 next) {
                        chain_decay(first.z, next.z), carry_on(next.z, first.w, next.w));
 }
 
-// What enters tile `id`, the step-th of its lane (step > 0), for this lane's
-// channels, `before` the word of the tile before as read earlier. False when a
-// wait ran out (here or elsewhere).
-__device__ __forceinline__ bool look_back(const GatedArgs &a, int64_t id, unsigned step,
-                                          int64_t lanes, float4 map, word before, f2 &in) {
-    const int lane = threadIdx.x & 31;
-    bool done = before != kEmpty;
-    in = before;
-    if (__all_sync(0xffffffffu, done)) return true;
-    store_word(&a.maps[(id * 32 + lane) * 2], map.x, map.y);
-    store_word(&a.maps[(id * 32 + lane) * 2 + 1], map.z, map.w);
-    const long long began = clock64();
-    while (true) {
-        word e[kWindow], m0[kWindow - 1], m1[kWindow - 1];
-#pragma unroll
-        for (int j = 0; j < kWindow; ++j) {
-            const int64_t at = (id - (j + 1) * lanes) * 32 + lane;
-            e[j] = (unsigned)j < step ? load_word(&a.ends[at]) : kEmpty;
-            if (j + 1 < kWindow) {
-                m0[j] = (unsigned)j < step ? load_word(&a.maps[at * 2]) : kEmpty;
-                m1[j] = (unsigned)j < step ? load_word(&a.maps[at * 2 + 1]) : kEmpty;
-            }
-        }
-        if (!done) {
-            int from = kWindow;  // the nearest tile with an end, and maps up to it
-#pragma unroll
-            for (int j = kWindow - 1; j >= 0; --j) {
-                if (e[j] != kEmpty) from = j;
-                else if (j + 1 < kWindow && (m0[j] == kEmpty || m1[j] == kEmpty)) from = kWindow;
-            }
-            if (from < kWindow) {
-                done = true;
-#pragma unroll
-                for (int j = kWindow - 1; j >= 0; --j) {
-                    if (j == from) in = e[j];
-                    if (j + 1 < kWindow && j < from) {
-                        float4 m;
-                        f2_unpack(m0[j], m.x, m.y);
-                        f2_unpack(m1[j], m.z, m.w);
-                        in = apply(m, in);
-                    }
-                }
-            }
-        }
-        if (__all_sync(0xffffffffu, done)) return true;
+// A bounded wait of the chain warp: false once it, or another thread block's,
+// has run out.
+struct Patience {
+    long long began = 0;
+    int polls = 0;
+    __device__ __forceinline__ bool more(const GatedArgs &a) {
+        if (polls == 0) began = clock64();
         bool stop = false;
-        if (lane == 0) {
-            stop = clock64() - began > a.wait || load_relaxed(a.abort) != 0;
+        if ((threadIdx.x & 31) == 0) {
+            stop = clock64() - began > a.wait || ((polls & 15) == 15 && load_relaxed(a.abort) != 0);
             if (stop) {
                 atomicExch(a.err, 0x6a7ed001u);
                 atomicExch(a.abort, 1u);
             }
         }
-        if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+        ++polls;
+        return !__shfl_sync(0xffffffffu, stop, 0);
     }
+};
+
+// The word of each lane once it is there; false when the wait ran out.
+__device__ __forceinline__ bool await(const GatedArgs &a, const word *p, word &v) {
+    if (__all_sync(0xffffffffu, v != kEmpty)) return true;
+    Patience wait;
+    while (true) {
+        v = load_word(p);
+        if (__all_sync(0xffffffffu, v != kEmpty)) return true;
+        if (!wait.more(a)) return false;
+    }
+}
+
+// The composed map of the `count` tiles before tile `id` in its group.
+__device__ __forceinline__ bool group_map(const GatedArgs &a, int64_t id, int count, int64_t lanes,
+                                          float4 &map) {
+    const int lane = threadIdx.x & 31;
+    map = make_float4(1.f, 0.f, 1.f, 0.f);
+    Patience wait;
+    constexpr int kBatch = 4;
+    for (int first = 0; first < count; first += kBatch) {
+        while (true) {
+            word m0[kBatch], m1[kBatch];
+            bool there = true;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const bool has = first + j < count;
+                const word *at = &a.maps[((id - (count - first - j) * lanes) * 32 + lane) * 2];
+                m0[j] = has ? load_word(at) : 0;
+                m1[j] = has ? load_word(at + 1) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) there = there && m0[j] != kEmpty && m1[j] != kEmpty;
+            if (__all_sync(0xffffffffu, there)) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+                    if (first + j < count) {
+                        float4 m;
+                        f2_unpack(m0[j], m.x, m.y);
+                        f2_unpack(m1[j], m.z, m.w);
+                        map = then(map, m);
+                    }
+                break;
+            }
+            if (!wait.more(a)) return false;
+        }
+    }
+    return true;
 }
 
 template <bool ALIGNED>
@@ -384,7 +435,6 @@ struct Shared {
     float2 right[kWarps][32];  // backward: R of each run
     f2 entry[kWarps][32];      // the state entering each run
     f2 grad[kWarps][32];       // backward: the gradient entering it from its right
-    float k[2][kTileCh];       // c softplus(lam), of this and the next tile
     float dlam[2][kWarps][kTileCh];
     unsigned top[2][3][kTileCh];  // 8-bit copies: largest magnitudes
     unsigned code[3][kTileCh];
@@ -393,13 +443,10 @@ struct Shared {
     int stop[2];
 };
 
+// k = c softplus(lam) of the lane's channels
 template <bool ALIGNED>
-__device__ __forceinline__ void gate_scales(const GatedArgs &a, int d0, float *k) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int c = channel<ALIGNED>(j);
-        k[c] = d0 + c < a.D ? a.scale[d0 + c] : 0.f;
-    }
+__device__ __forceinline__ f2 gate_scales(const GatedArgs &a, int d0) {
+    return read_state<ALIGNED>(a.scale, 0, d0, a.D);
 }
 // A wait of a compute warp ran out.
 __device__ __forceinline__ void give_up(const GatedArgs &a, int *stop) {
@@ -457,15 +504,18 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         const Tile t = tile_of<BACK>(a, now);
         const unsigned step = (unsigned)(BACK ? a.nb - 1 - t.blk : t.blk);
         unsigned after = tiles;
-        if (next < tiles) {
+        if (a.eager && next < tiles) {
             if (lane == 0) after = atomicAdd(a.counter, 1u);
-            gate_scales<ALIGNED>(a, tile_of<BACK>(a, next).d0, s.k[(n + 1) & 1]);
             after = __shfl_sync(0xffffffffu, after, 0);
         }
+        const int pos = (int)(step % kGroup);
+        const bool leaves = a.eager || pos == kGroup - 1;  // publishes what leaves it
+        const bool waits = a.eager ? step > 0 : step >= kGroup;
+        const int64_t slot = a.eager ? t.id : (int64_t)(step / kGroup) * lanes + t.id % lanes;
         f2 in = 0, h = 0;
         word before = kEmpty;
-        if (step == 0) in = read_state<ALIGNED>(a.first, t.b * a.D, t.d0, a.D);
-        else before = load_word(&a.ends[(t.id - lanes) * 32 + lane]);
+        if (waits) before = load_word(&a.ends[(slot - lanes) * 32 + lane]);
+        else in = read_state<ALIGNED>(a.first, t.b * a.D, t.d0, a.D);
         if (BACK) h = read_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D);
         bar_sync(kMapsReady);
         if (s.stop[n & 1]) {
@@ -488,17 +538,31 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         float4 all = m[BACK ? kWarps - 1 : 0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = then(all, m[BACK ? kWarps - 1 - w : w]);
-        if (step > 0 && !look_back(a, t.id, step, lanes, all, before, in)) {
+        bool ok = true;
+        if (chained && !a.eager) {
+            if (pos < kGroup - 1 && step + 1 < a.nb) {
+                store_word(&a.maps[(t.id * 32 + lane) * 2], all.x, all.y);
+                store_word(&a.maps[(t.id * 32 + lane) * 2 + 1], all.z, all.w);
+            }
+            float4 ahead;
+            ok = group_map(a, t.id, pos, lanes, ahead);
+            if (ok && waits) ok = await(a, &a.ends[(slot - lanes) * 32 + lane], before);
+            in = apply(ahead, waits ? before : in);
+        } else if (waits) {
+            ok = await(a, &a.ends[(slot - lanes) * 32 + lane], before);
+            in = before;
+        }
+        if (!ok) {
             if (lane == 0) s.stop[n & 1] = 1;
             __syncwarp();
             bar_arrive(kEntryReady);
             return;
         }
         const f2 out = apply(all, in);
-        if (chained && step + 1 < a.nb) {
+        if (chained && leaves && step + 1 < a.nb) {
             float2 e;
             f2_unpack(out, e.x, e.y);
-            store_word(&a.ends[t.id * 32 + lane], e.x, e.y);
+            store_word(&a.ends[slot * 32 + lane], e.x, e.y);
         }
         f2 run = in;
 #pragma unroll
@@ -520,9 +584,14 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
                         a.e[((w * a.batch + t.b) * a.nb + t.blk) * a.D + t.d0 + c] = (uint8_t)code;
                 }
         }
-        if (lane == 0) s.ticket[n & 1] = after;
+        if (a.eager && lane == 0) s.ticket[n & 1] = after;
         __syncwarp();
         bar_arrive(kEntryReady);
+        if (chained && !a.eager) {
+            if (lane == 0) s.ticket[0] = next = atomicAdd(a.counter, 1u);
+            next = __shfl_sync(0xffffffffu, next, 0);
+            bar_arrive(kTicketReady);
+        }
         if (!BACK && a.states)
             write_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D, in);
         if (a.last && step + 1 == a.nb) write_state<ALIGNED>(a.last, t.b * a.D, t.d0, a.D, out);
@@ -537,14 +606,14 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
     }
 }
 
-// The first two tickets of this thread block, its barriers and first gate scales.
+// The first tickets of this thread block, and its barriers.
 template <bool ALIGNED, bool BACK>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
     if (threadIdx.x == 0) {
         s.stop[0] = s.stop[1] = 0;
         if (a.nb > 1) {
             s.ticket[0] = atomicAdd(a.counter, 1u);
-            s.ticket[1] = atomicAdd(a.counter, 1u);
+            s.ticket[1] = a.eager ? atomicAdd(a.counter, 1u) : tiles;
         } else {  // one block of tokens: a tile a thread block
             s.ticket[0] = blockIdx.x;
             s.ticket[1] = tiles;
@@ -553,9 +622,6 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
         tc::fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 2 * 3 * kTileCh; i += kThreads) (&s.top[0][0][0])[i] = 0;
-    __syncthreads();
-    if (threadIdx.x >= kCompute && s.ticket[0] < tiles)
-        gate_scales<ALIGNED>(a, tile_of<BACK>(a, s.ticket[0]).d0, s.k[0]);
     __syncthreads();
 }
 
@@ -587,10 +653,11 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
     Tile t = tile_of<false>(a, s.ticket[0]);
     in.request(a, maps, t, src);
     unsigned mark = reset_byte(a, t);
+    f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
+    const bool chained = a.nb > 1;
     bool ahead = false;  // copies are on their way
     for (int n = 0;; ++n) {
-        const f2 k = f2_pack(s.k[n & 1][channel<ALIGNED>(0)], s.k[n & 1][channel<ALIGNED>(1)]);
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
         const bool plain = all_fast(k) && marks == 0 && left >= kRun;
@@ -646,17 +713,21 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
         bar_arrive(kMapsReady);
         Tile tn = t;
         ahead = here && next < tiles;
-        if (ahead) {  // the next tile's inputs are on their way while this one waits
+        f2 kn = k;
+        auto advance = [&] {  // the next tile's inputs are on their way while this one waits
             tn = tile_of<false>(a, next);
             in.request(a, maps, tn, src);
             mark = reset_byte(a, tn);
-        }
+            kn = gate_scales<ALIGNED>(a, tn.d0);
+        };
+        if (ahead) advance();
+        else if (chained && !a.eager) in.prefetch(a, maps, tiles, t, src, false);
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
             if (!here) in.wait(a.wait);
             break;
         }
-        const unsigned after = s.ticket[n & 1];
+        const unsigned after = a.eager ? s.ticket[n & 1] : tiles;
         f2 h = s.entry[warp][lane];
         const Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
         if (plain) {
@@ -694,8 +765,15 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
                 }
             }
         }
+        if (chained && !a.eager) {
+            bar_sync(kTicketReady);
+            next = s.ticket[0];
+            ahead = next < tiles;
+            if (ahead) advance();
+        }
         if (!ahead) break;
         t = tn;
+        k = kn;
         next = after;
     }
     if (ahead) in.wait(a.wait);  // nothing may be in flight to shared memory at the end
@@ -750,11 +828,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     Tile t = tile_of<true>(a, s.ticket[0]);
     in.request(a, maps, t, src);
     unsigned mark = reset_byte(a, t);
+    f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
     const f2 none = f2_both(0.f), one = f2_both(1.f);
+    const bool chained = a.nb > 1;
     bool ahead = false;
     for (int n = 0;; ++n) {
-        const f2 k = f2_pack(s.k[n & 1][channel<ALIGNED>(0)], s.k[n & 1][channel<ALIGNED>(1)]);
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
         const bool plain = all_fast(k) && marks == 0 && left >= kRun;
@@ -814,17 +893,21 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         bar_arrive(kMapsReady);
         Tile tn = t;
         ahead = here && next < tiles;
-        if (ahead) {
+        f2 kn = k;
+        auto advance = [&] {
             tn = tile_of<true>(a, next);
             in.request(a, maps, tn, src);
             mark = reset_byte(a, tn);
-        }
+            kn = gate_scales<ALIGNED>(a, tn.d0);
+        };
+        if (ahead) advance();
+        else if (chained && !a.eager) in.prefetch(a, maps, tiles, t, src, true);
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
             if (!here) in.wait(a.wait);
             break;
         }
-        const unsigned after = s.ticket[n & 1];
+        const unsigned after = a.eager ? s.ticket[n & 1] : tiles;
         f2 dl = none;
         auto grads = [&](auto run) {
             constexpr bool kPlain = decltype(run)::value;
@@ -873,11 +956,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         f2_unpack(dl, dw.x, dw.y);
         s.dlam[n & 1][warp][channel<ALIGNED>(0)] = dw.x;
         s.dlam[n & 1][warp][channel<ALIGNED>(1)] = dw.y;
+        if (chained && !a.eager) {
+            bar_sync(kTicketReady);
+            next = s.ticket[0];
+            ahead = next < tiles;
+            if (ahead) advance();
+        }
         if (!ahead) {
             bar_arrive(kMapsReady);  // the chain warp takes the last tile's dlam
             break;
         }
         t = tn;
+        k = kn;
         next = after;
     }
     if (ahead) in.wait(a.wait);
@@ -916,35 +1006,39 @@ __global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x
 
 // Clears the words that tiles publish and the counter, and prepares the gate
 // scales k = c softplus(lam).
-__global__ void gated_open_kernel(const GatedArgs a, int64_t words) {
+__global__ void gated_open_kernel(const GatedArgs a, int64_t ends, int64_t maps) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i == 0) *a.counter = *a.abort = 0;
     if (i < a.D) a.scale[i] = a.c * softplus_full(a.lam[i]);
-    // ends and maps are neighbours, each a multiple of 16 bytes
-    if (2 * i < words) reinterpret_cast<ulonglong2 *>(a.ends)[i] = make_ulonglong2(kEmpty, kEmpty);
+    const ulonglong2 empty = make_ulonglong2(kEmpty, kEmpty);
+    if (2 * i < ends) reinterpret_cast<ulonglong2 *>(a.ends)[i] = empty;
+    if (2 * i < maps) reinterpret_cast<ulonglong2 *>(a.maps)[i] = empty;
 }
 
 // Thread blocks of a persistent kernel: as many as fit, fewer where there are
 // fewer tiles; with one block of tokens one per tile.
 template <typename F>
-cudaError_t start(const char *name, F *kernel, size_t smem, const GatedArgs &a, const Maps &maps,
+cudaError_t start(const char *name, F *kernel, size_t smem, GatedArgs a, const Maps &maps,
                   cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     int per_sm = 1, dev = 0, sms = 0;
-    const int64_t tiles = a.batch * a.dblocks * a.nb;
-    int64_t grid = tiles;
-    const int64_t words = a.nb > 1 ? tiles * 32 * 3 : 0;
+    const int64_t lanes = a.batch * a.dblocks, tiles = lanes * a.nb;
+    int64_t grid = tiles, ends = 0, words = 0;
     if (e == cudaSuccess && a.nb > 1) {
         if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
             (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
         if (e == cudaSuccess && (int64_t)per_sm * sms < grid) grid = (int64_t)per_sm * sms;
+        a.eager = lanes >= grid;
+        ends = (a.eager ? tiles : lanes * (a.nb / kGroup)) * 32;
+        words = a.eager ? 0 : tiles * 64;
     }
     if (e != cudaSuccess) return e;
-    const int64_t n = words / 2 > a.D ? words / 2 : a.D;
+    int64_t n = ends > words ? ends / 2 : words / 2;
+    if (n < a.D) n = a.D;
     launch_begin("gated_open", st);
-    gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, words);
+    gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, ends, words);
     launch_end(st);
     launch_begin(name, st);
     kernel<<<(unsigned)grid, kThreads, smem, st>>>(a, maps);
