@@ -86,23 +86,27 @@ __device__ __forceinline__ unsigned load_relaxed(const unsigned *p) {
     return v;
 }
 
-struct Tile {
-    int64_t b, blk, row0;  // row0: offset of (b, first token, 0) in a (b, L, D) tensor
-    int64_t id;            // index of its record
-    int d0, n;             // first channel, tokens
+struct __align__(16) Tile {
+    int64_t row0;  // offset of (b, first token, 0) in a (b, L, D) tensor
+    int64_t blocks0;  // and of (b, blk, 0) in a (b, nb, D) one
+    int b, blk, d0, n;  // batch, block of tokens, first channel, tokens
+    unsigned id;   // its ticket, and the index of its record
+    bool last;     // of the tensor
 };
 template <bool BACK>
 __device__ __forceinline__ Tile tile_of(const GatedArgs &a, unsigned ticket) {
     Tile t;
     const unsigned lanes = (unsigned)(a.batch * a.dblocks);
     const unsigned step = ticket / lanes, lane = ticket % lanes;
-    t.b = lane / (unsigned)a.dblocks;
+    t.b = (int)(lane / (unsigned)a.dblocks);
     t.d0 = (int)(lane % (unsigned)a.dblocks) * kTileCh;
-    t.blk = BACK ? a.nb - 1 - step : step;
-    t.row0 = (t.b * a.L + t.blk * kBlock) * a.D;
-    const int64_t left = a.L - t.blk * kBlock;
+    t.blk = (int)(BACK ? a.nb - 1 - step : step);
+    t.row0 = (t.b * a.L + (int64_t)t.blk * kBlock) * a.D;
+    t.blocks0 = (t.b * a.nb + t.blk) * a.D;
+    const int64_t left = a.L - (int64_t)t.blk * kBlock;
     t.n = (int)(left < kBlock ? left : kBlock);
     t.id = ticket;
+    t.last = t.b == a.batch - 1 && t.blk == a.nb - 1 && t.d0 + kTileCh >= a.D;
     return t;
 }
 
@@ -131,7 +135,18 @@ __device__ __forceinline__ f2 widen(float2 v) { return f2_pack(v.x, v.y); }
 __device__ __forceinline__ f2 widen(uint32_t v) {
     return f2_pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
-__device__ __forceinline__ f2 widen(char2 v) { return f2_pack((float)v.x, (float)v.y); }
+template <>
+struct Pair<int8_t> {
+    using type = uint16_t;
+};
+// int8 -> float without the (special-function unit's) conversion: the byte
+// plus 128 in the low bits of 2^23.
+__device__ __forceinline__ f2 widen(uint16_t v) {
+    const uint32_t u = v ^ 0x8080u;
+    return f2_sub(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)),
+                          __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441))),
+                  f2_both(8388736.f));
+}
 
 // An output's rows for this lane: stores its two channels of one token.
 template <typename T, bool ALIGNED>
@@ -164,10 +179,10 @@ struct Rows {
 // memory a tile ahead and waits for nobody else's. Where rows are 16-byte
 // aligned, one TMA load a tensor does it, counted by the warp's own barrier;
 // past the last token and channel it fills zeros. Elsewhere the lanes copy the
-// 4-byte words that cover each row (33 for bf16 rows that start inside one)
+// 4-byte words that cover each row (one more for a row that starts inside one)
 // asynchronously, and read from the row's place in them. Words that may leave
-// the tensor (the last tile's; a bf16 tensor that starts inside a word) are
-// replaced by plain loads.
+// the tensor (the last tile's; a tensor that starts inside a word) are replaced
+// by plain loads. T is the I/O type, or int8 for 8-bit copies.
 struct Maps {
     CUtensorMap m[4];
 };
@@ -186,7 +201,8 @@ struct Stage {
     __device__ __forceinline__ Stage(unsigned char *all, uint64_t *bars)
         : buf(all + (threadIdx.x >> 5) * kWarpBytes), bar(bars + (threadIdx.x >> 5)), parity(0) {}
 
-    __device__ __forceinline__ void request(const GatedArgs &a, const Maps &maps, const Tile &t,
+    __device__ __forceinline__ void request(const GatedArgs &a, const CUtensorMap *maps,
+                                            const Tile &t,
                                             const void *const (&src)[TENSORS]) const {
         const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
         __syncwarp();  // the rows have been read
@@ -197,15 +213,14 @@ struct Stage {
                 if (any) {
 #pragma unroll
                     for (int w = 0; w < TENSORS; ++w)
-                        tc::tma_load_4d(buf + w * kRun * kPitch, &maps.m[w], bar, t.d0,
-                                        (int)(t.blk * kBlock) + tok0, (int)t.b, 0);
+                        tc::tma_load_4d(buf + w * kRun * kPitch, maps + w, bar, t.d0,
+                                        t.blk * kBlock + tok0, t.b, 0);
                 }
             }
         } else {
             const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
-            const bool last = t.b == a.batch - 1 && t.blk == a.nb - 1 && t.d0 + kTileCh >= a.D;
             const int64_t row0 = t.row0 + (int64_t)tok0 * a.D + t.d0;
-            if (sizeof(T) == 4 || last || !a.words) {
+            if (sizeof(T) == 4 || t.last || !a.words) {
 #pragma unroll
                 for (int w = 0; w < TENSORS; ++w)
 #pragma unroll
@@ -224,29 +239,33 @@ struct Stage {
                         }
                     }
             } else {
+                constexpr int kE = (int)sizeof(T), kWords = kTileCh * kE / 4;  // 32 or 16
+                constexpr int kRows = 32 / kWords;                             // a copy of all lanes
 #pragma unroll
                 for (int w = 0; w < TENSORS; ++w) {
-                    const uintptr_t row = reinterpret_cast<uintptr_t>(src[w]) + 2 * row0;
+                    const uintptr_t row = reinterpret_cast<uintptr_t>(src[w]) + kE * row0;
 #pragma unroll
-                    for (int j = 0; j < kRun; ++j) {
-                        if (tok0 + j >= t.n) break;
-                        const uintptr_t r = row + 2 * (uintptr_t)(j * a.D);
-                        const int words = ((int)(r & 3) + 2 * len + 3) / 4;
-                        if (lane < words)
-                            copy4(buf + (w * kRun + j) * kPitch + 4 * lane,
-                                  reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * lane));
+                    for (int j0 = 0; j0 < kRun; j0 += kRows) {
+                        const int j = j0 + lane / kWords, i = lane % kWords;
+                        if (tok0 + j0 >= t.n) break;
+                        const uintptr_t r = row + kE * (uintptr_t)(j * a.D);
+                        const int words = ((int)(r & 3) + kE * len + 3) / 4;
+                        if (i < words && tok0 + j < t.n)
+                            copy4(buf + (w * kRun + j) * kPitch + 4 * i,
+                                  reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * i));
                     }
                 }
-                // the 33rd words: lane w kRun + j
+                // the words after these: lane w kRun + j
                 const int w = lane / kRun, j = lane % kRun;
                 if (w < TENSORS && tok0 + j < t.n) {
                     uintptr_t row = 0;
 #pragma unroll
                     for (int v = 0; v < TENSORS; ++v)
-                        if (v == w) row = reinterpret_cast<uintptr_t>(src[v]) + 2 * (row0 + j * a.D);
-                    if ((int)(row & 3) + 2 * len > 128)
-                        copy4(buf + lane * kPitch + 128,
-                              reinterpret_cast<const void *>((row & ~uintptr_t(3)) + 128));
+                        if (v == w)
+                            row = reinterpret_cast<uintptr_t>(src[v]) + kE * (row0 + j * a.D);
+                    if ((int)(row & 3) + kE * len > 4 * kWords)
+                        copy4(buf + lane * kPitch + 4 * kWords,
+                              reinterpret_cast<const void *>((row & ~uintptr_t(3)) + 4 * kWords));
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -254,18 +273,16 @@ struct Stage {
     }
     // Without tickets ahead: brings the rows of the tile that comes one round of
     // thread blocks later to L2, whoever will take it.
-    __device__ __forceinline__ void prefetch(const GatedArgs &a, const Maps &maps, unsigned tiles,
-                                             const Tile &now, const void *const (&src)[TENSORS],
-                                             bool back) const {
+    __device__ __forceinline__ void prefetch(const GatedArgs &a, const CUtensorMap *maps,
+                                             unsigned tiles, const Tile &t,
+                                             const void *const (&src)[TENSORS]) const {
         const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
-        const unsigned later = (unsigned)now.id + gridDim.x;
-        if (later >= tiles || later < gridDim.x) return;
-        const Tile t = back ? tile_of<true>(a, later) : tile_of<false>(a, later);
+        if (t.id >= tiles) return;
         if constexpr (ALIGNED) {
             if (lane == 0 && tok0 < t.n) {
 #pragma unroll
                 for (int w = 0; w < TENSORS; ++w)
-                    tc::tma_prefetch_l2_4d(&maps.m[w], t.d0, (int)(t.blk * kBlock) + tok0, (int)t.b, 0);
+                    tc::tma_prefetch_l2_4d(maps + w, t.d0, t.blk * kBlock + tok0, t.b, 0);
             }
         } else {
             const int w = lane / kRun, j = lane % kRun;
@@ -315,9 +332,11 @@ struct Stage {
                          (threadIdx.x & 31);
             if constexpr (sizeof(T) == 4)
                 return make_float2(v[0], v[32]);
-            else
+            else if constexpr (sizeof(T) == 2)
                 return (uint32_t)__bfloat16_as_ushort(v[0]) |
                        (uint32_t)__bfloat16_as_ushort(v[32]) << 16;
+            else
+                return (uint16_t)((uint8_t)v[0] | (uint16_t)(uint8_t)v[32] << 8);
         }
     }
 };
@@ -326,7 +345,7 @@ struct Stage {
 __device__ __forceinline__ unsigned reset_byte(const GatedArgs &a, const Tile &t) {
     const int lane = threadIdx.x & 31, tok = (threadIdx.x >> 5) * kRun + lane;
     if (!a.reset || lane >= kRun || tok >= t.n) return 0;
-    return a.reset[t.b * a.L + t.blk * kBlock + tok];
+    return a.reset[(int64_t)t.b * a.L + (int64_t)t.blk * kBlock + tok];
 }
 
 // ------------------------------------------------------------ folding
@@ -436,10 +455,11 @@ struct Shared {
     f2 entry[kWarps][32];      // the state entering each run
     f2 grad[kWarps][32];       // backward: the gradient entering it from its right
     float dlam[2][kWarps][kTileCh];
-    unsigned top[2][3][kTileCh];  // 8-bit copies: largest magnitudes
+    uint2 top[3][kWarps][32];  // 8-bit copies: largest magnitudes of each run
     unsigned code[3][kTileCh];
-    uint64_t bars[kWarps];
-    unsigned ticket[2];        // of this and the next tile
+    uint64_t bars[2 * kWarps];
+    Tile tile[2];              // this thread block's next tiles
+    Tile later;                // without tickets ahead: one to bring to L2
     int stop[2];
 };
 
@@ -472,22 +492,55 @@ __device__ __forceinline__ uint32_t step_code(uint32_t bits) {
     const int code = (int)E - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);
     return code < 1 ? 1u : (uint32_t)code;
 }
-__device__ __forceinline__ int8_t in_steps(float v, uint32_t code) {
-    return code == 255 ? 0 : (int8_t)__float2int_rn(v * __uint_as_float((254u - code) << 23));
+// The largest magnitudes of a pair of channels, as bits.
+template <typename T>
+struct Largest;
+template <>
+struct Largest<float> {
+    uint2 m = {0, 0};
+    __device__ __forceinline__ void add(float2 v) {
+        m.x = max(m.x, __float_as_uint(v.x) & 0x7fffffffu);
+        m.y = max(m.y, __float_as_uint(v.y) & 0x7fffffffu);
+    }
+    __device__ __forceinline__ void join(const Largest &o) {
+        m.x = max(m.x, o.m.x);
+        m.y = max(m.y, o.m.y);
+    }
+    __device__ __forceinline__ uint32_t bits(int j) const { return j ? m.y : m.x; }
+};
+template <>
+struct Largest<__nv_bfloat16> {
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(uint32_t v) { m = __vmaxu2(m, v & 0x7fff7fffu); }
+    __device__ __forceinline__ void join(const Largest &o) { m = __vmaxu2(m, o.m); }
+    __device__ __forceinline__ uint32_t bits(int j) const { return j ? m & 0xffff0000u : m << 16; }
+};
+
+// Two values as int8 steps, in the low bytes: adding 1.5 2^23 rounds to the
+// nearest step, ties to even, and leaves it in the low byte.
+__device__ __forceinline__ uint32_t in_steps(f2 v, f2 inv, uint32_t keep) {
+    float lo, hi;
+    f2_unpack(f2_fma(v, inv, f2_both(12582912.f)), lo, hi);
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040) & keep;
 }
 
 // ------------------------------------------------------------ chain warp
+
+// The ticket one round of thread blocks on (or none).
+__device__ __forceinline__ unsigned round_on(unsigned ticket) {
+    return ticket + gridDim.x < ticket ? ~0u : ticket + gridDim.x;
+}
 
 // The ninth warp: for each tile of this thread block, folds its runs' maps,
 // finds what enters it, hands every run what enters that, and publishes what
 // leaves. While the others compute a tile it fetches the next ticket and
 // prepares the next tile's gate scales.
-template <bool ALIGNED, bool CK, bool BACK>
+template <typename T, bool ALIGNED, bool CK, bool BACK>
 __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsigned tiles,
                                            int64_t lanes) {
     const int lane = threadIdx.x & 31;
     const bool chained = a.nb > 1;
-    unsigned now = s.ticket[0], next = s.ticket[1];
+    unsigned now = s.tile[0].id, next = s.tile[1].id;
     int64_t last_row = -1;  // dlam of the tile before: its row and channels
     int last_d0 = 0;
     auto flush = [&](int slot) {
@@ -511,12 +564,13 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         const int pos = (int)(step % kGroup);
         const bool leaves = a.eager || pos == kGroup - 1;  // publishes what leaves it
         const bool waits = a.eager ? step > 0 : step >= kGroup;
-        const int64_t slot = a.eager ? t.id : (int64_t)(step / kGroup) * lanes + t.id % lanes;
+        const int64_t slot =
+            a.eager ? t.id : (int64_t)(step / kGroup) * lanes + t.id % (unsigned)lanes;
         f2 in = 0, h = 0;
         word before = kEmpty;
         if (waits) before = load_word(&a.ends[(slot - lanes) * 32 + lane]);
-        else in = read_state<ALIGNED>(a.first, t.b * a.D, t.d0, a.D);
-        if (BACK) h = read_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D);
+        else in = read_state<ALIGNED>(a.first, (int64_t)t.b * a.D, t.d0, a.D);
+        if (BACK) h = read_state<ALIGNED>(a.states, t.blocks0, t.d0, a.D);
         bar_sync(kMapsReady);
         if (s.stop[n & 1]) {
             bar_arrive(kEntryReady);
@@ -573,29 +627,35 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         }
         if (CK && !BACK) {
 #pragma unroll
-            for (int w = 0; w < 3; ++w)
+            for (int w = 0; w < 3; ++w) {
+                Largest<T> top;
+#pragma unroll
+                for (int j = 0; j < kWarps; ++j)
+                    top.join(reinterpret_cast<const Largest<T> *>(s.top[w][j])[lane]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int c = channel<ALIGNED>(j);
-                    const uint32_t code = step_code(s.top[n & 1][w][c]);
+                    const uint32_t code = step_code(top.bits(j));
                     s.code[w][c] = code;
-                    s.top[n & 1][w][c] = 0;
                     if (t.d0 + c < a.D)
-                        a.e[((w * a.batch + t.b) * a.nb + t.blk) * a.D + t.d0 + c] = (uint8_t)code;
+                        a.e[w * a.batch * a.nb * a.D + t.blocks0 + t.d0 + c] = (uint8_t)code;
                 }
+            }
         }
-        if (a.eager && lane == 0) s.ticket[n & 1] = after;
+        if (a.eager && lane == 0) s.tile[n & 1] = tile_of<BACK>(a, after);
         __syncwarp();
         bar_arrive(kEntryReady);
         if (chained && !a.eager) {
-            if (lane == 0) s.ticket[0] = next = atomicAdd(a.counter, 1u);
+            if (lane == 0) next = atomicAdd(a.counter, 1u);
             next = __shfl_sync(0xffffffffu, next, 0);
+            if (lane < 2) (lane ? s.later : s.tile[0]) = tile_of<BACK>(a, lane ? round_on(next) : next);
+            __syncwarp();
             bar_arrive(kTicketReady);
         }
         if (!BACK && a.states)
-            write_state<ALIGNED>(a.states, (t.b * a.nb + t.blk) * a.D, t.d0, a.D, in);
-        if (a.last && step + 1 == a.nb) write_state<ALIGNED>(a.last, t.b * a.D, t.d0, a.D, out);
-        last_row = (t.b * a.nb + t.blk) * a.D;
+            write_state<ALIGNED>(a.states, t.blocks0, t.d0, a.D, in);
+        if (a.last && step + 1 == a.nb) write_state<ALIGNED>(a.last, (int64_t)t.b * a.D, t.d0, a.D, out);
+        last_row = t.blocks0;
         last_d0 = t.d0;
         now = next;
         next = after;
@@ -611,17 +671,14 @@ template <bool ALIGNED, bool BACK>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
     if (threadIdx.x == 0) {
         s.stop[0] = s.stop[1] = 0;
-        if (a.nb > 1) {
-            s.ticket[0] = atomicAdd(a.counter, 1u);
-            s.ticket[1] = a.eager ? atomicAdd(a.counter, 1u) : tiles;
-        } else {  // one block of tokens: a tile a thread block
-            s.ticket[0] = blockIdx.x;
-            s.ticket[1] = tiles;
-        }
-        for (int w = 0; w < kWarps; ++w) tc::mbar_init(&s.bars[w], 1);
+        // one block of tokens: a tile a thread block
+        const unsigned first = a.nb > 1 ? atomicAdd(a.counter, 1u) : blockIdx.x;
+        s.tile[0] = tile_of<BACK>(a, first);
+        s.tile[1] = tile_of<BACK>(a, a.eager ? atomicAdd(a.counter, 1u) : tiles);
+        s.later = tile_of<BACK>(a, round_on(first));
+        for (int w = 0; w < 2 * kWarps; ++w) tc::mbar_init(&s.bars[w], 1);
         tc::fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 2 * 3 * kTileCh; i += kThreads) (&s.top[0][0][0])[i] = 0;
     __syncthreads();
 }
 
@@ -642,16 +699,15 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
     const unsigned tiles = (unsigned)(lanes * a.nb);
     open_block<ALIGNED, false>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<ALIGNED, CK, false>(a, s, tiles, lanes);
+        chain_warp<T, ALIGNED, CK, false>(a, s, tiles, lanes);
         return;
     }
     Stage<T, ALIGNED, 3> in(staged, s.bars);
     const void *const src[3] = {a.x, a.r, a.i};
     const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
-    unsigned next = s.ticket[1];
-    if (s.ticket[0] >= tiles) return;
-    Tile t = tile_of<false>(a, s.ticket[0]);
-    in.request(a, maps, t, src);
+    Tile t = s.tile[0];
+    if (t.id >= tiles) return;
+    in.request(a, maps.m, t, src);
     unsigned mark = reset_byte(a, t);
     f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
@@ -698,36 +754,32 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
         if (CK) {
 #pragma unroll
             for (int w = 0; w < 3; ++w) {
-                uint32_t m0 = 0, m1 = 0;
+                Largest<T> top;
 #pragma unroll
-                for (int j = 0; j < kRun; ++j) {
-                    const f2 f = widen(v[w][j]);
-                    m0 = max(m0, (uint32_t)f & 0x7fffffffu);
-                    m1 = max(m1, (uint32_t)(f >> 32) & 0x7fffffffu);
-                }
-                atomicMax(&s.top[n & 1][w][channel<ALIGNED>(0)], m0);
-                atomicMax(&s.top[n & 1][w][channel<ALIGNED>(1)], m1);
+                for (int j = 0; j < kRun; ++j) top.add(v[w][j]);
+                reinterpret_cast<Largest<T> *>(s.top[w][warp])[lane] = top;
             }
         }
         s.maps[warp][lane] = as_map(P, H);
         bar_arrive(kMapsReady);
-        Tile tn = t;
-        ahead = here && next < tiles;
+        Tile tn;
         f2 kn = k;
         auto advance = [&] {  // the next tile's inputs are on their way while this one waits
-            tn = tile_of<false>(a, next);
-            in.request(a, maps, tn, src);
+            in.request(a, maps.m, tn, src);
             mark = reset_byte(a, tn);
             kn = gate_scales<ALIGNED>(a, tn.d0);
         };
-        if (ahead) advance();
-        else if (chained && !a.eager) in.prefetch(a, maps, tiles, t, src, false);
+        ahead = false;
+        if (a.eager) {
+            tn = s.tile[(n + 1) & 1];
+            ahead = here && tn.id < tiles;
+            if (ahead) advance();
+        } else if (chained) in.prefetch(a, maps.m, tiles, s.later, src);
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
             if (!here) in.wait(a.wait);
             break;
         }
-        const unsigned after = a.eager ? s.ticket[n & 1] : tiles;
         f2 h = s.entry[warp][lane];
         const Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
         if (plain) {
@@ -749,51 +801,53 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
             for (int w = 0; w < 3; ++w) {
                 const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
                 const uint32_t k0 = s.code[w][c0], k1 = s.code[w][c1];
+                const f2 inv = f2_pack(k0 == 255 ? 0.f : __uint_as_float((254u - k0) << 23),
+                                       k1 == 255 ? 0.f : __uint_as_float((254u - k1) << 23));
+                const uint32_t keep = (k0 == 255 ? 0u : 0xffu) | (k1 == 255 ? 0u : 0xff00u);
                 int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok0 * a.D + t.d0;
+                if (ALIGNED && left >= kRun) {
+                    int8_t *to = q + (lane & 1) * a.D + (c0 & ~3);
+                    // four bytes a lane: of two neighbours' pairs of two rows, one takes the
+                    // even row's and the other the odd row's
 #pragma unroll
-                for (int j = 0; j < kRun; ++j, q += a.D) {
-                    if (j >= left) break;
-                    float lo, hi;
-                    f2_unpack(widen(v[w][j]), lo, hi);
-                    const int8_t q0 = in_steps(lo, k0), q1 = in_steps(hi, k1);
-                    if (ALIGNED) {  // q is 2-byte aligned and D even
-                        if (y.has0) *reinterpret_cast<char2 *>(q + c0) = make_char2(q0, q1);
-                    } else {
-                        if (y.has0) q[c0] = q0;
-                        if (y.has1) q[c1] = q1;
+                    for (int j = 0; j < kRun; j += 2, to += 2 * a.D) {
+                        const uint32_t even = in_steps(widen(v[w][j]), inv, keep);
+                        const uint32_t odd = in_steps(widen(v[w][j + 1]), inv, keep);
+                        const bool up = lane & 1;
+                        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, up ? even : odd, 1);
+                        const uint32_t word = up ? (theirs | odd << 16) : (even | theirs << 16);
+                        if (y.has0) *reinterpret_cast<uint32_t *>(to) = word;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kRun; ++j, q += a.D) {
+                        if (j >= left) break;
+                        const uint32_t both = in_steps(widen(v[w][j]), inv, keep);
+                        if (y.has0) q[c0] = (int8_t)(both & 0xff);
+                        if (y.has1) q[c1] = (int8_t)(both >> 8);
                     }
                 }
             }
         }
         if (chained && !a.eager) {
             bar_sync(kTicketReady);
-            next = s.ticket[0];
-            ahead = next < tiles;
+            tn = s.tile[0];
+            ahead = tn.id < tiles;
             if (ahead) advance();
         }
         if (!ahead) break;
         t = tn;
         k = kn;
-        next = after;
     }
     if (ahead) in.wait(a.wait);  // nothing may be in flight to shared memory at the end
 }
 
 // ------------------------------------------------------------ backward
 
-// A pair of an 8-bit copy: int8 steps.
-template <bool ALIGNED>
-__device__ __forceinline__ char2 copy_pair(const GatedArgs &a, const Tile &t, int w, int tok) {
-    if (tok >= t.n) return make_char2(0, 0);
-    const int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok * a.D + t.d0;
-    const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
-    if (ALIGNED)
-        return t.d0 + c0 < a.D ? *reinterpret_cast<const char2 *>(q + c0) : make_char2(0, 0);
-    return make_char2(t.d0 + c0 < a.D ? q[c0] : 0, t.d0 + c1 < a.D ? q[c1] : 0);
-}
+// The steps of an 8-bit copy's block.
 template <bool ALIGNED>
 __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w) {
-    const uint8_t *e = a.e + ((w * a.batch + t.b) * a.nb + t.blk) * a.D + t.d0;
+    const uint8_t *e = a.e + w * a.batch * a.nb * a.D + t.blocks0 + t.d0;
     const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
     return f2_pack(t.d0 + c0 < a.D ? __uint_as_float((uint32_t)e[c0] << 23) : 0.f,
                    t.d0 + c1 < a.D ? __uint_as_float((uint32_t)e[c1] << 23) : 0.f);
@@ -811,11 +865,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const unsigned tiles = (unsigned)(lanes * a.nb);
     open_block<ALIGNED, true>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<ALIGNED, CK, true>(a, s, tiles, lanes);
+        chain_warp<T, ALIGNED, CK, true>(a, s, tiles, lanes);
         return;
     }
-    Stage<T, ALIGNED, kIn> in(staged, s.bars);
+    using In = Stage<T, ALIGNED, kIn>;
+    using Copies = Stage<int8_t, ALIGNED, 3>;
+    In in(staged, s.bars);
+    Copies copies(staged + In::kBytes, s.bars + kWarps);  // used with CK
     const void *src[kIn];
+    const void *const csrc[3] = {a.q, a.q + a.batch * a.L * a.D, a.q + 2 * a.batch * a.L * a.D};
     src[0] = a.dy;
     if constexpr (!CK) {
         src[1] = a.r;
@@ -823,10 +881,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         src[3] = a.x;
     }
     const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
-    unsigned next = s.ticket[1];
-    if (s.ticket[0] >= tiles) return;
-    Tile t = tile_of<true>(a, s.ticket[0]);
-    in.request(a, maps, t, src);
+    Tile t = s.tile[0];
+    if (t.id >= tiles) return;
+    in.request(a, maps.m, t, src);
+    f2 steps[3], steps_next[3];
+    if constexpr (CK) {
+        copies.request(a, maps.m + 1, t, csrc);
+#pragma unroll
+        for (int w = 0; w < 3; ++w) steps[w] = copy_step<ALIGNED>(a, t, w);
+    }
     unsigned mark = reset_byte(a, t);
     f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
@@ -838,17 +901,19 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         const int left = t.n - tok0;
         const bool plain = all_fast(k) && marks == 0 && left >= kRun;
         // kept until the gradients: dy, x (as stored) and the two sigmoids
-        std::conditional_t<CK, char2, P2> xr[kRun];
+        std::conditional_t<CK, uint16_t, P2> xr[kRun];
         P2 dyr[kRun];
-        f2 sr[kRun], si[kRun], steps[3];
-        if (CK) {
-#pragma unroll
-            for (int w = 0; w < 3; ++w) steps[w] = copy_step<ALIGNED>(a, t, w);
-        }
+        f2 sr[kRun], si[kRun];
         uint32_t at[kIn];
 #pragma unroll
         for (int w = 0; w < kIn; ++w) at[w] = in.place(a, t, src[w]);
-        const bool here = in.wait(a.wait);
+        bool here = in.wait(a.wait);
+        uint32_t cat[3];
+        if constexpr (CK) {
+#pragma unroll
+            for (int w = 0; w < 3; ++w) cat[w] = copies.place(a, t, csrc[w]);
+            here = copies.wait(a.wait) && here;
+        }
         if (!here) give_up(a, &s.stop[n & 1]);
         f2 P = f2_both(1.f), H = none, R = none;
         auto gates = [&](auto run) {
@@ -858,10 +923,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 f2 rv, iv, x;
                 dyr[j] = in.get(0, j, at[0], rowbytes);
                 if constexpr (CK) {
-                    xr[j] = copy_pair<ALIGNED>(a, t, 0, tok0 + j);
+                    const uint32_t step = (uint32_t)a.D;
+                    xr[j] = copies.get(0, j, cat[0], step);
                     x = f2_mul(widen(xr[j]), steps[0]);
-                    rv = f2_mul(widen(copy_pair<ALIGNED>(a, t, 1, tok0 + j)), steps[1]);
-                    iv = f2_mul(widen(copy_pair<ALIGNED>(a, t, 2, tok0 + j)), steps[2]);
+                    rv = f2_mul(widen(copies.get(1, j, cat[1], step)), steps[1]);
+                    iv = f2_mul(widen(copies.get(2, j, cat[2], step)), steps[2]);
                 } else {
                     rv = widen(in.get(1, j, at[1], rowbytes));
                     iv = widen(in.get(2, j, at[2], rowbytes));
@@ -891,23 +957,35 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         f2_unpack(R, Rw.x, Rw.y);
         s.right[warp][lane] = Rw;
         bar_arrive(kMapsReady);
-        Tile tn = t;
-        ahead = here && next < tiles;
+        Tile tn;
         f2 kn = k;
         auto advance = [&] {
-            tn = tile_of<true>(a, next);
-            in.request(a, maps, tn, src);
+            in.request(a, maps.m, tn, src);
+            if constexpr (CK) {
+                copies.request(a, maps.m + 1, tn, csrc);
+#pragma unroll
+                for (int w = 0; w < 3; ++w) steps_next[w] = copy_step<ALIGNED>(a, tn, w);
+            }
             mark = reset_byte(a, tn);
             kn = gate_scales<ALIGNED>(a, tn.d0);
         };
-        if (ahead) advance();
-        else if (chained && !a.eager) in.prefetch(a, maps, tiles, t, src, true);
+        ahead = false;
+        if (a.eager) {
+            tn = s.tile[(n + 1) & 1];
+            ahead = here && tn.id < tiles;
+            if (ahead) advance();
+        } else if (chained) {
+            in.prefetch(a, maps.m, tiles, s.later, src);
+            if constexpr (CK) copies.prefetch(a, maps.m + 1, tiles, s.later, csrc);
+        }
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
-            if (!here) in.wait(a.wait);
+            if (!here) {
+                in.wait(a.wait);
+                if constexpr (CK) copies.wait(a.wait);
+            }
             break;
         }
-        const unsigned after = a.eager ? s.ticket[n & 1] : tiles;
         f2 dl = none;
         auto grads = [&](auto run) {
             constexpr bool kPlain = decltype(run)::value;
@@ -958,8 +1036,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         s.dlam[n & 1][warp][channel<ALIGNED>(1)] = dw.y;
         if (chained && !a.eager) {
             bar_sync(kTicketReady);
-            next = s.ticket[0];
-            ahead = next < tiles;
+            tn = s.tile[0];
+            ahead = tn.id < tiles;
             if (ahead) advance();
         }
         if (!ahead) {
@@ -968,9 +1046,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         }
         t = tn;
         k = kn;
-        next = after;
+        if constexpr (CK) {
+#pragma unroll
+            for (int w = 0; w < 3; ++w) steps[w] = steps_next[w];
+        }
     }
-    if (ahead) in.wait(a.wait);
+    if (ahead) {
+        in.wait(a.wait);
+        if constexpr (CK) copies.wait(a.wait);
+    }
 }
 
 // dlam: the blocks' sums over batch and blocks, times the channel's factor.
@@ -1069,8 +1153,9 @@ bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
     const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1};
     const cuuint64_t strides[3] = {row, row * (uint64_t)a.L, row * (uint64_t)a.L};
     const cuuint32_t box[4] = {kTileCh, kRun, 1, 1}, estr[4] = {1, 1, 1, 1};
-    return encoder()(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    return encoder()(m, sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                      4, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -1086,7 +1171,7 @@ cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
 template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
     Maps maps;
-    const bool aligned = on(a.y, 8) && on(a.q, 2) && make_map<T>(&maps.m[0], a.x, a) &&
+    const bool aligned = on(a.y, 8) && on(a.q, 4) && make_map<T>(&maps.m[0], a.x, a) &&
                          make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a);
     a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4);
     return aligned ? forward_t<T, true>(a, maps, st) : forward_t<T, false>(a, maps, st);
@@ -1095,18 +1180,22 @@ cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
 template <typename T, bool ALIGNED>
 cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     return a.q ? start("gated_backward", gated_backward_kernel<T, ALIGNED, true>,
-                       Stage<T, ALIGNED, 1>::kBytes, a, maps, st)
+                       Stage<T, ALIGNED, 1>::kBytes + Stage<int8_t, ALIGNED, 3>::kBytes, a, maps, st)
                : start("gated_backward", gated_backward_kernel<T, ALIGNED, false>,
                        Stage<T, ALIGNED, 4>::kBytes, a, maps, st);
 }
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     Maps maps;
-    const bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && on(a.q, 2) &&
-                         make_map<T>(&maps.m[0], a.dy, a) &&
-                         (a.q || (make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a) &&
-                                  make_map<T>(&maps.m[3], a.x, a)));
-    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4) && on(a.dy, 4);
+    bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && make_map<T>(&maps.m[0], a.dy, a);
+    if (a.q) {
+        for (int w = 0; w < 3; ++w)
+            aligned = aligned && make_map<int8_t>(&maps.m[1 + w], a.q + w * a.batch * a.L * a.D, a);
+    } else {
+        aligned = aligned && make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a) &&
+                  make_map<T>(&maps.m[3], a.x, a);
+    }
+    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4) && on(a.dy, 4) && on(a.q, 4);
     cudaError_t e = aligned ? backward_t<T, true>(a, maps, st) : backward_t<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
