@@ -8,7 +8,13 @@
 //   dA  = sum_t r dt a h_{t-1} + r (dw/dA) x B,  dw/dA  = (dt a - w) / A (hold)
 //
 // then ddt through the clamp (1 between its bounds, bounds included) and the
-// softplus. Every state entry takes an exponential a token and about a dozen
+// softplus. With the hold, the state is carried as g = A h, which moves by
+// E = exp(dt A) - 1 alone, without the cancellation of 1 - a:
+//
+//   g <- g + E (g + x B)   w = E / A   ddt = sum_n a r (g + x B)
+//   dA = (1/A) sum_t [dt a r (g + x B) - r w x B]
+//
+// (the last difference is taken term by term, from series, where |A| < 2^-5). Every state entry takes an exponential a token and about a dozen
 // fp32 operations, 16 or so times what a token's bytes need: the pass is bound
 // by the arithmetic, and by keeping sums over states (dx, ddt), over channels
 // (dB, dC) and over tokens (dA) all in registers.
@@ -24,6 +30,8 @@
 //   4. sums of dB and dC over blocks of channels, and of dA, dDskip and the
 //      bias's gradient over batch and chunks. No atomics: every sum has one order.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -97,35 +105,45 @@ __device__ __forceinline__ float prepare_step(float raw, float bias, const StepA
     return dt;
 }
 
-// exp(z), the input weight and (SLOPE) dw/dA of one state entry, z = dt A.
-// The hold takes e^z - 1 and what follows from it by their series where
-// |z| < 1/4: phi2 = (phi1 - 1) / z to z^4 (remainder below z^5/5040 < 2e-7),
-// phi1 = (e^z - 1) / z = 1 + z phi2, w = dt phi1, dw/dA = dt^2 (phi1 - phi2),
-// none of which cancels. A = 0 comes as -1e-30 (read_A).
-template <bool ZOH, bool SLOPE>
-__device__ __forceinline__ void entry(float dt, float A, float invA, float &a, float &w,
-                                      float &slope) {
-    if (!ZOH) {
-        a = tc::fast_exp2(dt * A);  // A holds A log2 e
-        w = dt;
-        return;
-    }
-    const float z = dt * A;
-    const float e = tc::fast_exp2(z * kLog2eB), em = e - 1.f;
-    float phi2 = 1.f / 720.f;
-    phi2 = fmaf(phi2, z, 1.f / 120.f);
-    phi2 = fmaf(phi2, z, 1.f / 24.f);
-    phi2 = fmaf(phi2, z, 1.f / 6.f);
-    phi2 = fmaf(phi2, z, 0.5f);
-    const float phi1 = fmaf(z, phi2, 1.f);
-    const bool small = fabsf(z) < 0.25f;
-    a = small ? fmaf(z, phi1, 1.f) : e;
-    w = small ? dt * phi1 : em * invA;
-    if (SLOPE) slope = small ? dt * dt * (phi1 - phi2) : (dt * e - w) * invA;
-}
+// One pair of state entries at one step: F is exp(dt A) (Euler) or
+// E = exp(dt A) - 1 (hold), the latter by its series where |z| < 1/4, z = dt A
+// (remainder below z^6 / 5040 < 5e-8 relative), else from exp2, whose error of
+// 2^-22 is then at most 1e-6 of it.
+using tc::f2;
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_mul;
+using tc::f2_pack;
+using tc::f2_sub;
+using tc::f2_unpack;
+__device__ __forceinline__ f2 f2_both(float v) { return f2_pack(v, v); }
 
-__device__ __forceinline__ float read_A(float A, bool zoh) {
-    return zoh ? (A == 0.f ? -1e-30f : A) : A * kLog2eB;
+template <bool ZOH>
+struct Decay {
+    f2 A, Al;  // A (hold: kept off zero) and A log2 e
+    __device__ __forceinline__ f2 at(f2 dt) const {
+        float z0, z1, l0, l1;
+        f2_unpack(f2_mul(dt, Al), l0, l1);
+        const f2 e = f2_pack(tc::fast_exp2(l0), tc::fast_exp2(l1));
+        if (!ZOH) return e;
+        const f2 z = f2_mul(dt, A);
+        f2 p = f2_fma(f2_both(1.f / 720.f), z, f2_both(1.f / 120.f));
+        p = f2_fma(p, z, f2_both(1.f / 24.f));
+        p = f2_fma(p, z, f2_both(1.f / 6.f));
+        p = f2_fma(p, z, f2_both(0.5f));
+        p = f2_fma(p, z, f2_both(1.f));
+        float s0, s1, e0, e1;
+        f2_unpack(f2_mul(z, p), s0, s1);
+        f2_unpack(f2_add(e, f2_both(-1.f)), e0, e1);
+        f2_unpack(z, z0, z1);
+        return f2_pack(fabsf(z0) < 0.25f ? s0 : e0, fabsf(z1) < 0.25f ? s1 : e1);
+    }
+};
+
+// A as the hold uses it: |A| >= 2^-40, which changes no result by more than
+// 2^-40 a token and lets g = A h carry the state of A = 0 too.
+__device__ __forceinline__ float off_zero(float A) {
+    return fabsf(A) < 0x1p-40f ? (A > 0.f ? 0x1p-40f : -0x1p-40f) : A;
 }
 
 struct BwdArgs {
@@ -145,7 +163,7 @@ struct BwdArgs {
 
 // Shared memory of the staged tile, in floats.
 template <int N>
-struct Tile {
+struct __align__(16) Tile {
     static constexpr int kState = kCh * N;
     float x[kCh][kRow], dt[kCh][kRow], dy[kCh][kRow];
     float B[kChunk][N], C[kChunk][N];
@@ -219,36 +237,81 @@ __device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Til
     }
 }
 
-// The map of a run of tokens for one thread's states: end state S from zero,
-// gradient R handed to the left when none comes from the right, product P.
+__device__ __forceinline__ void load4x(const float *p, f2 (&v)[2]) {
+    const float4 q = *reinterpret_cast<const float4 *>(p);
+    v[0] = f2_pack(q.x, q.y);
+    v[1] = f2_pack(q.z, q.w);
+}
+__device__ __forceinline__ void store4x(float *p, const f2 (&v)[2]) {
+    float4 q;
+    f2_unpack(v[0], q.x, q.y);
+    f2_unpack(v[1], q.z, q.w);
+    *reinterpret_cast<float4 *>(p) = q;
+}
+
+// One token's move of the state: s <- a s + w x B, or with the hold g.
+template <bool ZOH>
+__device__ __forceinline__ f2 move(f2 F, f2 s, f2 in) {
+    return ZOH ? f2_fma(F, f2_add(s, in), s) : f2_fma(F, s, in);
+}
+template <bool ZOH>
+__device__ __forceinline__ f2 times_decay(f2 v, f2 F) {
+    return ZOH ? f2_fma(v, F, v) : f2_mul(v, F);
+}
+
+// The map of a run of tokens for one thread's four states: end state S from
+// zero, gradient R handed to the left when none comes from the right, product P.
 template <int N, bool ZOH, int TOKENS>
 __device__ __forceinline__ void run_sums(const Tile<N> &s, int c, int t0, int n0,
-                                         const float (&A)[kQ], const float (&invA)[kQ],
-                                         float (&S)[kQ], float (&R)[kQ], float (&P)[kQ]) {
+                                         const Decay<ZOH> (&A)[2], f2 (&S)[2], f2 (&R)[2],
+                                         f2 (&P)[2]) {
 #pragma unroll
-    for (int k = 0; k < kQ; ++k) S[k] = R[k] = 0.f, P[k] = 1.f;
-#pragma unroll 4
-    for (int t = t0; t < t0 + TOKENS; ++t) {
-        const float xv = s.x[c][t], dtv = s.dt[c][t], yv = s.dy[c][t];
+    for (int k = 0; k < 2; ++k) S[k] = R[k] = f2_both(0.f), P[k] = f2_both(1.f);
+#pragma unroll 1
+    for (int t4 = t0; t4 < t0 + TOKENS; t4 += 4) {
+        const float4 x4 = *reinterpret_cast<const float4 *>(&s.x[c][t4]);
+        const float4 d4 = *reinterpret_cast<const float4 *>(&s.dt[c][t4]);
+        const float4 y4 = *reinterpret_cast<const float4 *>(&s.dy[c][t4]);
+        const float xs[4] = {x4.x, x4.y, x4.z, x4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w},
+                    ys[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) {
-            float av, w, unused;
-            entry<ZOH, false>(dtv, A[k], invA[k], av, w, unused);
-            S[k] = fmaf(av, S[k], w * xv * s.B[t][n0 + k]);
-            P[k] *= av;
-            R[k] = fmaf(P[k], yv * s.C[t][n0 + k], R[k]);
+        for (int j = 0; j < 4; ++j) {
+            const f2 in = f2_both(ZOH ? xs[j] : xs[j] * ds[j]), dt = f2_both(ds[j]),
+                     dy = f2_both(ys[j]);
+            f2 B[2], C[2];
+            load4x(&s.B[t4 + j][n0], B);
+            load4x(&s.C[t4 + j][n0], C);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f2 F = A[k].at(dt);
+                S[k] = move<ZOH>(F, S[k], f2_mul(in, B[k]));
+                P[k] = times_decay<ZOH>(P[k], F);
+                R[k] = f2_fma(P[k], f2_mul(dy, C[k]), R[k]);
+            }
         }
     }
 }
 
-template <int N>
-__device__ __forceinline__ void load_A(const BwdArgs &a, int64_t d, int n0, bool zoh,
-                                       float (&A)[kQ], float (&invA)[kQ]) {
+// A of a thread's states, 1 / A and whether any is too near zero for the
+// plain form of the hold's dA.
+template <int N, bool ZOH>
+__device__ __forceinline__ bool load_A(const BwdArgs &a, int64_t d, int n0, Decay<ZOH> (&A)[2],
+                                       f2 (&raw)[2], f2 (&invA)[2]) {
+    float v[kQ];
+    bool tiny = false;
 #pragma unroll
     for (int k = 0; k < kQ; ++k) {
-        A[k] = read_A(a.A[d * N + n0 + k], zoh);
-        invA[k] = zoh ? 1.f / A[k] : 0.f;
+        v[k] = a.A[d * N + n0 + k];
+        if (ZOH) v[k] = off_zero(v[k]);
+        tiny = tiny || fabsf(v[k]) < 0x1p-5f;
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        raw[k] = A[k].A = f2_pack(v[2 * k], v[2 * k + 1]);
+        A[k].Al = f2_mul(A[k].A, f2_both(kLog2eB));
+        invA[k] = ZOH ? f2_pack(1.f / v[2 * k], 1.f / v[2 * k + 1]) : 0;
+    }
+    return ZOH && tiny;
 }
 
 template <typename T, int N, bool ZOH>
@@ -267,16 +330,14 @@ __global__ void __launch_bounds__(kCh *N / kQ) scan_bwd_sums(const BwdArgs a) {
         const int c = threadIdx.x / kLanes, n0 = (threadIdx.x % kLanes) * kQ;
         const bool has = d0 + c < dend;
         const int64_t d = has ? d0 + c : dend - 1;
-        float A[kQ], invA[kQ], S[kQ], R[kQ], P[kQ];
-        load_A<N>(a, d, n0, ZOH, A, invA);
-        run_sums<N, ZOH, kChunk>(s, c, 0, n0, A, invA, S, R, P);
+        Decay<ZOH> A[2];
+        f2 v[2], invA[2], S[2], R[2], P[2];
+        load_A<N, ZOH>(a, d, n0, A, v, invA);
+        run_sums<N, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
         if (has) {
             const int64_t at = (p.b * a.nc + p.chunk) * a.D + d;
-#pragma unroll
-            for (int j = 0; j < kQ; ++j) {
-                a.S[at * N + n0 + j] = S[j];
-                a.R[at * N + n0 + j] = R[j];
-            }
+            store4x(&a.S[at * N + n0], S);
+            store4x(&a.R[at * N + n0], R);
             if (n0 == 0) {
                 float sum = 0.f;
                 for (int t = 0; t < kChunk; ++t) sum += s.dt[c][t];
@@ -286,23 +347,40 @@ __global__ void __launch_bounds__(kCh *N / kQ) scan_bwd_sums(const BwdArgs a) {
     }
 }
 
-// The chains over chunks: blockIdx.y 0 the states, 1 the gradients.
-__global__ void scan_bwd_chain(const BwdArgs a, int N, const float *h0, const float *dh_final,
-                               float *dh0) {
+// The chains over chunks: blockIdx.y 0 the states (with the hold g = A h), 1
+// the gradients. Eight chunks' words are loaded at a time.
+template <int N, bool ZOH>
+__global__ void __launch_bounds__(128)
+scan_bwd_chain(const BwdArgs a, const float *h0, const float *dh_final, float *dh0) {
+    constexpr int kBatch = 8;
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t lane_len = a.D * N;
     if (i >= a.batch * lane_len) return;
     const int64_t b = i / lane_len, dn = i % lane_len;
     const bool back = blockIdx.y == 1;
-    const float A = a.A[dn] * kLog2eB;
+    float A = a.A[dn];
+    if (ZOH) A = off_zero(A);
+    const float Al = A * kLog2eB;
     const float *first = back ? dh_final : h0;
-    float *S = back ? a.R : a.S;
+    const int64_t way = back ? -1 : 1, c0 = b * a.nc + (back ? a.nc - 1 : 0);
+    float *S = (back ? a.R : a.S) + c0 * lane_len + dn;
+    const float *steps = a.steps + c0 * a.D + dn / N;
     float h = first ? first[i] : 0.f;
-    for (int64_t j = 0; j < a.nc; ++j) {
-        const int64_t c = b * a.nc + (back ? a.nc - 1 - j : j);
-        const float v = S[c * lane_len + dn];
-        S[c * lane_len + dn] = h;
-        h = fmaf(tc::fast_exp2(a.steps[c * a.D + dn / N] * A), h, v);
+    if (ZOH && !back) h *= A;
+    for (int64_t j0 = 0; j0 < a.nc; j0 += kBatch) {
+        float v[kBatch], t[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const bool has = j0 + j < a.nc;
+            v[j] = has ? S[way * (j0 + j) * lane_len] : 0.f;
+            t[j] = has ? steps[way * (j0 + j) * a.D] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (j0 + j >= a.nc) break;
+            S[way * (j0 + j) * lane_len] = h;
+            h = fmaf(tc::fast_exp2(t[j] * Al), h, v[j]);
+        }
     }
     if (back && dh0) dh0[i] = h;
 }
@@ -315,6 +393,55 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+// Sums of the piece's four values over a channel's LANES lanes: with 4 lanes,
+// lane i ends with token i's, with 2 lane i with those of tokens 2i and 2i + 1.
+template <int LANES>
+__device__ __forceinline__ void share_sums(float (&u)[kPiece], float (&v)[kPiece], int lane) {
+    if constexpr (LANES == 4) {
+        const bool up = lane & 2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float su = up ? u[j] : u[j + 2], sv = up ? v[j] : v[j + 2];
+            u[j] = (up ? u[j + 2] : u[j]) + __shfl_xor_sync(0xffffffffu, su, 2);
+            v[j] = (up ? v[j + 2] : v[j]) + __shfl_xor_sync(0xffffffffu, sv, 2);
+        }
+        const bool odd = lane & 1;
+        const float su = odd ? u[0] : u[1], sv = odd ? v[0] : v[1];
+        u[0] = (odd ? u[1] : u[0]) + __shfl_xor_sync(0xffffffffu, su, 1);
+        v[0] = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, sv, 1);
+    } else if constexpr (LANES == 2) {
+        const bool up = lane & 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float su = up ? u[j] : u[j + 2], sv = up ? v[j] : v[j + 2];
+            u[j] = (up ? u[j + 2] : u[j]) + __shfl_xor_sync(0xffffffffu, su, 1);
+            v[j] = (up ? v[j + 2] : v[j]) + __shfl_xor_sync(0xffffffffu, sv, 1);
+        }
+    }
+}
+
+// The hold's dw/dA = (dt e^z - w) / A of a pair, for A near zero: with
+// phi1 = (e^z - 1) / z and phi2 = (phi1 - 1) / z it is dt^2 (phi1 - phi2),
+// where |z| < 1/4 from the series of phi2 (remainder below z^5/5040 < 2e-7).
+__device__ __forceinline__ f2 slope(float dt, f2 A, f2 invA, f2 E) {
+    float a[2], i[2], e[2], r[2];
+    f2_unpack(A, a[0], a[1]);
+    f2_unpack(invA, i[0], i[1]);
+    f2_unpack(E, e[0], e[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float z = dt * a[k];
+        float phi2 = 1.f / 720.f;
+        phi2 = fmaf(phi2, z, 1.f / 120.f);
+        phi2 = fmaf(phi2, z, 1.f / 24.f);
+        phi2 = fmaf(phi2, z, 1.f / 6.f);
+        phi2 = fmaf(phi2, z, 0.5f);
+        r[k] = fabsf(z) < 0.25f ? dt * dt * (fmaf(z, phi2, 1.f) - phi2)
+                                : (fmaf(dt, e[k], dt) - e[k] * i[k]) * i[k];
+    }
+    return f2_pack(r[0], r[1]);
+}
+
 template <typename T, int N, bool ZOH>
 __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a) {
     constexpr int kLanes = N / kQ, kPerWarp = 32 / kLanes, kState = kCh * N;
@@ -324,11 +451,12 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
     const int64_t dend = (p.g + 1) * a.gch;
     const int tid = threadIdx.x, lane = tid & 31, piece = tid >> 5;
     const int n0 = (lane % kLanes) * kQ, t0 = piece * kPiece;
-    float accB[kPiece][kQ], accC[kPiece][kQ];
+    const f2 none = f2_both(0.f);
+    f2 accB[kPiece][2], accC[kPiece][2];
 #pragma unroll
     for (int t = 0; t < kPiece; ++t)
 #pragma unroll
-        for (int k = 0; k < kQ; ++k) accB[t][k] = accC[t][k] = 0.f;
+        for (int k = 0; k < 2; ++k) accB[t][k] = accC[t][k] = none;
     stage_rows<T, N, kMainThreads>(a, p, s);
     for (int tile = 0; tile < p.tiles; ++tile) {
         const int64_t d0 = p.g * a.gch + (int64_t)(p.tile0 + tile) * kCh;
@@ -343,24 +471,25 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
             r = a.R[(row + d0) * N + tid];
         }
         __syncthreads();
+#pragma unroll 1
         for (int c = lane / kLanes; c < kCh; c += kPerWarp) {
-            float A[kQ], invA[kQ], S[kQ], R[kQ], P[kQ];
-            load_A<N>(a, d0 + c < dend ? d0 + c : dend - 1, n0, ZOH, A, invA);
-            run_sums<N, ZOH, kPiece>(s, c, t0, n0, A, invA, S, R, P);
-#pragma unroll
-            for (int k = 0; k < kQ; ++k) {
-                s.S[piece][c * N + n0 + k] = S[k];
-                s.R[piece][c * N + n0 + k] = R[k];
-                s.P[piece][c * N + n0 + k] = P[k];
-            }
+            Decay<ZOH> A[2];
+            f2 v[2], invA[2], S[2], R[2], P[2];
+            load_A<N, ZOH>(a, d0 + c < dend ? d0 + c : dend - 1, n0, A, v, invA);
+            run_sums<N, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
+            store4x(&s.S[piece][c * N + n0], S);
+            store4x(&s.R[piece][c * N + n0], R);
+            store4x(&s.P[piece][c * N + n0], P);
         }
         __syncthreads();
         if (tid < kState) {
+#pragma unroll 4
             for (int j = 0; j < kPieces; ++j) {
                 const float v = s.S[j][tid];
                 s.S[j][tid] = h;
                 h = fmaf(s.P[j][tid], h, v);
             }
+#pragma unroll 4
             for (int j = kPieces - 1; j >= 0; --j) {
                 const float v = s.R[j][tid];
                 s.R[j][tid] = r;
@@ -368,73 +497,108 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
             }
         }
         __syncthreads();
+#pragma unroll 1
         for (int c = lane / kLanes; c < kCh; c += kPerWarp) {
             const int64_t d = d0 + c < dend ? d0 + c : dend - 1;
-            float A[kQ], invA[kQ], An[kQ], dA[kQ], hp[kPiece][kQ], av[kPiece][kQ],
-                sl[kPiece][kQ], hc[kQ], rc[kQ];
-            load_A<N>(a, d, n0, ZOH, A, invA);
+            Decay<ZOH> A[2];
+            f2 An[2], invA[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
+            const bool tiny = load_A<N, ZOH>(a, d, n0, A, An, invA);
             const float Ds = a.Dskip ? a.Dskip[d] : 0.f;
-#pragma unroll
-            for (int k = 0; k < kQ; ++k) {
-                An[k] = ZOH ? A[k] : a.A[d * N + n0 + k];
-                dA[k] = 0.f;
-                hc[k] = s.S[piece][c * N + n0 + k];
-                rc[k] = s.R[piece][c * N + n0 + k];
-            }
+            load4x(&s.S[piece][c * N + n0], st);
+            load4x(&s.R[piece][c * N + n0], carry);
+            const float4 x4 = *reinterpret_cast<const float4 *>(&s.x[c][t0]);
+            const float4 d4 = *reinterpret_cast<const float4 *>(&s.dt[c][t0]);
+            const float4 y4 = *reinterpret_cast<const float4 *>(&s.dy[c][t0]);
+            const float xs[kPiece] = {x4.x, x4.y, x4.z, x4.w}, ds[kPiece] = {d4.x, d4.y, d4.z, d4.w},
+                        ys[kPiece] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
             for (int t = 0; t < kPiece; ++t) {
-                const float xv = s.x[c][t0 + t], dtv = s.dt[c][t0 + t], yv = s.dy[c][t0 + t];
+                const f2 in = f2_both(ZOH ? xs[t] : xs[t] * ds[t]), dt = f2_both(ds[t]),
+                         dy = f2_both(ys[t]);
+                f2 B[2];
+                load4x(&s.B[t0 + t][n0], B);
 #pragma unroll
-                for (int k = 0; k < kQ; ++k) {
-                    float w;
-                    entry<ZOH, true>(dtv, A[k], invA[k], av[t][k], w, sl[t][k]);
-                    hp[t][k] = hc[k];
-                    hc[k] = fmaf(av[t][k], hc[k], w * xv * s.B[t0 + t][n0 + k]);
-                    accC[t][k] = fmaf(yv, hc[k], accC[t][k]);
+                for (int k = 0; k < 2; ++k) {
+                    F[t][k] = A[k].at(dt);
+                    before[t][k] = st[k];
+                    st[k] = move<ZOH>(F[t][k], st[k], f2_mul(in, B[k]));
+                    const f2 h = ZOH ? f2_mul(st[k], invA[k]) : st[k];
+                    accC[t][k] = f2_fma(dy, h, accC[t][k]);
                 }
             }
             float vB[kPiece], vA[kPiece];
 #pragma unroll
-            for (int t = kPiece - 1; t >= 0; --t) {
-                const float xv = s.x[c][t0 + t], dtv = s.dt[c][t0 + t], yv = s.dy[c][t0 + t];
-                vB[t] = vA[t] = 0.f;
+            for (int k = 0; k < 2; ++k) dA[k] = dA2[k] = none;
+            auto back = [&](auto near_zero) {
 #pragma unroll
-                for (int k = 0; k < kQ; ++k) {
-                    const float Bv = s.B[t0 + t][n0 + k];
-                    const float rv = fmaf(yv, s.C[t0 + t][n0 + k], rc[k]);
-                    const float ra = rv * av[t][k];
-                    if (ZOH) {
-                        const float w = fmaf(dtv, av[t][k], -An[k] * sl[t][k]);
-                        const float rw = rv * w, xB = xv * Bv;
-                        vB[t] = fmaf(rw, Bv, vB[t]);
-                        accB[t][k] = fmaf(rw, xv, accB[t][k]);
-                        vA[t] = fmaf(ra, fmaf(An[k], hp[t][k], xB), vA[t]);
-                        dA[k] = fmaf(ra * dtv, hp[t][k], fmaf(rv * sl[t][k], xB, dA[k]));
-                    } else {
-                        vB[t] = fmaf(rv, Bv, vB[t]);
-                        accB[t][k] = fmaf(rv, dtv * xv, accB[t][k]);
-                        const float t1 = ra * hp[t][k];
-                        vA[t] = fmaf(An[k], t1, vA[t]);
-                        dA[k] = fmaf(dtv, t1, dA[k]);
+                for (int t = kPiece - 1; t >= 0; --t) {
+                    const f2 x = f2_both(xs[t]), dt = f2_both(ds[t]), dy = f2_both(ys[t]),
+                             u = f2_both(xs[t] * ds[t]);
+                    f2 B[2], C[2], sB = none, sA = none;
+                    load4x(&s.B[t0 + t][n0], B);
+                    load4x(&s.C[t0 + t][n0], C);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const f2 rv = f2_fma(dy, C[k], carry[k]);
+                        const f2 ra = times_decay<ZOH>(rv, F[t][k]);
+                        if (ZOH) {
+                            const f2 rw = f2_mul(rv, f2_mul(F[t][k], invA[k]));
+                            const f2 in = f2_mul(x, B[k]);
+                            const f2 rt = f2_mul(ra, f2_add(before[t][k], in));
+                            sB = f2_fma(rw, B[k], sB);
+                            accB[t][k] = f2_fma(rw, x, accB[t][k]);
+                            sA = f2_add(sA, rt);
+                            if constexpr (decltype(near_zero)::value) {
+                                // term by term: dt a r h + r x B dw/dA
+                                dA[k] = f2_fma(f2_mul(ra, dt), f2_mul(before[t][k], invA[k]), dA[k]);
+                                dA2[k] = f2_fma(f2_mul(rv, in), slope(ds[t], An[k], invA[k], F[t][k]),
+                                                dA2[k]);
+                            } else {
+                                dA[k] = f2_fma(dt, rt, dA[k]);
+                                dA2[k] = f2_fma(rw, in, dA2[k]);
+                            }
+                        } else {
+                            const f2 t1 = f2_mul(ra, before[t][k]);
+                            sB = f2_fma(rv, B[k], sB);
+                            accB[t][k] = f2_fma(rv, u, accB[t][k]);
+                            sA = f2_fma(An[k], t1, sA);
+                            dA[k] = f2_fma(dt, t1, dA[k]);
+                        }
+                        carry[k] = ra;
                     }
-                    rc[k] = ra;
+                    float lo, hi;
+                    f2_unpack(sB, lo, hi);
+                    vB[t] = lo + hi;
+                    f2_unpack(sA, lo, hi);
+                    vA[t] = lo + hi;
                 }
-            }
+            };
+            if (__any_sync(0xffffffffu, tiny)) {
+                back(std::true_type{});
 #pragma unroll
-            for (int t = 0; t < kPiece; ++t) {
-                const float sB = lanes_sum<kLanes>(vB[t]), sA = lanes_sum<kLanes>(vA[t]);
-                if (lane % kLanes == 0) {
-                    const float xv = s.x[c][t0 + t], yv = s.dy[c][t0 + t];
-                    s.dx[c][t0 + t] = fmaf(Ds, yv, ZOH ? sB : sB * s.dt[c][t0 + t]);
-                    s.fac[c][t0 + t] *= ZOH ? sA : fmaf(xv, sB, sA);  // ddt
-                }
-            }
+                for (int k = 0; k < 2; ++k) dA[k] = f2_add(dA[k], dA2[k]);
+            } else {
+                back(std::false_type{});
 #pragma unroll
-            for (int k = 0; k < kQ; ++k) s.P[piece][c * N + n0 + k] = dA[k];
+                for (int k = 0; k < 2; ++k)
+                    if (ZOH) dA[k] = f2_mul(invA[k], f2_sub(dA[k], dA2[k]));
+            }
+            // dx and ddt: each lane of the channel ends with the sums of its share of the tokens
+            share_sums<kLanes>(vB, vA, lane);
+            constexpr int kShare = kPiece / kLanes;
+#pragma unroll
+            for (int j = 0; j < kShare; ++j) {
+                const int t = t0 + (lane % kLanes) * kShare + j;
+                const float sB = vB[j], sA = vA[j];
+                s.dx[c][t] = fmaf(Ds, s.dy[c][t], ZOH ? sB : sB * s.dt[c][t]);
+                s.fac[c][t] *= ZOH ? sA : fmaf(s.x[c][t], sB, sA);  // ddt
+            }
+            store4x(&s.P[piece][c * N + n0], dA);
         }
         __syncthreads();
         if (chain) {
             float v = 0.f;
+#pragma unroll
             for (int j = 0; j < kPieces; ++j) v += s.P[j][tid];
             a.dA_part[(row + d0) * N + tid] = v;
         }
@@ -467,7 +631,10 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
     for (int t = 0; t < kPiece; ++t)
 #pragma unroll
         for (int k = 0; k < kQ; ++k) {
-            float vb = accB[t][k], vc = accC[t][k];
+            float b0, b1, c0, c1;
+            f2_unpack(accB[t][k / 2], b0, b1);
+            f2_unpack(accC[t][k / 2], c0, c1);
+            float vb = k & 1 ? b1 : b0, vc = k & 1 ? c1 : c0;
 #pragma unroll
             for (int o = kLanes; o < 32; o <<= 1) {
                 vb += __shfl_xor_sync(0xffffffffu, vb, o);
@@ -569,8 +736,8 @@ cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *d
     launch_end(st);
     const int64_t lanes = a.batch * a.D * N;
     launch_begin("scan_bwd_chain", st);
-    scan_bwd_chain<<<dim3((unsigned)((lanes + 127) / 128), 2), 128, 0, st>>>(a, N, h0, dh_final,
-                                                                            dh0);
+    scan_bwd_chain<N, ZOH><<<dim3((unsigned)((lanes + 127) / 128), 2), 128, 0, st>>>(a, h0, dh_final,
+                                                                                    dh0);
     launch_end(st);
     launch_begin("scan_bwd_main", st);
     scan_bwd_main<T, N, ZOH><<<grid, kMainThreads, main_smem, st>>>(a);
