@@ -19,12 +19,12 @@
 // by the arithmetic, and by keeping sums over states (dx, ddt), over channels
 // (dB, dC) and over tokens (dA) all in registers.
 //
-// Time is cut into chunks of 64 tokens that run side by side:
+// Time is cut into chunks of 32 tokens that run side by side:
 //   1. scan_bwd_sums: each chunk's end state from a zero state, and the
 //      gradient it hands to its left when none comes from its right;
 //   2. scan_bwd_chain: the chains over chunks, forward and backward, leaving
 //      the state entering each chunk and the gradient entering it from its right;
-//   3. scan_bwd_main: the same again inside a chunk over its 16 pieces of four
+//   3. scan_bwd_main: the same again inside a chunk over its eight pieces of four
 //      tokens (a warp each), then each piece's states forward and gradients
 //      back, from registers;
 //   4. sums of dB and dC over blocks of channels, and of dA, dDskip and the
@@ -41,7 +41,7 @@ namespace ssd {
 namespace {
 
 constexpr float kLog2eB = 1.4426950408889634f;
-constexpr int kChunk = 64;               // tokens of a chunk
+constexpr int kChunk = 32;               // tokens of a chunk
 constexpr int kPiece = 4;                // tokens of a piece
 constexpr int kPieces = kChunk / kPiece;  // = warps of the main kernel
 constexpr int kCh = 32;                  // channels of a tile
@@ -159,19 +159,28 @@ struct BwdArgs {
     int64_t gch;         // channels of a group
     int tiles_per_group, tiles_per_block, blocks_per_group;
     StepArgs step;
+    bool words;          // x, dt and dy start on 4 bytes
 };
 
-// Shared memory of the staged tile, in floats.
-template <int N>
+// Shared memory of the staged tile. Channels' rows of tokens, as stored, arrive
+// in `words` a tile ahead by asynchronous copies of the 4-byte words that cover
+// them, and are spread from there as floats, tokens along a row.
+template <typename T, int N, int CH>
 struct __align__(16) Tile {
-    static constexpr int kState = kCh * N;
-    float x[kCh][kRow], dt[kCh][kRow], dy[kCh][kRow];
+    static constexpr int kState = CH * N;
+    float x[CH][kRow], dt[CH][kRow], dy[CH][kRow];
     float B[kChunk][N], C[kChunk][N];
+    float A[kState], Al[kState], invA[kState];
+    // as they arrive: rows of x, dt and dy, A, bias and Dskip
+    unsigned char words[3][kChunk][CH * (int)sizeof(T) + 16];
+    float next_A[kState], next_bias[CH], next_Ds[CH];
 };
-template <int N>
-struct MainTile : Tile<N> {
-    float fac[kCh][kRow], dx[kCh][kRow];
-    float S[kPieces][Tile<N>::kState], R[kPieces][Tile<N>::kState], P[kPieces][Tile<N>::kState];
+template <typename T, int N, int CH>
+struct MainTile : Tile<T, N, CH> {
+    float fac[CH][kRow], dx[CH][kRow];
+    float S[kPieces][CH * N], R[kPieces][CH * N], P[kPieces][CH * N];
+    float Ds[CH];
+    int tiny;
 };
 
 struct Place {
@@ -196,33 +205,92 @@ __device__ __forceinline__ Place place(const BwdArgs &a) {
     return p;
 }
 
-// x, dt (prepared) and dy of a tile of channels as floats, tokens along a
-// row; channels and tokens past the end are zeros (dt = 0: a = 1, w = 0).
-template <typename T, int N, bool GRAD, int THREADS>
-__device__ __forceinline__ void stage_channels(const BwdArgs &a, const Place &p, int64_t d0,
-                                               int64_t dend, Tile<N> &s, float (*fac)[kRow]) {
-    const T *x = static_cast<const T *>(a.x), *dt = static_cast<const T *>(a.dt),
-            *dy = static_cast<const T *>(a.dy);
-    const int c = threadIdx.x % kCh;
-    const bool has = d0 + c < dend;
-    const float bias = (has && a.step.pre.bias) ? a.step.pre.bias[d0 + c] : 0.f;
-    const int64_t base = (p.b * a.L + p.t0) * a.D + d0 + c;
-    for (int t = threadIdx.x / kCh; t < kChunk; t += THREADS / kCh) {
-        float xv = 0.f, dv = 0.f, yv = 0.f, f = 0.f;
-        if (has && t < p.n) {
-            const int64_t off = base + t * a.D;
-            xv = to_f(x[off]);
-            yv = to_f(dy[off]);
-            dv = prepare_step<GRAD>(to_f(dt[off]), bias, a.step, f);
+__device__ __forceinline__ void copy4(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from)
+                 : "memory");
+}
+
+// Requests the rows of x, dt and dy of the tile at d0. Words that might leave
+// the tensor (its last tile; a bf16 tensor that starts inside a word) are not
+// requested: spread() then reads the tensors themselves.
+template <typename T, int CH>
+__device__ __forceinline__ bool by_words(const BwdArgs &a, const Place &p, int64_t d0) {
+    return sizeof(T) == 4 || (a.words && !(p.b == a.batch - 1 && p.chunk == a.nc - 1 &&
+                                           d0 + CH >= a.D));
+}
+template <typename T, int N, int CH, int THREADS>
+__device__ __forceinline__ void request(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
+                                        Tile<T, N, CH> &s) {
+    constexpr int kE = (int)sizeof(T), kWords = CH * kE / 4;  // of a row that starts on one
+    const void *const src[3] = {a.x, a.dt, a.dy};
+    if (by_words<T, CH>(a, p, d0)) {
+        const int len = (int)(dend - d0 < CH ? dend - d0 : CH);
+        const int i = threadIdx.x % kWords, t0 = threadIdx.x / kWords;
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            const uintptr_t row = reinterpret_cast<uintptr_t>(src[w]) +
+                                  kE * ((p.b * a.L + p.t0) * a.D + d0);
+            for (int t = t0; t < p.n; t += THREADS / kWords) {
+                const uintptr_t r = row + kE * (uintptr_t)(t * a.D);
+                const int words = ((int)(r & 3) + kE * len + 3) / 4;
+                if (i < words)
+                    copy4(&s.words[w][t][4 * i], reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * i));
+                if (kE == 2 && i == 0 && words > kWords)
+                    copy4(&s.words[w][t][4 * kWords],
+                          reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * kWords));
+            }
         }
-        s.x[c][t] = xv;
-        s.dt[c][t] = dv;
-        s.dy[c][t] = yv;
+    }
+    const int has = (int)(dend - d0 < CH ? dend - d0 : CH);
+    for (int i = threadIdx.x; i < has * N; i += THREADS) copy4(&s.next_A[i], a.A + d0 * N + i);
+    for (int i = threadIdx.x; i < has; i += THREADS) {
+        if (a.step.pre.bias) copy4(&s.next_bias[i], a.step.pre.bias + d0 + i);
+        if (a.Dskip) copy4(&s.next_Ds[i], a.Dskip + d0 + i);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// The requested tile as floats, dt prepared; channels and tokens past the end
+// are zeros (dt = 0: a = 1, w = 0). Also A and what follows from it.
+template <typename T, int N, int CH, bool ZOH, bool GRAD, int THREADS>
+__device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
+                                       Tile<T, N, CH> &s, float (*fac)[kRow]) {
+    const void *const src[3] = {a.x, a.dt, a.dy};
+    const bool words = by_words<T, CH>(a, p, d0);
+    const int c = threadIdx.x % CH;
+    const bool has = d0 + c < dend;
+    const float bias = (has && a.step.pre.bias) ? s.next_bias[c] : 0.f;
+    const int64_t base = (p.b * a.L + p.t0) * a.D + d0;
+    for (int t = threadIdx.x / CH; t < kChunk; t += THREADS / CH) {
+        float v[3] = {0.f, 0.f, 0.f}, f = 0.f;
+        if (has && t < p.n) {
+#pragma unroll
+            for (int w = 0; w < 3; ++w) {
+                const T *row = static_cast<const T *>(src[w]) + base + t * a.D;
+                if (words)
+                    row = reinterpret_cast<const T *>(&s.words[w][t][reinterpret_cast<uintptr_t>(row) & 3]);
+                v[w] = to_f(row[c]);
+            }
+            v[1] = prepare_step<GRAD>(v[1], bias, a.step, f);
+        }
+        s.x[c][t] = v[0];
+        s.dt[c][t] = v[1];
+        s.dy[c][t] = v[2];
         if (GRAD) fac[c][t] = f;
     }
+    bool tiny = false;
+    for (int i = threadIdx.x; i < CH * N; i += THREADS) {
+        float v = d0 + i / N < dend ? s.next_A[i] : -1.f;
+        if (ZOH) v = off_zero(v);
+        tiny = tiny || fabsf(v) < 0x1p-5f;
+        s.A[i] = v;
+        s.Al[i] = v * kLog2eB;
+        if (ZOH) s.invA[i] = 1.f / v;
+    }
+    return tiny;
 }
-template <typename T, int N, int THREADS>
-__device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Tile<N> &s) {
+template <typename T, int N, int CH, int THREADS>
+__device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Tile<T, N, CH> &s) {
     const T *B = static_cast<const T *>(a.B), *C = static_cast<const T *>(a.C);
     for (int i = threadIdx.x; i < kChunk * N; i += THREADS) {
         const int t = i / N, n = i % N;
@@ -261,8 +329,8 @@ __device__ __forceinline__ f2 times_decay(f2 v, f2 F) {
 
 // The map of a run of tokens for one thread's four states: end state S from
 // zero, gradient R handed to the left when none comes from the right, product P.
-template <int N, bool ZOH, int TOKENS>
-__device__ __forceinline__ void run_sums(const Tile<N> &s, int c, int t0, int n0,
+template <typename T, int N, int CH, bool ZOH, int TOKENS>
+__device__ __forceinline__ void run_sums(const Tile<T, N, CH> &s, int c, int t0, int n0,
                                          const Decay<ZOH> (&A)[2], f2 (&S)[2], f2 (&R)[2],
                                          f2 (&P)[2]) {
 #pragma unroll
@@ -292,50 +360,42 @@ __device__ __forceinline__ void run_sums(const Tile<N> &s, int c, int t0, int n0
     }
 }
 
-// A of a thread's states, 1 / A and whether any is too near zero for the
-// plain form of the hold's dA.
-template <int N, bool ZOH>
-__device__ __forceinline__ bool load_A(const BwdArgs &a, int64_t d, int n0, Decay<ZOH> (&A)[2],
-                                       f2 (&raw)[2], f2 (&invA)[2]) {
-    float v[kQ];
-    bool tiny = false;
-#pragma unroll
-    for (int k = 0; k < kQ; ++k) {
-        v[k] = a.A[d * N + n0 + k];
-        if (ZOH) v[k] = off_zero(v[k]);
-        tiny = tiny || fabsf(v[k]) < 0x1p-5f;
-    }
+template <typename T, int N, int CH, bool ZOH>
+__device__ __forceinline__ void load_A(const Tile<T, N, CH> &s, int at, Decay<ZOH> (&A)[2]) {
+    f2 v[2], l[2];
+    load4x(&s.A[at], v);
+    load4x(&s.Al[at], l);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        raw[k] = A[k].A = f2_pack(v[2 * k], v[2 * k + 1]);
-        A[k].Al = f2_mul(A[k].A, f2_both(kLog2eB));
-        invA[k] = ZOH ? f2_pack(1.f / v[2 * k], 1.f / v[2 * k + 1]) : 0;
+        A[k].A = v[k];
+        A[k].Al = l[k];
     }
-    return ZOH && tiny;
 }
 
 template <typename T, int N, bool ZOH>
 __global__ void __launch_bounds__(kCh *N / kQ) scan_bwd_sums(const BwdArgs a) {
-    constexpr int kThreads = kCh * N / kQ, kLanes = N / kQ;
+    constexpr int CH = kCh, kThreads = CH * N / kQ, kLanes = N / kQ;
     extern __shared__ __align__(16) unsigned char raw[];
-    Tile<N> &s = *reinterpret_cast<Tile<N> *>(raw);
+    Tile<T, N, CH> &s = *reinterpret_cast<Tile<T, N, CH> *>(raw);
     const Place p = place(a);
-    const int64_t dend = (p.g + 1) * a.gch;
-    stage_rows<T, N, kThreads>(a, p, s);
+    const int64_t dend = (p.g + 1) * a.gch, dstart = p.g * a.gch + (int64_t)p.tile0 * CH;
+    request<T, N, CH, kThreads>(a, p, dstart, dend, s);
+    stage_rows<T, N, CH, kThreads>(a, p, s);
     for (int k = 0; k < p.tiles; ++k) {
-        const int64_t d0 = p.g * a.gch + (int64_t)(p.tile0 + k) * kCh;
+        const int64_t d0 = dstart + (int64_t)k * CH;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        stage_channels<T, N, false, kThreads>(a, p, d0, dend, s, nullptr);
+        spread<T, N, CH, ZOH, false, kThreads>(a, p, d0, dend, s, nullptr);
         __syncthreads();
+        if (k + 1 < p.tiles) request<T, N, CH, kThreads>(a, p, d0 + CH, dend, s);
         const int c = threadIdx.x / kLanes, n0 = (threadIdx.x % kLanes) * kQ;
         const bool has = d0 + c < dend;
-        const int64_t d = has ? d0 + c : dend - 1;
         Decay<ZOH> A[2];
-        f2 v[2], invA[2], S[2], R[2], P[2];
-        load_A<N, ZOH>(a, d, n0, A, v, invA);
-        run_sums<N, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
+        f2 S[2], R[2], P[2];
+        load_A<T, N, CH, ZOH>(s, c * N + n0, A);
+        run_sums<T, N, CH, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
         if (has) {
-            const int64_t at = (p.b * a.nc + p.chunk) * a.D + d;
+            const int64_t at = (p.b * a.nc + p.chunk) * a.D + d0 + c;
             store4x(&a.S[at * N + n0], S);
             store4x(&a.R[at * N + n0], R);
             if (n0 == 0) {
@@ -443,10 +503,10 @@ __device__ __forceinline__ f2 slope(float dt, f2 A, f2 invA, f2 E) {
 }
 
 template <typename T, int N, bool ZOH>
-__global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a) {
-    constexpr int kLanes = N / kQ, kPerWarp = 32 / kLanes, kState = kCh * N;
+__global__ void __launch_bounds__(kMainThreads, 2) scan_bwd_main(const BwdArgs a) {
+    constexpr int CH = kCh, kLanes = N / kQ, kPerWarp = 32 / kLanes, kState = CH * N;
     extern __shared__ __align__(16) unsigned char raw[];
-    MainTile<N> &s = *reinterpret_cast<MainTile<N> *>(raw);
+    MainTile<T, N, CH> &s = *reinterpret_cast<MainTile<T, N, CH> *>(raw);
     const Place p = place(a);
     const int64_t dend = (p.g + 1) * a.gch;
     const int tid = threadIdx.x, lane = tid & 31, piece = tid >> 5;
@@ -457,53 +517,68 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
     for (int t = 0; t < kPiece; ++t)
 #pragma unroll
         for (int k = 0; k < 2; ++k) accB[t][k] = accC[t][k] = none;
-    stage_rows<T, N, kMainThreads>(a, p, s);
+    const int64_t dstart = p.g * a.gch + (int64_t)p.tile0 * CH;
+    request<T, N, CH, kMainThreads>(a, p, dstart, dend, s);
+    stage_rows<T, N, CH, kMainThreads>(a, p, s);
     for (int tile = 0; tile < p.tiles; ++tile) {
-        const int64_t d0 = p.g * a.gch + (int64_t)(p.tile0 + tile) * kCh;
+        const int64_t d0 = dstart + (int64_t)tile * CH;
         const int64_t row = (p.b * a.nc + p.chunk) * a.D;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (tid == 0) s.tiny = 0;
         __syncthreads();
-        stage_channels<T, N, true, kMainThreads>(a, p, d0, dend, s, s.fac);
-        // this thread's state of the chain over pieces
-        float h = 0.f, r = 0.f;
-        const bool chain = tid < kState && d0 + tid / N < dend;
-        if (chain) {
-            h = a.S[(row + d0) * N + tid];
-            r = a.R[(row + d0) * N + tid];
+        if (spread<T, N, CH, ZOH, true, kMainThreads>(a, p, d0, dend, s, s.fac)) s.tiny = 1;
+        if (tid < CH) s.Ds[tid] = (a.Dskip && d0 + tid < dend) ? s.next_Ds[tid] : 0.f;
+        // this thread's links of the chains over pieces
+        constexpr int kOwn = (kState + kMainThreads - 1) / kMainThreads;
+        float link_h[kOwn], link_r[kOwn];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int at = tid + i * kMainThreads;
+            const bool has = at < kState && d0 + at / N < dend;
+            link_h[i] = has ? a.S[(row + d0) * N + at] : 0.f;
+            link_r[i] = has ? a.R[(row + d0) * N + at] : 0.f;
         }
         __syncthreads();
+        if (tile + 1 < p.tiles) request<T, N, CH, kMainThreads>(a, p, d0 + CH, dend, s);
 #pragma unroll 1
-        for (int c = lane / kLanes; c < kCh; c += kPerWarp) {
+        for (int c = lane / kLanes; c < CH; c += kPerWarp) {
             Decay<ZOH> A[2];
-            f2 v[2], invA[2], S[2], R[2], P[2];
-            load_A<N, ZOH>(a, d0 + c < dend ? d0 + c : dend - 1, n0, A, v, invA);
-            run_sums<N, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
+            f2 S[2], R[2], P[2];
+            load_A<T, N, CH, ZOH>(s, c * N + n0, A);
+            run_sums<T, N, CH, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
             store4x(&s.S[piece][c * N + n0], S);
             store4x(&s.R[piece][c * N + n0], R);
             store4x(&s.P[piece][c * N + n0], P);
         }
         __syncthreads();
-        if (tid < kState) {
-#pragma unroll 4
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int at = tid + i * kMainThreads;
+            if (at >= kState) break;
+            float P[kPieces], S[kPieces], R[kPieces];
+#pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const float v = s.S[j][tid];
-                s.S[j][tid] = h;
-                h = fmaf(s.P[j][tid], h, v);
+                P[j] = s.P[j][at];
+                S[j] = s.S[j][at];
+                R[j] = s.R[j][at];
             }
-#pragma unroll 4
-            for (int j = kPieces - 1; j >= 0; --j) {
-                const float v = s.R[j][tid];
-                s.R[j][tid] = r;
-                r = fmaf(s.P[j][tid], r, v);
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                const int k = kPieces - 1 - j;
+                s.S[j][at] = link_h[i];
+                s.R[k][at] = link_r[i];
+                link_h[i] = fmaf(P[j], link_h[i], S[j]);
+                link_r[i] = fmaf(P[k], link_r[i], R[k]);
             }
         }
         __syncthreads();
 #pragma unroll 1
-        for (int c = lane / kLanes; c < kCh; c += kPerWarp) {
-            const int64_t d = d0 + c < dend ? d0 + c : dend - 1;
+        for (int c = lane / kLanes; c < CH; c += kPerWarp) {
             Decay<ZOH> A[2];
-            f2 An[2], invA[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
-            const bool tiny = load_A<N, ZOH>(a, d, n0, A, An, invA);
-            const float Ds = a.Dskip ? a.Dskip[d] : 0.f;
+            f2 invA[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
+            load_A<T, N, CH, ZOH>(s, c * N + n0, A);
+            load4x(&s.invA[c * N + n0], invA);
+            const float Ds = s.Ds[c];
             load4x(&s.S[piece][c * N + n0], st);
             load4x(&s.R[piece][c * N + n0], carry);
             const float4 x4 = *reinterpret_cast<const float4 *>(&s.x[c][t0]);
@@ -551,7 +626,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
                             if constexpr (decltype(near_zero)::value) {
                                 // term by term: dt a r h + r x B dw/dA
                                 dA[k] = f2_fma(f2_mul(ra, dt), f2_mul(before[t][k], invA[k]), dA[k]);
-                                dA2[k] = f2_fma(f2_mul(rv, in), slope(ds[t], An[k], invA[k], F[t][k]),
+                                dA2[k] = f2_fma(f2_mul(rv, in), slope(ds[t], A[k].A, invA[k], F[t][k]),
                                                 dA2[k]);
                             } else {
                                 dA[k] = f2_fma(dt, rt, dA[k]);
@@ -561,7 +636,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
                             const f2 t1 = f2_mul(ra, before[t][k]);
                             sB = f2_fma(rv, B[k], sB);
                             accB[t][k] = f2_fma(rv, u, accB[t][k]);
-                            sA = f2_fma(An[k], t1, sA);
+                            sA = f2_fma(A[k].A, t1, sA);
                             dA[k] = f2_fma(dt, t1, dA[k]);
                         }
                         carry[k] = ra;
@@ -573,7 +648,7 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
                     vA[t] = lo + hi;
                 }
             };
-            if (__any_sync(0xffffffffu, tiny)) {
+            if (ZOH && s.tiny) {
                 back(std::true_type{});
 #pragma unroll
                 for (int k = 0; k < 2; ++k) dA[k] = f2_add(dA[k], dA2[k]);
@@ -596,30 +671,35 @@ __global__ void __launch_bounds__(kMainThreads, 1) scan_bwd_main(const BwdArgs a
             store4x(&s.P[piece][c * N + n0], dA);
         }
         __syncthreads();
-        if (chain) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int at = tid + i * kMainThreads;
+            if (at >= kState || d0 + at / N >= dend) break;
             float v = 0.f;
 #pragma unroll
-            for (int j = 0; j < kPieces; ++j) v += s.P[j][tid];
-            a.dA_part[(row + d0) * N + tid] = v;
+            for (int j = 0; j < kPieces; ++j) v += s.P[j][at];
+            a.dA_part[(row + d0) * N + at] = v;
         }
-        for (int i = tid; i < kChunk * kCh; i += kMainThreads) {
-            const int t = i / kCh, c = i % kCh;
+        for (int i = tid; i < kChunk * CH; i += kMainThreads) {
+            const int t = i / CH, c = i % CH;
             if (t < p.n && d0 + c < dend) {
                 const int64_t off = (p.b * a.L + p.t0 + t) * a.D + d0 + c;
                 a.dx[off] = s.dx[c][t];
                 a.ddt[off] = s.fac[c][t];
             }
         }
-        // sums over the chunk's tokens: 16 lanes a channel
+        // sums over the chunk's tokens: eight lanes a channel
+        static_assert(kMainThreads == 8 * CH, "lanes of a channel");
         {
-            const int c = tid / 16, q = tid % 16;
+            const int c = tid / 8, q = tid % 8;
             float dd = 0.f, db = 0.f;
-            for (int t = q; t < kChunk; t += 16) {
+#pragma unroll
+            for (int t = q; t < kChunk; t += 8) {
                 dd = fmaf(s.x[c][t], s.dy[c][t], dd);
                 db += t < p.n ? s.fac[c][t] : 0.f;
             }
-            dd = lanes_sum<16>(dd);
-            db = lanes_sum<16>(db);
+            dd = lanes_sum<8>(dd);
+            db = lanes_sum<8>(db);
             if (q == 0 && d0 + c < dend) {
                 a.d_part[(row + d0 + c) * 2] = dd;
                 a.d_part[(row + d0 + c) * 2 + 1] = db;
@@ -684,17 +764,18 @@ __global__ void scan_bwd_params(const float *__restrict__ part, float *__restric
 
 int64_t chunks(const Problem &pr) { return (pr.seqlen + kChunk - 1) / kChunk; }
 
-// Tiles of channels that one CUDA block of the main kernel walks: as many as
-// leave four blocks for each SM, up to eight (fewer sums of dB and dC).
-void split(const Problem &pr, BwdArgs &a) {
+// Tiles of `ch` channels that one CUDA block walks: as many as leave four
+// blocks for each SM, up to `most` (fewer sums of dB and dC, inputs a tile ahead).
+void split(const Problem &pr, BwdArgs &a, int ch, int most) {
     a.gch = pr.nheads / pr.ngroups;
-    a.tiles_per_group = (int)((a.gch + kCh - 1) / kCh);
+    a.tiles_per_group = (int)((a.gch + ch - 1) / ch);
     const int64_t rows = pr.batch * chunks(pr) * pr.ngroups;
-    int k = 8;
+    int k = most;
     while (k > 1 && rows * ((a.tiles_per_group + k - 1) / k) < 4 * 148) --k;
     a.tiles_per_block = k;
     a.blocks_per_group = (a.tiles_per_group + k - 1) / k;
 }
+void split_main(const Problem &pr, BwdArgs &a) { split(pr, a, kCh, 8); }
 
 struct Carved {
     size_t S, R, steps, bc, dA, d, total;
@@ -722,8 +803,12 @@ template <typename T, int N, bool ZOH>
 cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *dh_final,
                    float *dA, float *dD, float *ddt_bias, float *dh0, cudaStream_t st) {
     cudaError_t e;
+    BwdArgs first = a;
+    split(pr, first, kCh, 8);
     const unsigned grid = (unsigned)(a.batch * a.nc * a.G * a.blocks_per_group);
-    const int sums_smem = (int)sizeof(Tile<N>), main_smem = (int)sizeof(MainTile<N>);
+    const unsigned first_grid = (unsigned)(a.batch * a.nc * a.G * first.blocks_per_group);
+    const int sums_smem = (int)sizeof(Tile<T, N, kCh>),
+              main_smem = (int)sizeof(MainTile<T, N, kCh>);
     if ((e = cudaFuncSetAttribute(scan_bwd_sums<T, N, ZOH>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, sums_smem)) !=
             cudaSuccess ||
@@ -732,7 +817,7 @@ cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *d
             cudaSuccess)
         return e;
     launch_begin("scan_bwd_sums", st);
-    scan_bwd_sums<T, N, ZOH><<<grid, kCh * N / kQ, sums_smem, st>>>(a);
+    scan_bwd_sums<T, N, ZOH><<<first_grid, kCh * N / kQ, sums_smem, st>>>(first);
     launch_end(st);
     const int64_t lanes = a.batch * a.D * N;
     launch_begin("scan_bwd_chain", st);
@@ -788,7 +873,7 @@ void softplus_preimage(double v, float (&out)[2]) {
 
 size_t scan_backward_workspace_bytes(const Problem &pr) {
     BwdArgs a;
-    split(pr, a);
+    split_main(pr, a);
     return carve(pr, a).total;
 }
 
@@ -811,7 +896,7 @@ ssd_status scan_backward_launch(const Problem &pr, const void *x, const void *dt
         return e == cudaSuccess ? SSD_OK : cuda_fail(e, "selective scan backward");
     }
     BwdArgs a;
-    split(pr, a);
+    split_main(pr, a);
     const Carved c = carve(pr, a);
     char *w = static_cast<char *>(ws);
     a.x = x;
@@ -836,6 +921,8 @@ ssd_status scan_backward_launch(const Problem &pr, const void *x, const void *dt
     a.D = pr.nheads;
     a.G = pr.ngroups;
     a.nc = chunks(pr);
+    a.words = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dt) |
+                reinterpret_cast<uintptr_t>(dy)) & 3) == 0;
     a.step.pre = DtPreArgs{pre.bias, pre.softplus, pre.zoh, pre.dt_min, pre.dt_max};
     a.step.on = pre.bias || pre.softplus || pre.dt_max > 0.f;
     for (int k = 0; k < 2; ++k) a.step.lo[k] = a.step.hi[k] = 0.f;

@@ -497,7 +497,7 @@ static ssd_status check_scan_backward_dims(const ssd_dims *dims) {
         return fail(SSD_ERR_UNSUPPORTED, "selective scan: dstate %lld: supported 4, 8, 16",
                     (long long)dims->dstate);
     // 32-bit grids over (batch, chunks, groups, channel tiles) and over states
-    const double chunks = (double)((dims->seqlen + 63) / 64);
+    const double chunks = (double)((dims->seqlen + 31) / 32);
     const double gch = (double)(dims->nheads / dims->ngroups);
     if (dims->batch > 65535 || dims->seqlen > (int64_t)1 << 30 ||
         dims->nheads > (int64_t)1 << 24 ||
