@@ -39,6 +39,7 @@
 // tells the others and all return.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "gated.cuh"
@@ -1099,33 +1100,50 @@ __global__ void gated_open_kernel(const GatedArgs a, int64_t ends, int64_t maps)
     if (2 * i < maps) reinterpret_cast<ulonglong2 *>(a.maps)[i] = empty;
 }
 
-// Thread blocks of a persistent kernel: as many as fit, fewer where there are
-// fewer tiles; with one block of tokens one per tile.
-template <typename F>
-cudaError_t start(const char *name, F *kernel, size_t smem, GatedArgs a, const Maps &maps,
-                  cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    int per_sm = 1, dev = 0, sms = 0;
+// Thread blocks of K that fit the current device (0: an error), found once for
+// each device; the kernel's shared memory is allowed on the way.
+template <auto K>
+int resident_blocks(size_t smem, cudaError_t *err) {
+    static std::atomic<int> known[64];
+    int dev = 0, per_sm = 0, sms = 0;
+    if ((*err = cudaGetDevice(&dev)) != cudaSuccess) return 0;
+    if (dev < 64) {
+        const int n = known[dev].load(std::memory_order_relaxed);
+        if (n > 0) return n;
+    }
+    if ((*err = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+            cudaSuccess ||
+        (*err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (*err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, K, kThreads, smem)) !=
+            cudaSuccess)
+        return 0;
+    if (per_sm < 1) per_sm = 1;
+    if (dev < 64) known[dev].store(per_sm * sms, std::memory_order_relaxed);
+    return per_sm * sms;
+}
+
+// A persistent kernel's launch: as many thread blocks as fit, fewer where there
+// are fewer tiles; with one block of tokens one per tile.
+template <auto K>
+cudaError_t start(const char *name, size_t smem, GatedArgs a, const Maps &maps, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
     const int64_t lanes = a.batch * a.dblocks, tiles = lanes * a.nb;
     int64_t grid = tiles, ends = 0, words = 0;
-    if (e == cudaSuccess && a.nb > 1) {
-        if ((e = cudaGetDevice(&dev)) == cudaSuccess &&
-            (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
-        if (e == cudaSuccess && (int64_t)per_sm * sms < grid) grid = (int64_t)per_sm * sms;
+    const int64_t fit = resident_blocks<K>(smem, &e);
+    if (e != cudaSuccess) return e;
+    if (a.nb > 1) {
+        if (fit < grid) grid = fit;
         a.eager = lanes >= grid;
         ends = (a.eager ? tiles : lanes * (a.nb / kGroup)) * 32;
         words = a.eager ? 0 : tiles * 64;
     }
-    if (e != cudaSuccess) return e;
     int64_t n = ends > words ? ends / 2 : words / 2;
     if (n < a.D) n = a.D;
     launch_begin("gated_open", st);
     gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, ends, words);
     launch_end(st);
     launch_begin(name, st);
-    kernel<<<(unsigned)grid, kThreads, smem, st>>>(a, maps);
+    K<<<(unsigned)grid, kThreads, smem, st>>>(a, maps);
     launch_end(st);
     return cudaGetLastError();
 }
@@ -1165,8 +1183,8 @@ bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
 template <typename T, bool ALIGNED>
 cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     const size_t smem = Stage<T, ALIGNED, 3>::kBytes;
-    return a.q ? start("gated_forward", gated_forward_kernel<T, ALIGNED, true>, smem, a, maps, st)
-               : start("gated_forward", gated_forward_kernel<T, ALIGNED, false>, smem, a, maps, st);
+    return a.q ? start<gated_forward_kernel<T, ALIGNED, true>>("gated_forward", smem, a, maps, st)
+               : start<gated_forward_kernel<T, ALIGNED, false>>("gated_forward", smem, a, maps, st);
 }
 template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
@@ -1179,10 +1197,11 @@ cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
 
 template <typename T, bool ALIGNED>
 cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
-    return a.q ? start("gated_backward", gated_backward_kernel<T, ALIGNED, true>,
-                       Stage<T, ALIGNED, 1>::kBytes + Stage<int8_t, ALIGNED, 3>::kBytes, a, maps, st)
-               : start("gated_backward", gated_backward_kernel<T, ALIGNED, false>,
-                       Stage<T, ALIGNED, 4>::kBytes, a, maps, st);
+    return a.q ? start<gated_backward_kernel<T, ALIGNED, true>>(
+                     "gated_backward",
+                     Stage<T, ALIGNED, 1>::kBytes + Stage<int8_t, ALIGNED, 3>::kBytes, a, maps, st)
+               : start<gated_backward_kernel<T, ALIGNED, false>>(
+                     "gated_backward", Stage<T, ALIGNED, 4>::kBytes, a, maps, st);
 }
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {

@@ -257,26 +257,32 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
                                        Tile<T, N, CH> &s, float (*fac)[kRow]) {
     const void *const src[3] = {a.x, a.dt, a.dy};
     const bool words = by_words<T, CH>(a, p, d0);
-    const int c = threadIdx.x % CH;
-    const bool has = d0 + c < dend;
-    const float bias = (has && a.step.pre.bias) ? s.next_bias[c] : 0.f;
+    // eight channels by four runs of four tokens a warp: rows are written 16 bytes at a time
     const int64_t base = (p.b * a.L + p.t0) * a.D + d0;
-    for (int t = threadIdx.x / CH; t < kChunk; t += THREADS / CH) {
-        float v[3] = {0.f, 0.f, 0.f}, f = 0.f;
-        if (has && t < p.n) {
+    for (int i = threadIdx.x; i < CH * (kChunk / 4); i += THREADS) {
+        const int c = (i / 8 / (kChunk / 4)) * 8 + i % 8, t0 = (i / 8) % (kChunk / 4) * 4;
+        const bool has = d0 + c < dend;
+        const float bias = (has && a.step.pre.bias) ? s.next_bias[c] : 0.f;
+        float v[3][4], f[4];
 #pragma unroll
-            for (int w = 0; w < 3; ++w) {
-                const T *row = static_cast<const T *>(src[w]) + base + t * a.D;
-                if (words)
-                    row = reinterpret_cast<const T *>(&s.words[w][t][reinterpret_cast<uintptr_t>(row) & 3]);
-                v[w] = to_f(row[c]);
+        for (int j = 0; j < 4; ++j) {
+            f[j] = v[0][j] = v[1][j] = v[2][j] = 0.f;
+            if (has && t0 + j < p.n) {
+#pragma unroll
+                for (int w = 0; w < 3; ++w) {
+                    const T *row = static_cast<const T *>(src[w]) + base + (t0 + j) * a.D;
+                    if (words)
+                        row = reinterpret_cast<const T *>(
+                            &s.words[w][t0 + j][reinterpret_cast<uintptr_t>(row) & 3]);
+                    v[w][j] = to_f(row[c]);
+                }
+                v[1][j] = prepare_step<GRAD>(v[1][j], bias, a.step, f[j]);
             }
-            v[1] = prepare_step<GRAD>(v[1], bias, a.step, f);
         }
-        s.x[c][t] = v[0];
-        s.dt[c][t] = v[1];
-        s.dy[c][t] = v[2];
-        if (GRAD) fac[c][t] = f;
+        *reinterpret_cast<float4 *>(&s.x[c][t0]) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+        *reinterpret_cast<float4 *>(&s.dt[c][t0]) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+        *reinterpret_cast<float4 *>(&s.dy[c][t0]) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
+        if (GRAD) *reinterpret_cast<float4 *>(&fac[c][t0]) = make_float4(f[0], f[1], f[2], f[3]);
     }
     bool tiny = false;
     for (int i = threadIdx.x; i < CH * N; i += THREADS) {
@@ -427,19 +433,29 @@ scan_bwd_chain(const BwdArgs a, const float *h0, const float *dh_final, float *d
     const float *steps = a.steps + c0 * a.D + dn / N;
     float h = first ? first[i] : 0.f;
     if (ZOH && !back) h *= A;
-    for (int64_t j0 = 0; j0 < a.nc; j0 += kBatch) {
-        float v[kBatch], t[kBatch];
+    float v[kBatch], t[kBatch];
+    auto load = [&](int64_t j0) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const bool has = j0 + j < a.nc;
-            v[j] = has ? S[way * (j0 + j) * lane_len] : 0.f;
-            t[j] = has ? steps[way * (j0 + j) * a.D] : 0.f;
+            v[j] = has ? __ldcg(S + way * (j0 + j) * lane_len) : 0.f;
+            t[j] = has ? __ldcg(steps + way * (j0 + j) * a.D) : 0.f;
         }
+    };
+    load(0);
+    for (int64_t j0 = 0; j0 < a.nc; j0 += kBatch) {
+        float e[kBatch], u[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            e[j] = t[j];
+            u[j] = v[j];
+        }
+        if (j0 + kBatch < a.nc) load(j0 + kBatch);  // the next batch is on its way
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (j0 + j >= a.nc) break;
             S[way * (j0 + j) * lane_len] = h;
-            h = fmaf(tc::fast_exp2(t[j] * Al), h, v[j]);
+            h = fmaf(tc::fast_exp2(e[j] * Al), h, u[j]);
         }
     }
     if (back && dh0) dh0[i] = h;
