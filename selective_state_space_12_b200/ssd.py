@@ -9,6 +9,7 @@ do not allocate inside the library.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -340,41 +341,78 @@ def ssd_selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tens
     N = A.shape[1]
     G = B.shape[2]
     dev, io = x.device, x.dtype
-    for name, t, shape, dtype in (("x", x, (batch, L, Dc), io), ("dt", dt, (batch, L, Dc), io),
-                                  ("A", A, (Dc, N), torch.float32),
-                                  ("B", B, (batch, L, G, N), io), ("C", C, (batch, L, G, N), io),
-                                  ("dy", dy, (batch, L, Dc), io)):
-        _check_tensor(name, t, shape, dtype, dev)
+    _check_all((("x", x), ("dt", dt), ("dy", dy)), (batch, L, Dc), io, dev)
+    _check_all((("A", A),), (Dc, N), torch.float32, dev)
+    _check_all((("B", B), ("C", C)), (batch, L, G, N), io, dev)
     for name, t in (("Dskip", Dskip), ("dt_bias", dt_bias)):
         if t is not None:
-            _check_tensor(name, t, (Dc,), torch.float32, dev)
+            _check_all(((name, t),), (Dc,), torch.float32, dev)
     for name, t in (("h0", h0), ("dh_final", dh_final)):
         if t is not None:
-            _check_tensor(name, t, (batch, Dc, N), torch.float32, dev)
+            _check_all(((name, t),), (batch, Dc, N), torch.float32, dev)
     f = dict(dtype=torch.float32, device=dev)
+    dims, need = _call_sizes(batch, L, Dc, N, G, io, "ssd_selective_scan_backward_workspace_size")
     out = dict(dx=torch.empty((batch, L, Dc), **f), ddt=torch.empty((batch, L, Dc), **f),
                dA=torch.empty((Dc, N), **f), dB=torch.empty((batch, L, G, N), **f),
                dC=torch.empty((batch, L, G, N), **f), dD=torch.empty((Dc,), **f),
                ddt_bias=torch.empty((Dc,), **f),
                dh0=torch.empty((batch, Dc, N), **f) if want_dh0 else None)
-    dims = make_dims(batch, L, Dc, 1, N, G, io)
     opts = make_options(dt_bias, dt_softplus, dt_limit, zoh)
-    need = int(lib.ssd_selective_scan_backward_workspace_size(ctypes.byref(dims)))
     workspace, ws_given = _workspace(need, workspace, dev)
-    with torch.cuda.device(dev):
-        st = lib.ssd_selective_scan_backward(
-            _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(h0), _ptr(dy),
-            _ptr(dh_final), *[_ptr(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD",
-                                                     "ddt_bias", "dh0")],
-            ctypes.byref(dims), ctypes.byref(opts), _ptr(workspace), ws_given,
-            _stream_handle(stream, dev))
-    if st != _lib.SSD_OK:
-        raise SSDError(st, "ssd_selective_scan_backward")
+    _call(lib.ssd_selective_scan_backward, dev, stream, "ssd_selective_scan_backward", _at(x),
+          _at(dt), _at(A), _at(B), _at(C), _at(Dskip), _at(h0), _at(dy), _at(dh_final),
+          *[_at(out[k]) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0")], dims,
+          ctypes.byref(opts), _at(workspace), ws_given)
     return out
 
 
-def _gated_dims(batch, L, D, dtype) -> _lib.Dims:
-    return make_dims(batch, L, D, 1, 1, 1, dtype)
+# The elementwise recurrences are called with small tensors too, where the host's
+# time is the call's: sizes are marshalled once (by value), addresses go to ctypes
+# as integers, and the device is only entered when it is not the current one.
+
+@functools.lru_cache(maxsize=1024)
+def _call_sizes(batch, L, channels, dstate, ngroups, dtype, size_fn):
+    """(dims by reference, workspace bytes) of a call; size_fn names the entry
+    point that gives the latter."""
+    dims = make_dims(batch, L, channels, 1, dstate, ngroups, dtype)
+    ref = ctypes.byref(dims)
+    return ref, int(getattr(_lib.load(), size_fn)(ref)) if size_fn else 0
+
+
+def _check_all(tensors, shape, dtype, device):
+    """_check_tensor of several tensors of one shape and type."""
+    index = device.index
+    for name, t in tensors:
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.is_cuda and t.get_device() == index and t.is_contiguous()):
+            _check_tensor(name, t, shape, dtype, device)
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, device, stream, where, *args):
+    """fn(*args, stream) on the device."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != _lib.SSD_OK:
+        raise SSDError(st, where)
 
 
 def gated_blocks(seqlen: int) -> int:
@@ -410,7 +448,7 @@ def _check_reset(reset, batch, L, dev):
     if reset is not None:
         if reset.dtype == torch.bool:
             raise TypeError("reset must be uint8 (use reset.view(torch.uint8))")
-        _check_tensor("reset", reset, (batch, L), torch.uint8, dev)
+        _check_all((("reset", reset),), (batch, L), torch.uint8, dev)
 
 
 def _workspace(need: int, workspace: Optional[torch.Tensor], dev):
@@ -444,39 +482,34 @@ def ssd_gated_scan(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch
     lib = _lib.load()
     batch, L, D = x.shape
     dev, io = x.device, x.dtype
-    for name, t in (("x", x), ("r", r), ("i", i)):
-        _check_tensor(name, t, (batch, L, D), io, dev)
-    _check_tensor("lam", lam, (D,), torch.float32, dev)
+    _check_all((("x", x), ("r", r), ("i", i)), (batch, L, D), io, dev)
+    _check_all((("lam", lam),), (D,), torch.float32, dev)
     _check_reset(reset, batch, L, dev)
     if h0 is not None:
-        _check_tensor("h0", h0, (batch, D), torch.float32, dev)
-    dims = _gated_dims(batch, L, D, io)
+        _check_all((("h0", h0),), (batch, D), torch.float32, dev)
     nb = gated_blocks(L)
     q = e = None
     if checkpoint is not None:
         if states is not None:
             raise ValueError("give states or a checkpoint (which holds them), not both")
         states, q, e = checkpoint.states, checkpoint.q, checkpoint.e
-        _check_tensor("checkpoint.q", q, (3, batch, L, D), torch.int8, dev)
-        _check_tensor("checkpoint.e", e, (3, batch, nb, D), torch.uint8, dev)
+        _check_all((("checkpoint.q", q),), (3, batch, L, D), torch.int8, dev)
+        _check_all((("checkpoint.e", e),), (3, batch, nb, D), torch.uint8, dev)
     if states is not None:
-        _check_tensor("states", states, (batch, nb, D), torch.float32, dev)
+        _check_all((("states", states),), (batch, nb, D), torch.float32, dev)
+    dims, need = _call_sizes(batch, L, D, 1, 1, io, "ssd_gated_scan_workspace_size")
     if y is None:
         y = torch.empty_like(x)
-    _check_tensor("y", y, (batch, L, D), io, dev)
-    if h_final is None and want_final:
-        h_final = torch.empty((batch, D), dtype=torch.float32, device=dev)
+    else:
+        _check_all((("y", y),), (batch, L, D), io, dev)
     if h_final is not None:
-        _check_tensor("h_final", h_final, (batch, D), torch.float32, dev)
-    need = int(lib.ssd_gated_scan_workspace_size(ctypes.byref(dims)))
+        _check_all((("h_final", h_final),), (batch, D), torch.float32, dev)
+    elif want_final:
+        h_final = torch.empty((batch, D), dtype=torch.float32, device=dev)
     workspace, ws_given = _workspace(need, workspace, dev)
-    with torch.cuda.device(dev):
-        st = lib.ssd_gated_scan(_ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(c), _ptr(reset),
-                                _ptr(h0), _ptr(y), _ptr(h_final), _ptr(states), _ptr(q), _ptr(e),
-                                ctypes.byref(dims), _ptr(workspace), ws_given,
-                                _stream_handle(stream, dev))
-    if st != _lib.SSD_OK:
-        raise SSDError(st, "ssd_gated_scan")
+    _call(lib.ssd_gated_scan, dev, stream, "ssd_gated_scan", _at(x), _at(r), _at(i), _at(lam),
+          float(c), _at(reset), _at(h0), _at(y), _at(h_final), _at(states), _at(q), _at(e), dims,
+          _at(workspace), ws_given)
     return y, h_final
 
 
@@ -488,33 +521,26 @@ def _gated_backward(x, r, i, ckpt, lam, states, dy, dh_final, c, reset, want_dh0
     nb = gated_blocks(L)
     q = e = None
     if ckpt is None:
-        for name, t in (("x", x), ("r", r), ("i", i)):
-            _check_tensor(name, t, (batch, L, D), io, dev)
+        _check_all((("x", x), ("r", r), ("i", i)), (batch, L, D), io, dev)
     else:
         states, q, e = ckpt.states, ckpt.q, ckpt.e
-        _check_tensor("checkpoint.q", q, (3, batch, L, D), torch.int8, dev)
-        _check_tensor("checkpoint.e", e, (3, batch, nb, D), torch.uint8, dev)
-    _check_tensor("states", states, (batch, nb, D), torch.float32, dev)
-    _check_tensor("dy", dy, (batch, L, D), io, dev)
-    _check_tensor("lam", lam, (D,), torch.float32, dev)
+        _check_all((("checkpoint.q", q),), (3, batch, L, D), torch.int8, dev)
+        _check_all((("checkpoint.e", e),), (3, batch, nb, D), torch.uint8, dev)
+    _check_all((("states", states),), (batch, nb, D), torch.float32, dev)
+    _check_all((("dy", dy),), (batch, L, D), io, dev)
+    _check_all((("lam", lam),), (D,), torch.float32, dev)
     _check_reset(reset, batch, L, dev)
     if dh_final is not None:
-        _check_tensor("dh_final", dh_final, (batch, D), torch.float32, dev)
-    dims = _gated_dims(batch, L, D, io)
+        _check_all((("dh_final", dh_final),), (batch, D), torch.float32, dev)
+    dims, need = _call_sizes(batch, L, D, 1, 1, io, "ssd_gated_scan_backward_workspace_size")
     out = dict(dx=torch.empty_like(dy), dr=torch.empty_like(dy), di=torch.empty_like(dy),
                dlam=torch.empty_like(lam),
                dh0=torch.empty((batch, D), dtype=torch.float32, device=dev) if want_dh0 else None)
-    need = int(lib.ssd_gated_scan_backward_workspace_size(ctypes.byref(dims)))
     workspace, ws_given = _workspace(need, workspace, dev)
-    with torch.cuda.device(dev):
-        st = lib.ssd_gated_scan_backward(_ptr(x), _ptr(r), _ptr(i), _ptr(q), _ptr(e), _ptr(lam),
-                                         float(c), _ptr(reset), _ptr(states), _ptr(dy),
-                                         _ptr(dh_final), _ptr(out["dx"]), _ptr(out["dr"]),
-                                         _ptr(out["di"]), _ptr(out["dlam"]), _ptr(out["dh0"]),
-                                         ctypes.byref(dims), _ptr(workspace), ws_given,
-                                         _stream_handle(stream, dev))
-    if st != _lib.SSD_OK:
-        raise SSDError(st, where)
+    _call(lib.ssd_gated_scan_backward, dev, stream, where, _at(x), _at(r), _at(i), _at(q), _at(e),
+          _at(lam), float(c), _at(reset), _at(states), _at(dy), _at(dh_final), _at(out["dx"]),
+          _at(out["dr"]), _at(out["di"]), _at(out["dlam"]), _at(out["dh0"]), dims, _at(workspace),
+          ws_given)
     return out
 
 
@@ -552,19 +578,16 @@ def ssd_gated_step(h: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.T
     lib = _lib.load()
     batch, D = h.shape
     dev, io = x.device, x.dtype
-    _check_tensor("h", h, (batch, D), torch.float32, dev)
-    for name, t in (("x", x), ("r", r), ("i", i)):
-        _check_tensor(name, t, (batch, D), io, dev)
-    _check_tensor("lam", lam, (D,), torch.float32, dev)
+    _check_all((("h", h),), (batch, D), torch.float32, dev)
+    _check_all((("x", x), ("r", r), ("i", i)), (batch, D), io, dev)
+    _check_all((("lam", lam),), (D,), torch.float32, dev)
     if y is None:
         y = torch.empty_like(x)
-    _check_tensor("y", y, (batch, D), io, dev)
-    dims = _gated_dims(batch, 1, D, io)
-    with torch.cuda.device(dev):
-        st = lib.ssd_gated_step(_ptr(h), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), float(c), _ptr(y),
-                                ctypes.byref(dims), _stream_handle(stream, dev))
-    if st != _lib.SSD_OK:
-        raise SSDError(st, "ssd_gated_step")
+    else:
+        _check_all((("y", y),), (batch, D), io, dev)
+    dims, _ = _call_sizes(batch, 1, D, 1, 1, io, None)
+    _call(lib.ssd_gated_step, dev, stream, "ssd_gated_step", _at(h), _at(x), _at(r), _at(i),
+          _at(lam), float(c), _at(y), dims)
     return y
 
 
