@@ -188,11 +188,12 @@ struct Maps {
     CUtensorMap m[4];
 };
 
-template <typename T, bool ALIGNED, int TENSORS>
+template <typename T, bool ALIGNED, int TENSORS, int KEEP = 0>
 struct Stage {
     using P = typename Pair<T>::type;
     static constexpr int kPitch = kTileCh * (int)sizeof(T) + (ALIGNED ? 0 : 16);
-    static constexpr int kWarpBytes = TENSORS * kRun * kPitch;
+    static constexpr int kRowsBytes = TENSORS * kRun * kPitch;
+    static constexpr int kWarpBytes = kRowsBytes > KEEP ? kRowsBytes : KEEP;
     static constexpr size_t kBytes = (size_t)kWarps * kWarpBytes;
 
     unsigned char *buf;  // this warp's rows
@@ -208,9 +209,13 @@ struct Stage {
         const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
         __syncwarp();  // the rows have been read
         if constexpr (ALIGNED) {
+            if (KEEP > 0) {  // what was kept there was written by ordinary stores
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+            }
             if (lane == 0) {
                 const bool any = tok0 < t.n;
-                tc::mbar_arrive_expect_tx(bar, any ? kWarpBytes : 0);
+                tc::mbar_arrive_expect_tx(bar, any ? kRowsBytes : 0);
                 if (any) {
 #pragma unroll
                     for (int w = 0; w < TENSORS; ++w)
@@ -536,7 +541,7 @@ __device__ __forceinline__ unsigned round_on(unsigned ticket) {
 // finds what enters it, hands every run what enters that, and publishes what
 // leaves. While the others compute a tile it fetches the next ticket and
 // prepares the next tile's gate scales.
-template <typename T, bool ALIGNED, bool CK, bool BACK>
+template <typename T, bool ALIGNED, bool CK, bool BACK, bool EAGER>
 __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsigned tiles,
                                            int64_t lanes) {
     const int lane = threadIdx.x & 31;
@@ -558,15 +563,15 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         const Tile t = tile_of<BACK>(a, now);
         const unsigned step = (unsigned)(BACK ? a.nb - 1 - t.blk : t.blk);
         unsigned after = tiles;
-        if (a.eager && next < tiles) {
+        if (EAGER && next < tiles) {
             if (lane == 0) after = atomicAdd(a.counter, 1u);
             after = __shfl_sync(0xffffffffu, after, 0);
         }
         const int pos = (int)(step % kGroup);
-        const bool leaves = a.eager || pos == kGroup - 1;  // publishes what leaves it
-        const bool waits = a.eager ? step > 0 : step >= kGroup;
+        const bool leaves = EAGER || pos == kGroup - 1;  // publishes what leaves it
+        const bool waits = EAGER ? step > 0 : step >= kGroup;
         const int64_t slot =
-            a.eager ? t.id : (int64_t)(step / kGroup) * lanes + t.id % (unsigned)lanes;
+            EAGER ? t.id : (int64_t)(step / kGroup) * lanes + t.id % (unsigned)lanes;
         f2 in = 0, h = 0;
         word before = kEmpty;
         if (waits) before = load_word(&a.ends[(slot - lanes) * 32 + lane]);
@@ -594,7 +599,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = then(all, m[BACK ? kWarps - 1 - w : w]);
         bool ok = true;
-        if (chained && !a.eager) {
+        if (chained && !EAGER) {
             if (pos < kGroup - 1 && step + 1 < a.nb) {
                 store_word(&a.maps[(t.id * 32 + lane) * 2], all.x, all.y);
                 store_word(&a.maps[(t.id * 32 + lane) * 2 + 1], all.z, all.w);
@@ -643,10 +648,10 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
                 }
             }
         }
-        if (a.eager && lane == 0) s.tile[n & 1] = tile_of<BACK>(a, after);
+        if (EAGER && lane == 0) s.tile[n & 1] = tile_of<BACK>(a, after);
         __syncwarp();
         bar_arrive(kEntryReady);
-        if (chained && !a.eager) {
+        if (chained && !EAGER) {
             if (lane == 0) next = atomicAdd(a.counter, 1u);
             next = __shfl_sync(0xffffffffu, next, 0);
             if (lane < 2) (lane ? s.later : s.tile[0]) = tile_of<BACK>(a, lane ? round_on(next) : next);
@@ -668,14 +673,14 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
 }
 
 // The first tickets of this thread block, and its barriers.
-template <bool ALIGNED, bool BACK>
+template <bool BACK, bool EAGER>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
     if (threadIdx.x == 0) {
         s.stop[0] = s.stop[1] = 0;
         // one block of tokens: a tile a thread block
         const unsigned first = a.nb > 1 ? atomicAdd(a.counter, 1u) : blockIdx.x;
         s.tile[0] = tile_of<BACK>(a, first);
-        s.tile[1] = tile_of<BACK>(a, a.eager ? atomicAdd(a.counter, 1u) : tiles);
+        s.tile[1] = tile_of<BACK>(a, EAGER ? atomicAdd(a.counter, 1u) : tiles);
         s.later = tile_of<BACK>(a, round_on(first));
         for (int w = 0; w < 2 * kWarps; ++w) tc::mbar_init(&s.bars[w], 1);
         tc::fence_mbar_init();
@@ -690,20 +695,24 @@ struct AnyRun : std::false_type {};
 
 // ------------------------------------------------------------ forward
 
-template <typename T, bool ALIGNED, bool CK>
-__global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
+// Bytes that a warp keeps in its rows' place while it waits: a and u.
+template <bool CK, bool EAGER>
+constexpr int kForwardKeep = !EAGER && !CK ? 2 * kRun * 32 * 8 : 0;
+
+template <typename T, bool ALIGNED, bool CK, bool EAGER>
+__global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<ALIGNED, false>(a, s, tiles);
+    open_block<false, EAGER>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<T, ALIGNED, CK, false>(a, s, tiles, lanes);
+        chain_warp<T, ALIGNED, CK, false, EAGER>(a, s, tiles, lanes);
         return;
     }
-    Stage<T, ALIGNED, 3> in(staged, s.bars);
+    Stage<T, ALIGNED, 3, kForwardKeep<CK, EAGER>> in(staged, s.bars);
     const void *const src[3] = {a.x, a.r, a.i};
     const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
     Tile t = s.tile[0];
@@ -762,6 +771,18 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
             }
         }
         s.maps[warp][lane] = as_map(P, H);
+        // without a ticket ahead the rows' place is free: a and u wait there, so that more
+        // thread blocks fit
+        f2 *const keep = reinterpret_cast<f2 *>(in.buf) + lane;
+        constexpr bool kKeep = !EAGER && !CK;
+        if (kKeep) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) {
+                keep[2 * j * 32] = av[j];
+                keep[(2 * j + 1) * 32] = u[j];
+            }
+        }
         bar_arrive(kMapsReady);
         Tile tn;
         f2 kn = k;
@@ -771,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
             kn = gate_scales<ALIGNED>(a, tn.d0);
         };
         ahead = false;
-        if (a.eager) {
+        if (EAGER) {
             tn = s.tile[(n + 1) & 1];
             ahead = here && tn.id < tiles;
             if (ahead) advance();
@@ -787,13 +808,14 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
             int64_t off = 0;
 #pragma unroll
             for (int j = 0; j < kRun; ++j, off += a.D) {
-                h = f2_fma(av[j], h, u[j]);
+                h = f2_fma(kKeep ? keep[2 * j * 32] : av[j], h, kKeep ? keep[(2 * j + 1) * 32] : u[j]);
                 y.put(off, h);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                h = (marks >> j & 1) ? u[j] : f2_fma(av[j], h, u[j]);
+                const f2 uj = kKeep ? keep[(2 * j + 1) * 32] : u[j];
+                h = (marks >> j & 1) ? uj : f2_fma(kKeep ? keep[2 * j * 32] : av[j], h, uj);
                 if (j < left) y.put(j * a.D, h);
             }
         }
@@ -830,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : 3) gated_forward_kernel(
                 }
             }
         }
-        if (chained && !a.eager) {
+        if (chained && !EAGER) {
             bar_sync(kTicketReady);
             tn = s.tile[0];
             ahead = tn.id < tiles;
@@ -854,7 +876,7 @@ __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w
                    t.d0 + c1 < a.D ? __uint_as_float((uint32_t)e[c1] << 23) : 0.f);
 }
 
-template <typename T, bool ALIGNED, bool CK>
+template <typename T, bool ALIGNED, bool CK, bool EAGER>
 __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
@@ -864,9 +886,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<ALIGNED, true>(a, s, tiles);
+    open_block<true, EAGER>(a, s, tiles);
     if (warp == kWarps) {
-        chain_warp<T, ALIGNED, CK, true>(a, s, tiles, lanes);
+        chain_warp<T, ALIGNED, CK, true, EAGER>(a, s, tiles, lanes);
         return;
     }
     using In = Stage<T, ALIGNED, kIn>;
@@ -971,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
             kn = gate_scales<ALIGNED>(a, tn.d0);
         };
         ahead = false;
-        if (a.eager) {
+        if (EAGER) {
             tn = s.tile[(n + 1) & 1];
             ahead = here && tn.id < tiles;
             if (ahead) advance();
@@ -1014,18 +1036,19 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 Gate2 g;
                 decay_from2(F[j], g);
                 const f2 x = CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]);
-                const f2 vx = f2_mul(si[j], x);  // sigmoid(i) x
+                const f2 srj = sr[j], sij = si[j];
+                const f2 vx = f2_mul(sij, x);  // sigmoid(i) x
                 const f2 gm = cut ? G[j] : f2_mul(G[j], g.m);
                 // q dm/dq = q a^2 / m: finite where q -> 0
-                const f2 qa = f2_mul(f2_mul(k, sr[j]), g.a);
+                const f2 qa = f2_mul(f2_mul(k, srj), g.a);
                 const f2 e = cut ? none
                                  : f2_mul(f2_mul(G[j], qa),
                                           f2_sub(f2_mul(f2_mul(g.a, g.rm), vx), h));
                 dl = f2_add(dl, e);
                 const f2 gv = f2_mul(gm, vx);
-                dx.put(off, f2_mul(gm, si[j]));
-                dr.put(off, f2_mul(e, f2_sub(one, sr[j])));
-                di.put(off, f2_mul(gv, f2_sub(one, si[j])));
+                dx.put(off, f2_mul(gm, sij));
+                dr.put(off, f2_mul(e, f2_sub(one, srj)));
+                di.put(off, f2_mul(gv, f2_sub(one, sij)));
                 h = cut ? vx : f2_fma(g.a, h, f2_mul(g.m, vx));
             }
         };
@@ -1035,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         f2_unpack(dl, dw.x, dw.y);
         s.dlam[n & 1][warp][channel<ALIGNED>(0)] = dw.x;
         s.dlam[n & 1][warp][channel<ALIGNED>(1)] = dw.y;
-        if (chained && !a.eager) {
+        if (chained && !EAGER) {
             bar_sync(kTicketReady);
             tn = s.tile[0];
             ahead = tn.id < tiles;
@@ -1125,7 +1148,8 @@ int resident_blocks(size_t smem, cudaError_t *err) {
 // A persistent kernel's launch: as many thread blocks as fit, fewer where there
 // are fewer tiles; with one block of tokens one per tile.
 template <auto K>
-cudaError_t start(const char *name, size_t smem, GatedArgs a, const Maps &maps, cudaStream_t st) {
+cudaError_t start(const char *name, size_t smem, bool eager, const GatedArgs &a, const Maps &maps,
+                  cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const int64_t lanes = a.batch * a.dblocks, tiles = lanes * a.nb;
     int64_t grid = tiles, ends = 0, words = 0;
@@ -1133,9 +1157,8 @@ cudaError_t start(const char *name, size_t smem, GatedArgs a, const Maps &maps, 
     if (e != cudaSuccess) return e;
     if (a.nb > 1) {
         if (fit < grid) grid = fit;
-        a.eager = lanes >= grid;
-        ends = (a.eager ? tiles : lanes * (a.nb / kGroup)) * 32;
-        words = a.eager ? 0 : tiles * 64;
+        ends = (eager ? tiles : lanes * (a.nb / kGroup)) * 32;
+        words = eager ? 0 : tiles * 64;
     }
     int64_t n = ends > words ? ends / 2 : words / 2;
     if (n < a.D) n = a.D;
@@ -1180,11 +1203,29 @@ bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool ALIGNED>
+// Many lanes or few (see the top): whether every thread block of the kernel
+// that holds tickets ahead has a lane of its own.
+template <auto K>
+bool many_lanes(const GatedArgs &a, size_t smem, cudaError_t *e) {
+    const int64_t fit = resident_blocks<K>(smem, e);
+    return *e == cudaSuccess && a.nb > 1 && a.batch * a.dblocks >= fit;
+}
+
+template <typename T, bool ALIGNED, bool CK>
 cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
-    const size_t smem = Stage<T, ALIGNED, 3>::kBytes;
-    return a.q ? start<gated_forward_kernel<T, ALIGNED, true>>("gated_forward", smem, a, maps, st)
-               : start<gated_forward_kernel<T, ALIGNED, false>>("gated_forward", smem, a, maps, st);
+    constexpr size_t ahead = Stage<T, ALIGNED, 3, kForwardKeep<CK, true>>::kBytes,
+                     kept = Stage<T, ALIGNED, 3, kForwardKeep<CK, false>>::kBytes;
+    constexpr auto *many = gated_forward_kernel<T, ALIGNED, CK, true>;
+    constexpr auto *few = gated_forward_kernel<T, ALIGNED, CK, false>;
+    cudaError_t e = cudaSuccess;
+    const bool eager = many_lanes<many>(a, ahead, &e);
+    if (e != cudaSuccess) return e;
+    return eager ? start<many>("gated_forward", ahead, true, a, maps, st)
+                 : start<few>("gated_forward", kept, false, a, maps, st);
+}
+template <typename T, bool ALIGNED>
+cudaError_t forward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
+    return a.q ? forward_t<T, ALIGNED, true>(a, maps, st) : forward_t<T, ALIGNED, false>(a, maps, st);
 }
 template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
@@ -1192,16 +1233,25 @@ cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
     const bool aligned = on(a.y, 8) && on(a.q, 4) && make_map<T>(&maps.m[0], a.x, a) &&
                          make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a);
     a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4);
-    return aligned ? forward_t<T, true>(a, maps, st) : forward_t<T, false>(a, maps, st);
+    return aligned ? forward_c<T, true>(a, maps, st) : forward_c<T, false>(a, maps, st);
 }
 
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, bool CK>
 cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
-    return a.q ? start<gated_backward_kernel<T, ALIGNED, true>>(
-                     "gated_backward",
-                     Stage<T, ALIGNED, 1>::kBytes + Stage<int8_t, ALIGNED, 3>::kBytes, a, maps, st)
-               : start<gated_backward_kernel<T, ALIGNED, false>>(
-                     "gated_backward", Stage<T, ALIGNED, 4>::kBytes, a, maps, st);
+    constexpr size_t smem =
+        Stage<T, ALIGNED, CK ? 1 : 4>::kBytes + (CK ? Stage<int8_t, ALIGNED, 3>::kBytes : 0);
+    constexpr auto *many = gated_backward_kernel<T, ALIGNED, CK, true>;
+    constexpr auto *few = gated_backward_kernel<T, ALIGNED, CK, false>;
+    cudaError_t e = cudaSuccess;
+    const bool eager = many_lanes<many>(a, smem, &e);
+    if (e != cudaSuccess) return e;
+    return eager ? start<many>("gated_backward", smem, true, a, maps, st)
+                 : start<few>("gated_backward", smem, false, a, maps, st);
+}
+template <typename T, bool ALIGNED>
+cudaError_t backward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
+    return a.q ? backward_t<T, ALIGNED, true>(a, maps, st)
+               : backward_t<T, ALIGNED, false>(a, maps, st);
 }
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
@@ -1215,7 +1265,7 @@ cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
                   make_map<T>(&maps.m[3], a.x, a);
     }
     a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4) && on(a.dy, 4) && on(a.q, 4);
-    cudaError_t e = aligned ? backward_t<T, true>(a, maps, st) : backward_t<T, false>(a, maps, st);
+    cudaError_t e = aligned ? backward_c<T, true>(a, maps, st) : backward_c<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
     gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 8), 0, st>>>(

@@ -144,7 +144,6 @@ struct GatedArgs {
     float *last = nullptr;         // h_final, or dh0
     float *dlam_part = nullptr;    // (b, nb, D)
     float *scale = nullptr;        // (D): c softplus(lam)
-    bool eager = false;            // thread blocks hold tickets ahead
     bool words = false;            // input tensors start on 4 bytes
     unsigned *counter = nullptr, *abort = nullptr, *err = nullptr;
     unsigned long long *ends = nullptr, *maps = nullptr;  // what tiles publish
