@@ -149,28 +149,34 @@ __device__ __forceinline__ f2 widen(uint16_t v) {
                   f2_both(8388736.f));
 }
 
-// An output's rows for this lane: stores its two channels of one token.
+// An output's rows for this lane: stores its two channels of one token after
+// the other. FULL: the tile's channels are all there.
 template <typename T, bool ALIGNED>
 struct Rows {
     T *p;
+    int64_t step;
     bool has0, has1;
     __device__ __forceinline__ Rows(void *base, int64_t row, int d0, int64_t D)
         : p(static_cast<T *>(base) + row + d0 + channel<ALIGNED>(0)),
+          step(D),
           has0(d0 + channel<ALIGNED>(0) < D),
           has1(d0 + channel<ALIGNED>(1) < D) {}
-    __device__ __forceinline__ void put(int64_t off, f2 val) const {
+    template <bool FULL>
+    __device__ __forceinline__ void put(f2 val) {
         float lo, hi;
         f2_unpack(val, lo, hi);
         if constexpr (ALIGNED) {
-            if (!has0) return;
-            if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<float2 *>(p + off) = make_float2(lo, hi);
-            else
-                *reinterpret_cast<uint32_t *>(p + off) = tc::pack_bf16(lo, hi);
+            if (FULL || has0) {
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<float2 *>(p) = make_float2(lo, hi);
+                else
+                    *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16(lo, hi);
+            }
         } else {
-            if (has0) p[off] = from_f<T>(lo);
-            if (has1) p[off + 32] = from_f<T>(hi);
+            if (FULL || has0) p[0] = from_f<T>(lo);
+            if (FULL || has1) p[32] = from_f<T>(hi);
         }
+        p += step;
     }
 };
 
@@ -688,7 +694,8 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
     __syncthreads();
 }
 
-// The plain case of a warp's eight tokens (all there, no reset, slow decays) is
+// The plain case of a warp's eight tokens (all there, with all the tile's
+// channels, no reset, slow decays) is
 // straight code; every other case runs a general copy with a branch a token.
 struct PlainRun : std::true_type {};
 struct AnyRun : std::false_type {};
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
     for (int n = 0;; ++n) {
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
-        const bool plain = all_fast(k) && marks == 0 && left >= kRun;
+        const bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
         uint32_t at[3];
 #pragma unroll
         for (int w = 0; w < 3; ++w) at[w] = in.place(a, t, src[w]);
@@ -803,20 +810,19 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
             break;
         }
         f2 h = s.entry[warp][lane];
-        const Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
+        Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
         if (plain) {
-            int64_t off = 0;
 #pragma unroll
-            for (int j = 0; j < kRun; ++j, off += a.D) {
+            for (int j = 0; j < kRun; ++j) {
                 h = f2_fma(kKeep ? keep[2 * j * 32] : av[j], h, kKeep ? keep[(2 * j + 1) * 32] : u[j]);
-                y.put(off, h);
+                y.template put<true>(h);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 const f2 uj = kKeep ? keep[(2 * j + 1) * 32] : u[j];
                 h = (marks >> j & 1) ? uj : f2_fma(kKeep ? keep[2 * j * 32] : av[j], h, uj);
-                if (j < left) y.put(j * a.D, h);
+                if (j < left) y.template put<false>(h);
             }
         }
         if (CK) {
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     for (int n = 0;; ++n) {
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
-        const bool plain = all_fast(k) && marks == 0 && left >= kRun;
+        const bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
         // kept until the gradients: dy, x (as stored) and the two sigmoids
         std::conditional_t<CK, uint16_t, P2> xr[kRun];
         P2 dyr[kRun];
@@ -1013,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         auto grads = [&](auto run) {
             constexpr bool kPlain = decltype(run)::value;
             const int64_t row = t.row0 + tok0 * a.D;
-            const Rows<T, ALIGNED> dx(a.dx, row, t.d0, a.D), dr(a.dr, row, t.d0, a.D),
+            Rows<T, ALIGNED> dx(a.dx, row, t.d0, a.D), dr(a.dr, row, t.d0, a.D),
                 di(a.di, row, t.d0, a.D);
             f2 F[kRun], G[kRun];
             f2 c = s.grad[warp][lane];
@@ -1028,9 +1034,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 }
             }
             f2 h = s.entry[warp][lane];
-            int64_t off = 0;
 #pragma unroll
-            for (int j = 0; j < kRun; ++j, off += a.D) {
+            for (int j = 0; j < kRun; ++j) {
                 if (!kPlain && j >= left) break;
                 const bool cut = !kPlain && (marks >> j & 1);
                 Gate2 g;
@@ -1046,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                                           f2_sub(f2_mul(f2_mul(g.a, g.rm), vx), h));
                 dl = f2_add(dl, e);
                 const f2 gv = f2_mul(gm, vx);
-                dx.put(off, f2_mul(gm, sij));
-                dr.put(off, f2_mul(e, f2_sub(one, srj)));
-                di.put(off, f2_mul(gv, f2_sub(one, sij)));
+                dx.template put<kPlain>(f2_mul(gm, sij));
+                dr.template put<kPlain>(f2_mul(e, f2_sub(one, srj)));
+                di.template put<kPlain>(f2_mul(gv, f2_sub(one, sij)));
                 h = cut ? vx : f2_fma(g.a, h, f2_mul(g.m, vx));
             }
         };
