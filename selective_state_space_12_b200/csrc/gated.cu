@@ -89,6 +89,7 @@ __device__ __forceinline__ unsigned load_relaxed(const unsigned *p) {
 
 struct __align__(16) Tile {
     int64_t row0;  // offset of (b, first token, 0) in a (b, L, D) tensor
+    int64_t flat;     // its first token's row in a (b L, D) tensor
     int64_t blocks0;  // and of (b, blk, 0) in a (b, nb, D) one
     int b, blk, d0, n;  // batch, block of tokens, first channel, tokens
     unsigned id;   // its ticket, and the index of its record
@@ -102,7 +103,8 @@ __device__ __forceinline__ Tile tile_of(const GatedArgs &a, unsigned ticket) {
     t.b = (int)(lane / (unsigned)a.dblocks);
     t.d0 = (int)(lane % (unsigned)a.dblocks) * kTileCh;
     t.blk = (int)(BACK ? a.nb - 1 - step : step);
-    t.row0 = (t.b * a.L + (int64_t)t.blk * kBlock) * a.D;
+    t.flat = t.b * a.L + (int64_t)t.blk * kBlock;
+    t.row0 = t.flat * a.D;
     t.blocks0 = (t.b * a.nb + t.blk) * a.D;
     const int64_t left = a.L - (int64_t)t.blk * kBlock;
     t.n = (int)(left < kBlock ? left : kBlock);
@@ -182,22 +184,23 @@ struct Rows {
 
 // ------------------------------------------------------------ staged inputs
 
-// Each warp brings its own eight tokens' rows of every input tensor to shared
-// memory a tile ahead and waits for nobody else's. Where rows are 16-byte
-// aligned, one TMA load a tensor does it, counted by the warp's own barrier;
-// past the last token and channel it fills zeros. Elsewhere the lanes copy the
-// 4-byte words that cover each row (one more for a row that starts inside one)
-// asynchronously, and read from the row's place in them. Words that may leave
-// the tensor (the last tile's; a tensor that starts inside a word) are replaced
-// by plain loads. T is the I/O type, or int8 for 8-bit copies.
+// Rows of a tile come to shared memory by TMA, a tile ahead where tickets are.
+// T is the I/O type, or int8 for 8-bit copies.
 struct Maps {
     CUtensorMap m[4];
 };
+// A wait for copies in flight before a thread block ends (about 9 ms), whatever
+// the limit on the waits before it.
+constexpr long long kDrain = 1ll << 24;
 
-template <typename T, bool ALIGNED, int TENSORS, int KEEP = 0>
-struct Stage {
+// Rows that start on 16 bytes: each warp brings its own eight tokens' rows, one
+// TMA load a tensor, counted by a barrier of its own, and waits for nobody
+// else's; past the last token and channel the load fills zeros.
+template <typename T, int TENSORS, int KEEP = 0>
+struct WarpRows {
     using P = typename Pair<T>::type;
-    static constexpr int kPitch = kTileCh * (int)sizeof(T) + (ALIGNED ? 0 : 16);
+    static constexpr bool kAhead = true;  // may be requested before other warps have read theirs
+    static constexpr int kPitch = kTileCh * (int)sizeof(T);
     static constexpr int kRowsBytes = TENSORS * kRun * kPitch;
     static constexpr int kWarpBytes = kRowsBytes > KEEP ? kRowsBytes : KEEP;
     static constexpr size_t kBytes = (size_t)kWarps * kWarpBytes;
@@ -206,152 +209,169 @@ struct Stage {
     uint64_t *bar;
     uint32_t parity;
 
-    __device__ __forceinline__ Stage(unsigned char *all, uint64_t *bars)
+    __device__ __forceinline__ WarpRows(unsigned char *all, uint64_t *bars)
         : buf(all + (threadIdx.x >> 5) * kWarpBytes), bar(bars + (threadIdx.x >> 5)), parity(0) {}
 
     __device__ __forceinline__ void request(const GatedArgs &a, const CUtensorMap *maps,
-                                            const Tile &t,
-                                            const void *const (&src)[TENSORS]) const {
-        const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
+                                            const Tile &t, const void *const (&)[TENSORS]) {
+        const int tok0 = (threadIdx.x >> 5) * kRun;
         __syncwarp();  // the rows have been read
-        if constexpr (ALIGNED) {
-            if (KEEP > 0) {  // what was kept there was written by ordinary stores
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (lane == 0) {
-                const bool any = tok0 < t.n;
-                tc::mbar_arrive_expect_tx(bar, any ? kRowsBytes : 0);
-                if (any) {
-#pragma unroll
-                    for (int w = 0; w < TENSORS; ++w)
-                        tc::tma_load_4d(buf + w * kRun * kPitch, maps + w, bar, t.d0,
-                                        t.blk * kBlock + tok0, t.b, 0);
-                }
-            }
-        } else {
-            const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
-            const int64_t row0 = t.row0 + (int64_t)tok0 * a.D + t.d0;
-            if (sizeof(T) == 4 || t.last || !a.words) {
+        if (KEEP > 0) {  // what was kept there was written by ordinary stores
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+        }
+        if ((threadIdx.x & 31) == 0) {
+            const bool any = tok0 < t.n;
+            tc::mbar_arrive_expect_tx(bar, any ? kRowsBytes : 0);
+            if (any) {
 #pragma unroll
                 for (int w = 0; w < TENSORS; ++w)
-#pragma unroll
-                    for (int j = 0; j < kRun; ++j) {
-                        if (tok0 + j >= t.n) break;
-                        const T *row = static_cast<const T *>(src[w]) + row0 + j * a.D;
-                        unsigned char *to = buf + (w * kRun + j) * kPitch +
-                                            (sizeof(T) == 4 ? 0u : ((uint32_t)(uintptr_t)row & 3u));
-#pragma unroll
-                        for (int c = lane; c < kTileCh; c += 32) {
-                            if (c >= len) continue;
-                            if constexpr (sizeof(T) == 4)
-                                copy4(to + 4 * c, row + c);
-                            else
-                                reinterpret_cast<T *>(to)[c] = row[c];
-                        }
-                    }
-            } else {
-                constexpr int kE = (int)sizeof(T), kWords = kTileCh * kE / 4;  // 32 or 16
-                constexpr int kRows = 32 / kWords;                             // a copy of all lanes
-#pragma unroll
-                for (int w = 0; w < TENSORS; ++w) {
-                    const uintptr_t row = reinterpret_cast<uintptr_t>(src[w]) + kE * row0;
-#pragma unroll
-                    for (int j0 = 0; j0 < kRun; j0 += kRows) {
-                        const int j = j0 + lane / kWords, i = lane % kWords;
-                        if (tok0 + j0 >= t.n) break;
-                        const uintptr_t r = row + kE * (uintptr_t)(j * a.D);
-                        const int words = ((int)(r & 3) + kE * len + 3) / 4;
-                        if (i < words && tok0 + j < t.n)
-                            copy4(buf + (w * kRun + j) * kPitch + 4 * i,
-                                  reinterpret_cast<const void *>((r & ~uintptr_t(3)) + 4 * i));
-                    }
-                }
-                // the words after these: lane w kRun + j
-                const int w = lane / kRun, j = lane % kRun;
-                if (w < TENSORS && tok0 + j < t.n) {
-                    uintptr_t row = 0;
-#pragma unroll
-                    for (int v = 0; v < TENSORS; ++v)
-                        if (v == w)
-                            row = reinterpret_cast<uintptr_t>(src[v]) + kE * (row0 + j * a.D);
-                    if ((int)(row & 3) + kE * len > 4 * kWords)
-                        copy4(buf + lane * kPitch + 4 * kWords,
-                              reinterpret_cast<const void *>((row & ~uintptr_t(3)) + 4 * kWords));
-                }
+                    tc::tma_load_4d(buf + w * kRun * kPitch, maps + w, bar, t.d0,
+                                    t.blk * kBlock + tok0, t.b, 0);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
-    // Without tickets ahead: brings the rows of the tile that comes one round of
-    // thread blocks later to L2, whoever will take it.
+    // Brings the rows of a tile that another thread block will take to L2.
     __device__ __forceinline__ void prefetch(const GatedArgs &a, const CUtensorMap *maps,
                                              unsigned tiles, const Tile &t,
-                                             const void *const (&src)[TENSORS]) const {
-        const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
-        if (t.id >= tiles) return;
-        if constexpr (ALIGNED) {
-            if (lane == 0 && tok0 < t.n) {
+                                             const void *const (&)[TENSORS]) const {
+        const int tok0 = (threadIdx.x >> 5) * kRun;
+        if (t.id < tiles && (threadIdx.x & 31) == 0 && tok0 < t.n) {
 #pragma unroll
-                for (int w = 0; w < TENSORS; ++w)
-                    tc::tma_prefetch_l2_4d(maps + w, t.d0, t.blk * kBlock + tok0, t.b, 0);
-            }
-        } else {
-            const int w = lane / kRun, j = lane % kRun;
-            if (w < TENSORS && tok0 + j < t.n) {
-                const T *row = nullptr;
-#pragma unroll
-                for (int v = 0; v < TENSORS; ++v)
-                    if (v == w) row = static_cast<const T *>(src[v]);
-                row += t.row0 + (tok0 + j) * a.D + t.d0;
-                const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
-                for (int c = 0; c < len; c += 64 / (int)sizeof(T))
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
-            }
+            for (int w = 0; w < TENSORS; ++w)
+                tc::tma_prefetch_l2_4d(maps + w, t.d0, t.blk * kBlock + tok0, t.b, 0);
         }
-    }
-    static __device__ __forceinline__ void copy4(void *to, const void *from) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(to)), "l"(from)
-                     : "memory");
     }
     // False when the wait ran out.
     __device__ __forceinline__ bool wait(long long limit) {
-        if constexpr (ALIGNED) {
-            const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
-            if (ok) parity ^= 1;
-            return ok;
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
+        if (ok) parity ^= 1;
+        return ok;
+    }
+    __device__ __forceinline__ P get(int w, int j) const {
+        return reinterpret_cast<const P *>(buf + (w * kRun + j) * kPitch)[threadIdx.x & 31];
+    }
+};
+
+// Rows that start anywhere. kSlots consecutive rows of a (b L, D) tensor make one
+// of 16 k bytes, so the tensor is mapped as (b L / kSlots, kSlots D): a box of
+// this map holds every kSlots-th row of a tile, all at the same place within 16
+// bytes, from which it starts (up to 15 bytes before the row). Eight warps bring
+// the boxes, one or two each a tensor, once all have read the rows before, and
+// wait for all of them. Lanes read from the rows' places in their boxes. A tile
+// with rows past the map's whole ones (at the tensor's end), or tensors that do
+// not start on 16 bytes, are read by plain loads. STACKED: the tensors lie behind
+// one another and share one map.
+template <typename T, int TENSORS, bool STACKED = false>
+struct FlatRows {
+    using P = typename Pair<T>::type;
+    static constexpr bool kAhead = false;
+    static constexpr int kE = (int)sizeof(T), kUnit = 16 / kE;
+    static constexpr int kSlots = kE == 1 ? 16 : 8, kSlotRows = kBlock / kSlots;
+    static constexpr int kPitch = kTileCh * kE + 16;
+    static constexpr int kSlotBytes = (kSlotRows * kPitch + 127) & ~127;
+    static constexpr size_t kBytes = (size_t)TENSORS * kSlots * kSlotBytes;
+
+    unsigned char *buf;  // all rows
+    uint64_t *bar;
+    uint32_t parity;
+    uint32_t first, low;  // the tile's first row and D, modulo the slots and the unit
+    uint32_t behind;      // STACKED: rows of a tensor, modulo the slots
+    bool plain;
+
+    __device__ __forceinline__ FlatRows(unsigned char *all, uint64_t *bars)
+        : buf(all), bar(bars), parity(0) {}
+
+    // token j of this warp: its box and its row there
+    static __device__ __forceinline__ int slot(int j) {
+        return kE == 1 ? ((threadIdx.x >> 5) & 1) * kRun + j : j;
+    }
+    static __device__ __forceinline__ int row() {
+        return kE == 1 ? threadIdx.x >> 6 : threadIdx.x >> 5;
+    }
+    __device__ __forceinline__ T *place(int w, int j) const {
+        const uint32_t r = first + slot(j) + (STACKED ? w * behind : 0);
+        const uint32_t shift = ((r & (kSlots - 1)) * low) & (kUnit - 1);
+        return reinterpret_cast<T *>(buf + (w * kSlots + slot(j)) * kSlotBytes + row() * kPitch) +
+               shift + (threadIdx.x & 31);
+    }
+    __device__ __forceinline__ void request(const GatedArgs &a, const CUtensorMap *maps,
+                                            const Tile &t, const void *const (&src)[TENSORS]) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        first = (uint32_t)t.flat & (kSlots - 1);
+        low = (uint32_t)a.D & (kUnit - 1);
+        const int64_t rows = a.batch * a.L, before = STACKED ? (TENSORS - 1) * rows : 0;
+        behind = (uint32_t)rows & (kSlots - 1);
+        plain = !a.flat || before + t.flat + t.n > (before + rows & ~(int64_t)(kSlots - 1));
+        if (plain) {
+            const int tok0 = warp * kRun;
+            const bool has0 = t.d0 + lane < a.D, has1 = t.d0 + lane + 32 < a.D;
+#pragma unroll
+            for (int w = 0; w < TENSORS; ++w)
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) {
+                    if (tok0 + j >= t.n) break;
+                    const T *from = static_cast<const T *>(src[w]) + t.row0 + (tok0 + j) * a.D +
+                                    t.d0 + lane;
+                    T *to = place(w, j);
+                    if (has0) to[0] = from[0];
+                    if (has1) to[32] = from[32];
+                }
+        } else if (lane == 0) {
+            // ordinary writes of a plain tile before these
+            tc::fence_proxy_async_smem();
+            constexpr int kMine = kSlots / kWarps;
+            tc::mbar_arrive_expect_tx(bar, kMine * TENSORS * kSlotRows * kPitch);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int w = 0; w < TENSORS; ++w) {
+                    const int64_t r = t.flat + warp * kMine + i + (STACKED ? w * rows : 0);
+                    const int x = (int)((int)(r & (kSlots - 1)) * a.D + t.d0) & ~(kUnit - 1);
+                    tc::tma_load_4d(buf + (w * kSlots + warp * kMine + i) * kSlotBytes,
+                                    maps + (STACKED ? 0 : w), bar, x, (int)(r / kSlots), 0, 0);
+                }
+        }
+    }
+    __device__ __forceinline__ void prefetch(const GatedArgs &a, const CUtensorMap *, unsigned tiles,
+                                             const Tile &t,
+                                             const void *const (&src)[TENSORS]) const {
+        const int lane = threadIdx.x & 31, tok0 = (threadIdx.x >> 5) * kRun;
+        const int w = lane / kRun, j = lane % kRun;
+        if (t.id < tiles && w < TENSORS && tok0 + j < t.n) {
+            const T *from = nullptr;
+#pragma unroll
+            for (int v = 0; v < TENSORS; ++v)
+                if (v == w) from = static_cast<const T *>(src[v]);
+            from += t.row0 + (tok0 + j) * a.D + t.d0;
+            const int len = (int)(a.D - t.d0 < kTileCh ? a.D - t.d0 : kTileCh);
+            for (int c = 0; c < len; c += 64 / kE)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + c));
+        }
+    }
+    __device__ __forceinline__ bool wait(long long limit) {
+        if (plain) {
             __syncwarp();
             return true;
         }
+        const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, limit));
+        if (ok) parity ^= 1;
+        return ok;
     }
-    // The address, in its low bits, of this warp's first row of a tensor.
-    static __device__ __forceinline__ uint32_t place(const GatedArgs &a, const Tile &t,
-                                                     const void *src) {
-        if (ALIGNED || sizeof(T) == 4) return 0;
-        return (uint32_t)reinterpret_cast<uintptr_t>(
-            static_cast<const char *>(src) +
-            (t.row0 + (int64_t)((threadIdx.x >> 5) * kRun) * a.D + t.d0) * (int64_t)sizeof(T));
-    }
-    __device__ __forceinline__ P get(int w, int j, uint32_t place0, uint32_t rowbytes) const {
-        const unsigned char *row = buf + (w * kRun + j) * kPitch;
-        if constexpr (ALIGNED) {
-            return reinterpret_cast<const P *>(row)[threadIdx.x & 31];
-        } else {
-            const T *v = reinterpret_cast<const T *>(
-                             row + (sizeof(T) == 4 ? 0u : ((place0 + j * rowbytes) & 3u))) +
-                         (threadIdx.x & 31);
-            if constexpr (sizeof(T) == 4)
-                return make_float2(v[0], v[32]);
-            else if constexpr (sizeof(T) == 2)
-                return (uint32_t)__bfloat16_as_ushort(v[0]) |
-                       (uint32_t)__bfloat16_as_ushort(v[32]) << 16;
-            else
-                return (uint16_t)((uint8_t)v[0] | (uint16_t)(uint8_t)v[32] << 8);
-        }
+    __device__ __forceinline__ P get(int w, int j) const {
+        const T *v = place(w, j);
+        if constexpr (kE == 4)
+            return make_float2(v[0], v[32]);
+        else if constexpr (kE == 2)
+            return (uint32_t)__bfloat16_as_ushort(v[0]) | (uint32_t)__bfloat16_as_ushort(v[32]) << 16;
+        else
+            return (uint16_t)((uint8_t)v[0] | (uint16_t)(uint8_t)v[32] << 8);
     }
 };
+
+template <typename T, bool ALIGNED, int TENSORS, int KEEP = 0>
+using Stage = std::conditional_t<ALIGNED, WarpRows<T, TENSORS, KEEP>,
+                                 FlatRows<T, TENSORS, std::is_same_v<T, int8_t>>>;
 
 // Reset marks of the warp's tokens, one bit each.
 __device__ __forceinline__ unsigned reset_byte(const GatedArgs &a, const Tile &t) {
@@ -679,7 +699,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
 }
 
 // The first tickets of this thread block, and its barriers.
-template <bool BACK, bool EAGER>
+template <bool ALIGNED, bool BACK, bool EAGER>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
     if (threadIdx.x == 0) {
         s.stop[0] = s.stop[1] = 0;
@@ -688,7 +708,8 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
         s.tile[0] = tile_of<BACK>(a, first);
         s.tile[1] = tile_of<BACK>(a, EAGER ? atomicAdd(a.counter, 1u) : tiles);
         s.later = tile_of<BACK>(a, round_on(first));
-        for (int w = 0; w < 2 * kWarps; ++w) tc::mbar_init(&s.bars[w], 1);
+        // a barrier a warp and stage, or one a stage that every warp arrives at
+        for (int w = 0; w < 2 * kWarps; ++w) tc::mbar_init(&s.bars[w], ALIGNED ? 1 : kWarps);
         tc::fence_mbar_init();
     }
     __syncthreads();
@@ -703,25 +724,24 @@ struct AnyRun : std::false_type {};
 // ------------------------------------------------------------ forward
 
 // Bytes that a warp keeps in its rows' place while it waits: a and u.
-template <bool CK, bool EAGER>
-constexpr int kForwardKeep = !EAGER && !CK ? 2 * kRun * 32 * 8 : 0;
+template <bool ALIGNED, bool CK, bool EAGER>
+constexpr int kForwardKeep = ALIGNED && !EAGER && !CK ? 2 * kRun * 32 * 8 : 0;
 
 template <typename T, bool ALIGNED, bool CK, bool EAGER>
-__global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forward_kernel(
+__global__ void __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) gated_forward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<false, EAGER>(a, s, tiles);
+    open_block<ALIGNED, false, EAGER>(a, s, tiles);
     if (warp == kWarps) {
         chain_warp<T, ALIGNED, CK, false, EAGER>(a, s, tiles, lanes);
         return;
     }
-    Stage<T, ALIGNED, 3, kForwardKeep<CK, EAGER>> in(staged, s.bars);
+    Stage<T, ALIGNED, 3, kForwardKeep<ALIGNED, CK, EAGER>> in(staged, s.bars);
     const void *const src[3] = {a.x, a.r, a.i};
-    const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
     Tile t = s.tile[0];
     if (t.id >= tiles) return;
     in.request(a, maps.m, t, src);
@@ -729,14 +749,12 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
     f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
     const bool chained = a.nb > 1;
+    constexpr bool kAhead = decltype(in)::kAhead;
     bool ahead = false;  // copies are on their way
     for (int n = 0;; ++n) {
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
         const bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
-        uint32_t at[3];
-#pragma unroll
-        for (int w = 0; w < 3; ++w) at[w] = in.place(a, t, src[w]);
         const bool here = in.wait(a.wait);
         if (!here) give_up(a, &s.stop[n & 1]);
         typename Pair<T>::type v[3][kRun];
@@ -747,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
 #pragma unroll
-                for (int w = 0; w < 3; ++w) v[w][j] = in.get(w, j, at[w], rowbytes);
+                for (int w = 0; w < 3; ++w) v[w][j] = in.get(w, j);
                 const Gate2 g = gate2<kPlain>(widen(v[1][j]), widen(v[2][j]), k);
                 const f2 ix = f2_mul(g.si, widen(v[0][j]));
                 if (kPlain || (j < left && !(marks >> j & 1))) {
@@ -781,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
         // without a ticket ahead the rows' place is free: a and u wait there, so that more
         // thread blocks fit
         f2 *const keep = reinterpret_cast<f2 *>(in.buf) + lane;
-        constexpr bool kKeep = !EAGER && !CK;
+        constexpr bool kKeep = kForwardKeep<ALIGNED, CK, EAGER> > 0;
         if (kKeep) {
             __syncwarp();
 #pragma unroll
@@ -802,13 +820,15 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
         if (EAGER) {
             tn = s.tile[(n + 1) & 1];
             ahead = here && tn.id < tiles;
-            if (ahead) advance();
+            if (ahead && kAhead) advance();
         } else if (chained) in.prefetch(a, maps.m, tiles, s.later, src);
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
-            if (!here) in.wait(a.wait);
+            if (!here) in.wait(kDrain);
+            ahead = ahead && kAhead;
             break;
         }
+        if (EAGER && !kAhead && ahead) advance();  // all warps have read their rows
         f2 h = s.entry[warp][lane];
         Rows<T, ALIGNED> y(a.y, t.row0 + tok0 * a.D, t.d0, a.D);
         if (plain) {
@@ -868,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, CK ? 2 : EAGER ? 3 : 4) gated_forwar
         t = tn;
         k = kn;
     }
-    if (ahead) in.wait(a.wait);  // nothing may be in flight to shared memory at the end
+    if (ahead) in.wait(kDrain);  // nothing may be in flight to shared memory at the end
 }
 
 // ------------------------------------------------------------ backward
@@ -892,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t lanes = a.batch * a.dblocks;
     const unsigned tiles = (unsigned)(lanes * a.nb);
-    open_block<true, EAGER>(a, s, tiles);
+    open_block<ALIGNED, true, EAGER>(a, s, tiles);
     if (warp == kWarps) {
         chain_warp<T, ALIGNED, CK, true, EAGER>(a, s, tiles, lanes);
         return;
@@ -909,7 +929,6 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         src[2] = a.i;
         src[3] = a.x;
     }
-    const uint32_t rowbytes = (uint32_t)a.D * (uint32_t)sizeof(T);
     Tile t = s.tile[0];
     if (t.id >= tiles) return;
     in.request(a, maps.m, t, src);
@@ -924,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const int tok0 = warp * kRun;
     const f2 none = f2_both(0.f), one = f2_both(1.f);
     const bool chained = a.nb > 1;
+    constexpr bool kAhead = In::kAhead;
     bool ahead = false;
     for (int n = 0;; ++n) {
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
@@ -933,16 +953,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         std::conditional_t<CK, uint16_t, P2> xr[kRun];
         P2 dyr[kRun];
         f2 sr[kRun], si[kRun];
-        uint32_t at[kIn];
-#pragma unroll
-        for (int w = 0; w < kIn; ++w) at[w] = in.place(a, t, src[w]);
         bool here = in.wait(a.wait);
-        uint32_t cat[3];
-        if constexpr (CK) {
-#pragma unroll
-            for (int w = 0; w < 3; ++w) cat[w] = copies.place(a, t, csrc[w]);
-            here = copies.wait(a.wait) && here;
-        }
+        if constexpr (CK) here = copies.wait(a.wait) && here;
         if (!here) give_up(a, &s.stop[n & 1]);
         f2 P = f2_both(1.f), H = none, R = none;
         auto gates = [&](auto run) {
@@ -950,17 +962,16 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 f2 rv, iv, x;
-                dyr[j] = in.get(0, j, at[0], rowbytes);
+                dyr[j] = in.get(0, j);
                 if constexpr (CK) {
-                    const uint32_t step = (uint32_t)a.D;
-                    xr[j] = copies.get(0, j, cat[0], step);
+                    xr[j] = copies.get(0, j);
                     x = f2_mul(widen(xr[j]), steps[0]);
-                    rv = f2_mul(widen(copies.get(1, j, cat[1], step)), steps[1]);
-                    iv = f2_mul(widen(copies.get(2, j, cat[2], step)), steps[2]);
+                    rv = f2_mul(widen(copies.get(1, j)), steps[1]);
+                    iv = f2_mul(widen(copies.get(2, j)), steps[2]);
                 } else {
-                    rv = widen(in.get(1, j, at[1], rowbytes));
-                    iv = widen(in.get(2, j, at[2], rowbytes));
-                    xr[j] = in.get(3, j, at[3], rowbytes);
+                    rv = widen(in.get(1, j));
+                    iv = widen(in.get(2, j));
+                    xr[j] = in.get(3, j);
                     x = widen(xr[j]);
                 }
                 const Gate2 g = gate2<kPlain>(rv, iv, k);
@@ -1002,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         if (EAGER) {
             tn = s.tile[(n + 1) & 1];
             ahead = here && tn.id < tiles;
-            if (ahead) advance();
+            if (ahead && kAhead) advance();
         } else if (chained) {
             in.prefetch(a, maps.m, tiles, s.later, src);
             if constexpr (CK) copies.prefetch(a, maps.m + 1, tiles, s.later, csrc);
@@ -1010,11 +1021,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
             if (!here) {
-                in.wait(a.wait);
-                if constexpr (CK) copies.wait(a.wait);
+                in.wait(kDrain);
+                if constexpr (CK) copies.wait(kDrain);
             }
+            ahead = ahead && kAhead;
             break;
         }
+        if (EAGER && !kAhead && ahead) advance();  // all warps have read their rows
         f2 dl = none;
         auto grads = [&](auto run) {
             constexpr bool kPlain = decltype(run)::value;
@@ -1081,8 +1094,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         }
     }
     if (ahead) {
-        in.wait(a.wait);
-        if constexpr (CK) copies.wait(a.wait);
+        in.wait(kDrain);
+        if constexpr (CK) copies.wait(kDrain);
     }
 }
 
@@ -1190,15 +1203,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A map over a (b, L, D) tensor whose box is one warp's rows of a tile. False
-// where the tensor's layout has none (the unaligned path then serves it).
 template <typename T>
-bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
-    const uint64_t row = (uint64_t)a.D * sizeof(T);
-    if (!encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1};
-    const cuuint64_t strides[3] = {row, row * (uint64_t)a.L, row * (uint64_t)a.L};
-    const cuuint32_t box[4] = {kTileCh, kRun, 1, 1}, estr[4] = {1, 1, 1, 1};
+bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4],
+            const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     return encoder()(m, sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                         : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8,
@@ -1206,6 +1214,42 @@ bool make_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A map over a (b, L, D) tensor whose box is one warp's rows of a tile. False
+// where rows do not start on 16 bytes.
+template <typename T>
+bool warp_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
+    const uint64_t row = (uint64_t)a.D * sizeof(T);
+    if (!encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
+    return encode<T>(m, base, {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1},
+                     {row, row * (uint64_t)a.L, row * (uint64_t)a.L}, {kTileCh, kRun, 1, 1});
+}
+
+// A map of FlatRows over the same tensor: its whole groups of kSlots rows.
+// False where there is none.
+template <typename T>
+bool flat_map(CUtensorMap *m, const void *base, int64_t rows, const GatedArgs &a) {
+    using F = FlatRows<T, 1>;
+    const uint64_t groups = (uint64_t)rows / F::kSlots;
+    const uint64_t row = (uint64_t)a.D * sizeof(T) * F::kSlots;
+    if (!encoder() || !on(base, 16) || groups == 0 || groups >= 1ull << 31 ||
+        row * groups >= 1ull << 40)
+        return false;
+    return encode<T>(m, base, {(cuuint64_t)a.D * F::kSlots, groups, 1, 1},
+                     {row, row * groups, row * groups},
+                     {kTileCh + F::kUnit, F::kSlotRows, 1, 1});
+}
+
+// The maps of `n` tensors; whether their rows are aligned, and if not, whether
+// the flat maps are there.
+template <typename T>
+void make_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &a, bool aligned,
+               bool *flat) {
+    for (int w = 0; w < n; ++w) {
+        if (aligned) warp_map<T>(m + w, base[w], a);
+        else *flat = flat_map<T>(m + w, base[w], a.batch * a.L, a) && *flat;
+    }
 }
 
 // Many lanes or few (see the top): whether every thread block of the kernel
@@ -1218,8 +1262,8 @@ bool many_lanes(const GatedArgs &a, size_t smem, cudaError_t *e) {
 
 template <typename T, bool ALIGNED, bool CK>
 cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
-    constexpr size_t ahead = Stage<T, ALIGNED, 3, kForwardKeep<CK, true>>::kBytes,
-                     kept = Stage<T, ALIGNED, 3, kForwardKeep<CK, false>>::kBytes;
+    constexpr size_t ahead = Stage<T, ALIGNED, 3, kForwardKeep<ALIGNED, CK, true>>::kBytes,
+                     kept = Stage<T, ALIGNED, 3, kForwardKeep<ALIGNED, CK, false>>::kBytes;
     constexpr auto *many = gated_forward_kernel<T, ALIGNED, CK, true>;
     constexpr auto *few = gated_forward_kernel<T, ALIGNED, CK, false>;
     cudaError_t e = cudaSuccess;
@@ -1232,12 +1276,22 @@ template <typename T, bool ALIGNED>
 cudaError_t forward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     return a.q ? forward_t<T, ALIGNED, true>(a, maps, st) : forward_t<T, ALIGNED, false>(a, maps, st);
 }
+// Whether TMA boxes of one warp's rows can be taken from a tensor.
+template <typename T>
+bool rows_aligned(const void *base, const GatedArgs &a) {
+    return on(base, 16) && a.D * (int64_t)sizeof(T) % 16 == 0 &&
+           (double)a.D * (double)a.L * sizeof(T) < 1.0e12;
+}
+
 template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
     Maps maps;
-    const bool aligned = on(a.y, 8) && on(a.q, 4) && make_map<T>(&maps.m[0], a.x, a) &&
-                         make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a);
-    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4);
+    const void *const in[3] = {a.x, a.r, a.i};
+    if (!encoder()) return cudaErrorNotSupported;
+    bool aligned = on(a.y, 8) && on(a.q, 4);
+    for (const void *p : in) aligned = aligned && rows_aligned<T>(p, a);
+    a.flat = true;
+    make_maps<T>(maps.m, in, 3, a, aligned, &a.flat);
     return aligned ? forward_c<T, true>(a, maps, st) : forward_c<T, false>(a, maps, st);
 }
 
@@ -1261,15 +1315,17 @@ cudaError_t backward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     Maps maps;
-    bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && make_map<T>(&maps.m[0], a.dy, a);
-    if (a.q) {
-        for (int w = 0; w < 3; ++w)
-            aligned = aligned && make_map<int8_t>(&maps.m[1 + w], a.q + w * a.batch * a.L * a.D, a);
-    } else {
-        aligned = aligned && make_map<T>(&maps.m[1], a.r, a) && make_map<T>(&maps.m[2], a.i, a) &&
-                  make_map<T>(&maps.m[3], a.x, a);
-    }
-    a.words = on(a.x, 4) && on(a.r, 4) && on(a.i, 4) && on(a.dy, 4) && on(a.q, 4);
+    if (!encoder()) return cudaErrorNotSupported;
+    const int64_t n = a.batch * a.L * a.D;
+    const void *const in[4] = {a.dy, a.r, a.i, a.x};
+    const void *const copies[3] = {a.q, a.q + n, a.q + 2 * n};
+    bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && rows_aligned<T>(a.dy, a);
+    for (int w = 0; w < 3; ++w)
+        aligned = aligned && (a.q ? rows_aligned<int8_t>(copies[w], a) : rows_aligned<T>(in[1 + w], a));
+    a.flat = true;
+    make_maps<T>(maps.m, in, a.q ? 1 : 4, a, aligned, &a.flat);
+    if (a.q && aligned) make_maps<int8_t>(maps.m + 1, copies, 3, a, aligned, &a.flat);
+    if (a.q && !aligned) a.flat = flat_map<int8_t>(&maps.m[1], a.q, 3 * a.batch * a.L, a) && a.flat;
     cudaError_t e = aligned ? backward_c<T, true>(a, maps, st) : backward_c<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);

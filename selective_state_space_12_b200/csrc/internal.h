@@ -144,7 +144,7 @@ struct GatedArgs {
     float *last = nullptr;         // h_final, or dh0
     float *dlam_part = nullptr;    // (b, nb, D)
     float *scale = nullptr;        // (D): c softplus(lam)
-    bool words = false;            // input tensors start on 4 bytes
+    bool flat = false;             // rows that start anywhere come by TMA too
     unsigned *counter = nullptr, *abort = nullptr, *err = nullptr;
     unsigned long long *ends = nullptr, *maps = nullptr;  // what tiles publish
     long long wait = 0;
