@@ -108,6 +108,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Sum of the rows first, first + step, ... of column d of a (rows, width) array
+// (0 past the last column), eight loads in flight.
+__device__ __forceinline__ float column_sum(const float *part, int64_t rows, int64_t width,
+                                            int64_t d, int first, int step) {
+    if (d >= width) return 0.f;
+    float s[8] = {};
+    const float *p = part + first * width + d;
+    const int64_t stride = step * width;
+    int64_t i = first;
+    for (; i + 7 * step < rows; i += 8 * step, p += 8 * stride) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += p[j * stride];
+    }
+    for (; i < rows; i += step, p += stride) s[0] += *p;
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
 // Inclusive prefix sum over a block of up to 1024 threads; `warp_tot` is
 // shared scratch of 32 floats. Every thread of the block must call it.
 __device__ __forceinline__ float block_inclusive_scan(float v, float *warp_tot) {

@@ -1100,19 +1100,17 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
 }
 
 // dlam: the blocks' sums over batch and blocks, times the channel's factor.
-__global__ void gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
-                                  float *__restrict__ dlam, int64_t rows, int64_t D) {
-    __shared__ float red[8][33];
+__global__ void __launch_bounds__(1024)
+gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
+                  float *__restrict__ dlam, int64_t rows, int64_t D) {
+    __shared__ float red[32][33];
     const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    float s = 0.f;
-    if (d < D)
-        for (int64_t i = threadIdx.y; i < rows; i += 8) s += part[i * D + d];
+    const float s = column_sum(part, rows, D, d, threadIdx.y, 32);
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && d < D) {
-        for (int j = 1; j < 8; ++j) s += red[j][threadIdx.x];
-        dlam[d] = s * lam_ratio(lam[d]);
-    }
+    const float v = warp_sum(red[threadIdx.x][threadIdx.y]);
+    const int64_t mine = (int64_t)blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && mine < D) dlam[mine] = v * lam_ratio(lam[mine]);
 }
 
 template <typename T>
@@ -1329,7 +1327,7 @@ cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     cudaError_t e = aligned ? backward_c<T, true>(a, maps, st) : backward_c<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
-    gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 8), 0, st>>>(
+    gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 32), 0, st>>>(
         a.dlam_part, a.lam, dlam, a.batch * a.nb, a.D);
     launch_end(st);
     return cudaGetLastError();

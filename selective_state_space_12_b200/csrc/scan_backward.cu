@@ -27,8 +27,9 @@
 //   3. scan_bwd_main: the same again inside a chunk over its eight pieces of four
 //      tokens (a warp each), then each piece's states forward and gradients
 //      back, from registers;
-//   4. sums of dB and dC over blocks of channels, and of dA, dDskip and the
-//      bias's gradient over batch and chunks. No atomics: every sum has one order.
+//   4. scan_bwd_finish: sums of dB and dC over blocks of channels, and of dA, dDskip
+//      and the bias's gradient over batch and chunks. No atomics: every sum has
+//      one order.
 #include <math.h>
 
 #include <type_traits>
@@ -745,36 +746,51 @@ __global__ void __launch_bounds__(kMainThreads, 2) scan_bwd_main(const BwdArgs a
         }
 }
 
-// dB and dC: the sum over blocks of channels.
-__global__ void scan_bwd_rows(const float2 *__restrict__ part, float *__restrict__ dB,
-                              float *__restrict__ dC, int parts, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n) return;
-    float b = 0.f, c = 0.f;
-    for (int j = 0; j < parts; ++j) {
-        const float2 v = part[j * n + i];
-        b += v.x;
-        c += v.y;
+// The last sums, a kernel: dB and dC over blocks of channels (blocks of threads
+// [0, row_blocks)), then dA, and dDskip and the bias's gradient (the even and odd
+// columns of d_part), over batch and chunks.
+struct Sums {
+    const float2 *rows;
+    float *dB, *dC;
+    int parts;
+    int64_t n;  // b L G N
+    const float *dA_part, *d_part;
+    float *dA, *dD, *ddt_bias;
+    int64_t chunks, wide_A, wide_d;
+    unsigned row_blocks, A_blocks;
+};
+__global__ void __launch_bounds__(512) scan_bwd_finish(const Sums q) {
+    const int x = threadIdx.x, y = threadIdx.y, tid = y * 32 + x;
+    if (blockIdx.x < q.row_blocks) {
+        const int64_t i = (int64_t)blockIdx.x * 512 + tid;
+        if (i >= q.n) return;
+        float b = 0.f, c = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < q.parts; ++j) {
+            const float2 v = q.rows[j * q.n + i];
+            b += v.x;
+            c += v.y;
+        }
+        q.dB[i] = b;
+        q.dC[i] = c;
+        return;
     }
-    dB[i] = b;
-    dC[i] = c;
-}
-
-// Sums over batch and chunks of rows of `width` floats; out2 takes the odd
-// columns where given.
-__global__ void scan_bwd_params(const float *__restrict__ part, float *__restrict__ out,
-                                float *__restrict__ out2, bool pairs, int64_t rows, int64_t width) {
-    __shared__ float red[8][33];
-    const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    float s = 0.f;
-    if (i < width)
-        for (int64_t j = threadIdx.y; j < rows; j += 8) s += part[j * width + i];
-    red[threadIdx.y][threadIdx.x] = s;
+    const unsigned block = blockIdx.x - q.row_blocks;
+    const bool is_A = block < q.A_blocks;
+    const int64_t i = (int64_t)(is_A ? block : block - q.A_blocks) * 32 + x;
+    const int64_t wide = is_A ? q.wide_A : q.wide_d;
+    __shared__ float red[16][33];
+    red[y][x] = column_sum(is_A ? q.dA_part : q.d_part, q.chunks, wide, i, y, 16);
     __syncthreads();
-    if (threadIdx.y == 0 && i < width) {
-        for (int j = 1; j < 8; ++j) s += red[j][threadIdx.x];
-        float *to = pairs ? ((i & 1) ? out2 : out) : out;
-        if (to) to[pairs ? i / 2 : i] = s;
+    if (y != 0 || i >= wide) return;
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s += red[j][x];
+    if (is_A) {
+        q.dA[i] = s;
+    } else {
+        float *to = (i & 1) ? q.ddt_bias : q.dD;
+        if (to) to[i / 2] = s;
     }
 }
 
@@ -843,18 +859,25 @@ cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *d
     launch_begin("scan_bwd_main", st);
     scan_bwd_main<T, N, ZOH><<<grid, kMainThreads, main_smem, st>>>(a);
     launch_end(st);
-    const int64_t n = a.batch * a.L * a.G * N;
-    launch_begin("scan_bwd_rows", st);
-    scan_bwd_rows<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(
-        reinterpret_cast<const float2 *>(a.bc_part), a.dB, a.dC, a.blocks_per_group, n);
-    launch_end(st);
-    launch_begin("scan_bwd_params", st);
-    scan_bwd_params<<<(unsigned)((a.D * N + 31) / 32), dim3(32, 8), 0, st>>>(
-        a.dA_part, dA, nullptr, false, a.batch * a.nc, a.D * N);
-    launch_end(st);
-    launch_begin("scan_bwd_params", st);
-    scan_bwd_params<<<(unsigned)((2 * a.D + 31) / 32), dim3(32, 8), 0, st>>>(
-        a.d_part, dD, ddt_bias, true, a.batch * a.nc, 2 * a.D);
+    Sums q;
+    q.rows = reinterpret_cast<const float2 *>(a.bc_part);
+    q.dB = a.dB;
+    q.dC = a.dC;
+    q.parts = a.blocks_per_group;
+    q.n = a.batch * a.L * a.G * N;
+    q.dA_part = a.dA_part;
+    q.d_part = a.d_part;
+    q.dA = dA;
+    q.dD = dD;
+    q.ddt_bias = ddt_bias;
+    q.chunks = a.batch * a.nc;
+    q.wide_A = a.D * N;
+    q.wide_d = 2 * a.D;
+    q.row_blocks = (unsigned)((q.n + 511) / 512);
+    q.A_blocks = (unsigned)((q.wide_A + 31) / 32);
+    launch_begin("scan_bwd_finish", st);
+    scan_bwd_finish<<<q.row_blocks + q.A_blocks + (unsigned)((q.wide_d + 31) / 32), dim3(32, 16), 0,
+                      st>>>(q);
     launch_end(st);
     return cudaGetLastError();
 }
