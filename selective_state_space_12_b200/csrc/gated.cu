@@ -1189,23 +1189,11 @@ cudaError_t start(const char *name, size_t smem, bool eager, const GatedArgs &a,
 
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault,
-                                                &q) == cudaSuccess &&
-                        q == cudaDriverEntryPointSuccess;
-        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
-    }();
-    return fn;
-}
-
 template <typename T>
 bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4],
             const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return encoder()(m, sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+    return tensor_map_encoder()(m, sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                         : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                      4, const_cast<void *>(base), dims, strides, box, estr,
@@ -1219,7 +1207,7 @@ bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4],
 template <typename T>
 bool warp_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
     const uint64_t row = (uint64_t)a.D * sizeof(T);
-    if (!encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
+    if (!tensor_map_encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
     return encode<T>(m, base, {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1},
                      {row, row * (uint64_t)a.L, row * (uint64_t)a.L}, {kTileCh, kRun, 1, 1});
 }
@@ -1231,7 +1219,7 @@ bool flat_map(CUtensorMap *m, const void *base, int64_t rows, const GatedArgs &a
     using F = FlatRows<T, 1>;
     const uint64_t groups = (uint64_t)rows / F::kSlots;
     const uint64_t row = (uint64_t)a.D * sizeof(T) * F::kSlots;
-    if (!encoder() || !on(base, 16) || groups == 0 || groups >= 1ull << 31 ||
+    if (!tensor_map_encoder() || !on(base, 16) || groups == 0 || groups >= 1ull << 31 ||
         row * groups >= 1ull << 40)
         return false;
     return encode<T>(m, base, {(cuuint64_t)a.D * F::kSlots, groups, 1, 1},
@@ -1285,7 +1273,7 @@ template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
     Maps maps;
     const void *const in[3] = {a.x, a.r, a.i};
-    if (!encoder()) return cudaErrorNotSupported;
+    if (!tensor_map_encoder()) return cudaErrorNotSupported;
     bool aligned = on(a.y, 8) && on(a.q, 4);
     for (const void *p : in) aligned = aligned && rows_aligned<T>(p, a);
     a.flat = true;
@@ -1313,7 +1301,7 @@ cudaError_t backward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     Maps maps;
-    if (!encoder()) return cudaErrorNotSupported;
+    if (!tensor_map_encoder()) return cudaErrorNotSupported;
     const int64_t n = a.batch * a.L * a.D;
     const void *const in[4] = {a.dy, a.r, a.i, a.x};
     const void *const copies[3] = {a.q, a.q + n, a.q + 2 * n};
@@ -1362,6 +1350,18 @@ size_t carve(const Problem &pr, GatedArgs &a, void *ws, bool back) {
 }
 
 }  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault,
+                                                &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
 
 int64_t gated_blocks(const Problem &pr) { return (pr.seqlen + kBlock - 1) / kBlock; }
 

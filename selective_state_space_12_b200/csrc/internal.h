@@ -1,6 +1,8 @@
 // Host-side declarations shared by the libssd translation units.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -162,6 +164,9 @@ ssd_status gated_step_launch(const Problem &pr, float *h, const void *x, const v
 ssd_status step_launch(const Problem &pr, float *h, const void *x, const void *dt,
                        const float *A, const void *B, const void *C, const float *D,
                        void *y, cudaStream_t st, const DtPre &pre = DtPre());
+
+// cuTensorMapEncodeTiled of the driver, or NULL.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Launch accounting: call around every kernel launch (see profile.cu).
 void launch_begin(const char *name, cudaStream_t st);

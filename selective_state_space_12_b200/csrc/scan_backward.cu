@@ -30,9 +30,8 @@
 //   4. scan_bwd_finish: sums of dB and dC over blocks of channels, and of dA, dDskip
 //      and the bias's gradient over batch and chunks. No atomics: every sum has
 //      one order.
+#include <cudaTypedefs.h>
 #include <math.h>
-
-#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -107,9 +106,10 @@ __device__ __forceinline__ float prepare_step(float raw, float bias, const StepA
 }
 
 // One pair of state entries at one step: F is exp(dt A) (Euler) or
-// E = exp(dt A) - 1 (hold), the latter by its series where |z| < 1/4, z = dt A
-// (remainder below z^6 / 5040 < 5e-8 relative), else from exp2, whose error of
-// 2^-22 is then at most 1e-6 of it.
+// E = exp(dt A) - 1 (hold). With y = dt A log2 e both start from exp2(y); the hold
+// takes E by its series in y where |y| < 3/8 (the sixth term, (y ln 2)^6 / 6!, ends
+// it: the next is below 7e-8 relative), else from exp2, whose error of 2^-22 is
+// then at most 1e-6 of it.
 using tc::f2;
 using tc::f2_add;
 using tc::f2_fma;
@@ -121,23 +121,24 @@ __device__ __forceinline__ f2 f2_both(float v) { return f2_pack(v, v); }
 
 template <bool ZOH>
 struct Decay {
-    f2 A, Al;  // A (hold: kept off zero) and A log2 e
+    f2 Al;  // A log2 e (hold: A kept off zero)
     __device__ __forceinline__ f2 at(f2 dt) const {
-        float z0, z1, l0, l1;
-        f2_unpack(f2_mul(dt, Al), l0, l1);
-        const f2 e = f2_pack(tc::fast_exp2(l0), tc::fast_exp2(l1));
+        const f2 y = f2_mul(dt, Al);
+        float y0, y1;
+        f2_unpack(y, y0, y1);
+        const f2 e = f2_pack(tc::fast_exp2(y0), tc::fast_exp2(y1));
         if (!ZOH) return e;
-        const f2 z = f2_mul(dt, A);
-        f2 p = f2_fma(f2_both(1.f / 720.f), z, f2_both(1.f / 120.f));
-        p = f2_fma(p, z, f2_both(1.f / 24.f));
-        p = f2_fma(p, z, f2_both(1.f / 6.f));
-        p = f2_fma(p, z, f2_both(0.5f));
-        p = f2_fma(p, z, f2_both(1.f));
+        constexpr double k = 0.693147180559945309;  // ln 2
+        f2 p = f2_fma(f2_both((float)(k * k * k * k * k * k / 720)), y,
+                      f2_both((float)(k * k * k * k * k / 120)));
+        p = f2_fma(p, y, f2_both((float)(k * k * k * k / 24)));
+        p = f2_fma(p, y, f2_both((float)(k * k * k / 6)));
+        p = f2_fma(p, y, f2_both((float)(k * k / 2)));
+        p = f2_fma(p, y, f2_both((float)k));
         float s0, s1, e0, e1;
-        f2_unpack(f2_mul(z, p), s0, s1);
+        f2_unpack(f2_mul(y, p), s0, s1);
         f2_unpack(f2_add(e, f2_both(-1.f)), e0, e1);
-        f2_unpack(z, z0, z1);
-        return f2_pack(fabsf(z0) < 0.25f ? s0 : e0, fabsf(z1) < 0.25f ? s1 : e1);
+        return f2_pack(fabsf(y0) < 0.375f ? s0 : e0, fabsf(y1) < 0.375f ? s1 : e1);
     }
 };
 
@@ -161,25 +162,34 @@ struct BwdArgs {
     int tiles_per_group, tiles_per_block, blocks_per_group;
     StepArgs step;
     bool words;          // x, dt and dy start on 4 bytes
+    unsigned *err;
+    long long wait;
 };
 
 // Shared memory of the staged tile. Channels' rows of tokens, as stored, arrive
-// in `words` a tile ahead by asynchronous copies of the 4-byte words that cover
-// them, and are spread from there as floats, tokens along a row.
-template <typename T, int N, int CH>
-struct __align__(16) Tile {
+// in `words` a tile ahead and are spread from there as floats, tokens along a
+// row. Where rows start on 16 bytes (ALIGNED) they come by one TMA load a tensor,
+// elsewhere by asynchronous copies of the 4-byte words that cover them.
+struct Maps {
+    CUtensorMap m[3];
+};
+constexpr long long kDrain = 1ll << 24;  // cycles: a wait for loads in flight at an early end
+template <typename T, int N, int CH, bool ALIGNED>
+struct __align__(128) Tile {
     static constexpr int kState = CH * N;
+    static constexpr int kPitch = CH * (int)sizeof(T) + (ALIGNED ? 0 : 16);
+    __align__(128) unsigned char words[3][kChunk][kPitch];
     float x[CH][kRow], dt[CH][kRow], dy[CH][kRow];
     float B[kChunk][N], C[kChunk][N];
     float A[kState], Al[kState], invA[kState];
-    // as they arrive: rows of x, dt and dy, A, bias and Dskip
-    unsigned char words[3][kChunk][CH * (int)sizeof(T) + 16];
-    float next_A[kState], next_bias[CH], next_Ds[CH];
+    float next_A[kState], next_bias[CH], next_Ds[CH];  // as they arrive
+    uint64_t bar;
 };
-template <typename T, int N, int CH>
-struct MainTile : Tile<T, N, CH> {
-    float fac[CH][kRow], dx[CH][kRow];
+template <typename T, int N, int CH, bool ALIGNED>
+struct MainTile : Tile<T, N, CH, ALIGNED> {
+    float fac[CH][kRow];
     float S[kPieces][CH * N], R[kPieces][CH * N], P[kPieces][CH * N];
+    float dd[kPieces][CH], db[kPieces][CH];
     float Ds[CH];
     int tiny;
 };
@@ -219,12 +229,19 @@ __device__ __forceinline__ bool by_words(const BwdArgs &a, const Place &p, int64
     return sizeof(T) == 4 || (a.words && !(p.b == a.batch - 1 && p.chunk == a.nc - 1 &&
                                            d0 + CH >= a.D));
 }
-template <typename T, int N, int CH, int THREADS>
-__device__ __forceinline__ void request(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
-                                        Tile<T, N, CH> &s) {
+template <typename T, int N, int CH, bool ALIGNED, int THREADS>
+__device__ __forceinline__ void request(const BwdArgs &a, const Maps &maps, const Place &p, int64_t d0,
+                                        int64_t dend, Tile<T, N, CH, ALIGNED> &s) {
     constexpr int kE = (int)sizeof(T), kWords = CH * kE / 4;  // of a row that starts on one
-    const void *const src[3] = {a.x, a.dt, a.dy};
-    if (by_words<T, CH>(a, p, d0)) {
+    if constexpr (ALIGNED) {
+        if (threadIdx.x == 0) {
+            tc::mbar_arrive_expect_tx(&s.bar, sizeof(s.words));
+#pragma unroll
+            for (int w = 0; w < 3; ++w)
+                tc::tma_load_4d(s.words[w], &maps.m[w], &s.bar, (int)d0, (int)p.t0, (int)p.b, 0);
+        }
+    } else if (by_words<T, CH>(a, p, d0)) {
+        const void *const src[3] = {a.x, a.dt, a.dy};
         const int len = (int)(dend - d0 < CH ? dend - d0 : CH);
         const int i = threadIdx.x % kWords, t0 = threadIdx.x / kWords;
 #pragma unroll
@@ -251,13 +268,30 @@ __device__ __forceinline__ void request(const BwdArgs &a, const Place &p, int64_
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
+// Waits for the requested tile, all threads; false when the wait ran out.
+template <typename T, int N, int CH, bool ALIGNED>
+__device__ __forceinline__ bool arrived(const BwdArgs &a, Tile<T, N, CH, ALIGNED> &s, uint32_t &parity) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if constexpr (!ALIGNED) {
+        __syncthreads();
+        return true;
+    }
+    if (__syncthreads_and(tc::mbar_wait(&s.bar, parity, a.wait))) {
+        parity ^= 1;
+        return true;
+    }
+    if (threadIdx.x == 0) atomicExch(a.err, 0x5bacd001u);
+    tc::mbar_wait(&s.bar, parity, kDrain);
+    return false;
+}
+
 // The requested tile as floats, dt prepared; channels and tokens past the end
 // are zeros (dt = 0: a = 1, w = 0). Also A and what follows from it.
-template <typename T, int N, int CH, bool ZOH, bool GRAD, int THREADS>
+template <typename T, int N, int CH, bool ALIGNED, bool ZOH, bool GRAD, int THREADS>
 __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
-                                       Tile<T, N, CH> &s, float (*fac)[kRow]) {
+                                       Tile<T, N, CH, ALIGNED> &s, float (*fac)[kRow]) {
     const void *const src[3] = {a.x, a.dt, a.dy};
-    const bool words = by_words<T, CH>(a, p, d0);
+    const bool words = ALIGNED || by_words<T, CH>(a, p, d0);
     // eight channels by four runs of four tokens a warp: rows are written 16 bytes at a time
     const int64_t base = (p.b * a.L + p.t0) * a.D + d0;
     for (int i = threadIdx.x; i < CH * (kChunk / 4); i += THREADS) {
@@ -271,11 +305,15 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
             if (has && t0 + j < p.n) {
 #pragma unroll
                 for (int w = 0; w < 3; ++w) {
-                    const T *row = static_cast<const T *>(src[w]) + base + (t0 + j) * a.D;
-                    if (words)
-                        row = reinterpret_cast<const T *>(
-                            &s.words[w][t0 + j][reinterpret_cast<uintptr_t>(row) & 3]);
-                    v[w][j] = to_f(row[c]);
+                    if constexpr (ALIGNED) {
+                        v[w][j] = to_f(reinterpret_cast<const T *>(s.words[w][t0 + j])[c]);
+                    } else {
+                        const T *row = static_cast<const T *>(src[w]) + base + (t0 + j) * a.D;
+                        if (words)
+                            row = reinterpret_cast<const T *>(
+                                &s.words[w][t0 + j][reinterpret_cast<uintptr_t>(row) & 3]);
+                        v[w][j] = to_f(row[c]);
+                    }
                 }
                 v[1][j] = prepare_step<GRAD>(v[1][j], bias, a.step, f[j]);
             }
@@ -296,8 +334,8 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
     }
     return tiny;
 }
-template <typename T, int N, int CH, int THREADS>
-__device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Tile<T, N, CH> &s) {
+template <typename T, int N, int CH, bool ALIGNED, int THREADS>
+__device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Tile<T, N, CH, ALIGNED> &s) {
     const T *B = static_cast<const T *>(a.B), *C = static_cast<const T *>(a.C);
     for (int i = threadIdx.x; i < kChunk * N; i += THREADS) {
         const int t = i / N, n = i % N;
@@ -336,8 +374,8 @@ __device__ __forceinline__ f2 times_decay(f2 v, f2 F) {
 
 // The map of a run of tokens for one thread's four states: end state S from
 // zero, gradient R handed to the left when none comes from the right, product P.
-template <typename T, int N, int CH, bool ZOH, int TOKENS>
-__device__ __forceinline__ void run_sums(const Tile<T, N, CH> &s, int c, int t0, int n0,
+template <typename T, int N, int CH, bool ALIGNED, bool ZOH, int TOKENS>
+__device__ __forceinline__ void run_sums(const Tile<T, N, CH, ALIGNED> &s, int c, int t0, int n0,
                                          const Decay<ZOH> (&A)[2], f2 (&S)[2], f2 (&R)[2],
                                          f2 (&P)[2]) {
 #pragma unroll
@@ -367,50 +405,58 @@ __device__ __forceinline__ void run_sums(const Tile<T, N, CH> &s, int c, int t0,
     }
 }
 
-template <typename T, int N, int CH, bool ZOH>
-__device__ __forceinline__ void load_A(const Tile<T, N, CH> &s, int at, Decay<ZOH> (&A)[2]) {
-    f2 v[2], l[2];
-    load4x(&s.A[at], v);
+template <typename T, int N, int CH, bool ALIGNED, bool ZOH>
+__device__ __forceinline__ void load_A(const Tile<T, N, CH, ALIGNED> &s, int at, Decay<ZOH> (&A)[2]) {
+    f2 l[2];
     load4x(&s.Al[at], l);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        A[k].A = v[k];
-        A[k].Al = l[k];
-    }
+    A[0].Al = l[0];
+    A[1].Al = l[1];
 }
 
-template <typename T, int N, bool ZOH>
-__global__ void __launch_bounds__(kCh *N / kQ) scan_bwd_sums(const BwdArgs a) {
+template <typename T, int N, bool ZOH, bool ALIGNED>
+__global__ void __launch_bounds__(kCh *N / kQ, 640 / (kCh * N / kQ))
+scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
     constexpr int CH = kCh, kThreads = CH * N / kQ, kLanes = N / kQ;
-    extern __shared__ __align__(16) unsigned char raw[];
-    Tile<T, N, CH> &s = *reinterpret_cast<Tile<T, N, CH> *>(raw);
+    extern __shared__ __align__(128) unsigned char raw[];
+    using S_ = Tile<T, N, CH, ALIGNED>;
+    S_ &s = *reinterpret_cast<S_ *>(raw);
     const Place p = place(a);
     const int64_t dend = (p.g + 1) * a.gch, dstart = p.g * a.gch + (int64_t)p.tile0 * CH;
-    request<T, N, CH, kThreads>(a, p, dstart, dend, s);
-    stage_rows<T, N, CH, kThreads>(a, p, s);
+    uint32_t parity = 0;
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&s.bar, 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    request<T, N, CH, ALIGNED, kThreads>(a, maps, p, dstart, dend, s);
+    stage_rows<T, N, CH, ALIGNED, kThreads>(a, p, s);
+    const int c = threadIdx.x / kLanes, n0 = (threadIdx.x % kLanes) * kQ;
     for (int k = 0; k < p.tiles; ++k) {
         const int64_t d0 = dstart + (int64_t)k * CH;
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (!arrived(a, s, parity)) return;
+        spread<T, N, CH, ALIGNED, ZOH, false, kThreads>(a, p, d0, dend, s, nullptr);
         __syncthreads();
-        spread<T, N, CH, ZOH, false, kThreads>(a, p, d0, dend, s, nullptr);
-        __syncthreads();
-        if (k + 1 < p.tiles) request<T, N, CH, kThreads>(a, p, d0 + CH, dend, s);
-        const int c = threadIdx.x / kLanes, n0 = (threadIdx.x % kLanes) * kQ;
+        if (k + 1 < p.tiles) request<T, N, CH, ALIGNED, kThreads>(a, maps, p, d0 + CH, dend, s);
         const bool has = d0 + c < dend;
         Decay<ZOH> A[2];
         f2 S[2], R[2], P[2];
-        load_A<T, N, CH, ZOH>(s, c * N + n0, A);
-        run_sums<T, N, CH, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
+        load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
+        run_sums<T, N, CH, ALIGNED, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
         if (has) {
             const int64_t at = (p.b * a.nc + p.chunk) * a.D + d0 + c;
             store4x(&a.S[at * N + n0], S);
             store4x(&a.R[at * N + n0], R);
             if (n0 == 0) {
                 float sum = 0.f;
-                for (int t = 0; t < kChunk; ++t) sum += s.dt[c][t];
+#pragma unroll
+                for (int t = 0; t < kChunk; t += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&s.dt[c][t]);
+                    sum += (v.x + v.y) + (v.z + v.w);
+                }
                 a.steps[at] = sum;
             }
         }
+        __syncthreads();  // the tile has been read
     }
 }
 
@@ -497,105 +543,124 @@ __device__ __forceinline__ void share_sums(float (&u)[kPiece], float (&v)[kPiece
     }
 }
 
-// The hold's dw/dA = (dt e^z - w) / A of a pair, for A near zero: with
-// phi1 = (e^z - 1) / z and phi2 = (phi1 - 1) / z it is dt^2 (phi1 - phi2),
-// where |z| < 1/4 from the series of phi2 (remainder below z^5/5040 < 2e-7).
-__device__ __forceinline__ f2 slope(float dt, f2 A, f2 invA, f2 E) {
-    float a[2], i[2], e[2], r[2];
-    f2_unpack(A, a[0], a[1]);
-    f2_unpack(invA, i[0], i[1]);
-    f2_unpack(E, e[0], e[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float z = dt * a[k];
-        float phi2 = 1.f / 720.f;
-        phi2 = fmaf(phi2, z, 1.f / 120.f);
-        phi2 = fmaf(phi2, z, 1.f / 24.f);
-        phi2 = fmaf(phi2, z, 1.f / 6.f);
-        phi2 = fmaf(phi2, z, 0.5f);
-        r[k] = fabsf(z) < 0.25f ? dt * dt * (fmaf(z, phi2, 1.f) - phi2)
-                                : (fmaf(dt, e[k], dt) - e[k] * i[k]) * i[k];
-    }
-    return f2_pack(r[0], r[1]);
+// The hold's dA of one piece, term by term, dt a r h + r x B dw/dA, where some |A|
+// is near zero: dw/dA = (dt e^z - w) / A is dt^2 (phi1 - phi2), with
+// phi1 = (e^z - 1) / z and phi2 = (phi1 - 1) / z, where |z| < 1/4 from the series of
+// phi2 (remainder below z^5/5040 < 2e-7). Replaces what the main loop left in P.
+template <typename T, int N, int CH, bool ALIGNED>
+__device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int piece, int lane) {
+    constexpr int kLanes = N / kQ;
+    for (int c = lane / kLanes; c < CH; c += 32 / kLanes)
+        for (int k = 0; k < kQ; ++k) {
+            const int n = (lane % kLanes) * kQ + k, at = c * N + n;
+            const float A = s.A[at], invA = s.invA[at];
+            float g[kPiece], E[kPiece], st = s.S[piece][at], carry = s.R[piece][at], dA = 0.f;
+            for (int t = 0; t < kPiece; ++t) {
+                const int tok = piece * kPiece + t;
+                float unused;
+                f2_unpack(Decay<true>{f2_both(s.Al[at])}.at(f2_both(s.dt[c][tok])), E[t], unused);
+                g[t] = st;
+                st = fmaf(E[t], st + s.x[c][tok] * s.B[tok][n], st);
+            }
+            for (int t = kPiece - 1; t >= 0; --t) {
+                const int tok = piece * kPiece + t;
+                const float dt = s.dt[c][tok], in = s.x[c][tok] * s.B[tok][n], z = dt * A;
+                const float r = fmaf(s.dy[c][tok], s.C[tok][n], carry);
+                carry = fmaf(r, E[t], r);
+                float phi2 = 1.f / 720.f;
+                phi2 = fmaf(phi2, z, 1.f / 120.f);
+                phi2 = fmaf(phi2, z, 1.f / 24.f);
+                phi2 = fmaf(phi2, z, 1.f / 6.f);
+                phi2 = fmaf(phi2, z, 0.5f);
+                const float slope = fabsf(z) < 0.25f ? dt * dt * (fmaf(z, phi2, 1.f) - phi2)
+                                                     : (fmaf(dt, E[t], dt) - E[t] * invA) * invA;
+                dA = fmaf(dt * carry, g[t] * invA, fmaf(r * in, slope, dA));
+            }
+            s.P[piece][at] = dA;
+        }
 }
 
-template <typename T, int N, bool ZOH>
-__global__ void __launch_bounds__(kMainThreads, 2) scan_bwd_main(const BwdArgs a) {
+template <typename T, int N, bool ZOH, bool ALIGNED>
+__global__ void __launch_bounds__(kMainThreads, 2)
+scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
     constexpr int CH = kCh, kLanes = N / kQ, kPerWarp = 32 / kLanes, kState = CH * N;
-    extern __shared__ __align__(16) unsigned char raw[];
-    MainTile<T, N, CH> &s = *reinterpret_cast<MainTile<T, N, CH> *>(raw);
+    constexpr int kShare = kPiece / kLanes;  // tokens of a piece whose dx and ddt a lane ends with
+    extern __shared__ __align__(128) unsigned char raw[];
+    using S_ = MainTile<T, N, CH, ALIGNED>;
+    S_ &s = *reinterpret_cast<S_ *>(raw);
     const Place p = place(a);
-    const int64_t dend = (p.g + 1) * a.gch;
+    const int64_t dend = (p.g + 1) * a.gch, dstart = p.g * a.gch + (int64_t)p.tile0 * CH;
     const int tid = threadIdx.x, lane = tid & 31, piece = tid >> 5;
-    const int n0 = (lane % kLanes) * kQ, t0 = piece * kPiece;
+    const int n0 = (lane % kLanes) * kQ, t0 = piece * kPiece, cl = lane / kLanes;
+    const int share0 = t0 + (lane % kLanes) * kShare;  // the first of this lane's tokens
     const f2 none = f2_both(0.f);
+    uint32_t parity = 0;
     f2 accB[kPiece][2], accC[kPiece][2];
 #pragma unroll
     for (int t = 0; t < kPiece; ++t)
 #pragma unroll
         for (int k = 0; k < 2; ++k) accB[t][k] = accC[t][k] = none;
-    const int64_t dstart = p.g * a.gch + (int64_t)p.tile0 * CH;
-    request<T, N, CH, kMainThreads>(a, p, dstart, dend, s);
-    stage_rows<T, N, CH, kMainThreads>(a, p, s);
+    if (tid == 0) {
+        tc::mbar_init(&s.bar, 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    request<T, N, CH, ALIGNED, kMainThreads>(a, maps, p, dstart, dend, s);
+    stage_rows<T, N, CH, ALIGNED, kMainThreads>(a, p, s);
+    const int64_t row = (p.b * a.nc + p.chunk) * a.D;
     for (int tile = 0; tile < p.tiles; ++tile) {
         const int64_t d0 = dstart + (int64_t)tile * CH;
-        const int64_t row = (p.b * a.nc + p.chunk) * a.D;
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const int here = (int)(dend - d0 < CH ? dend - d0 : CH);  // channels
         if (tid == 0) s.tiny = 0;
-        __syncthreads();
-        if (spread<T, N, CH, ZOH, true, kMainThreads>(a, p, d0, dend, s, s.fac)) s.tiny = 1;
-        if (tid < CH) s.Ds[tid] = (a.Dskip && d0 + tid < dend) ? s.next_Ds[tid] : 0.f;
-        // this thread's links of the chains over pieces
-        constexpr int kOwn = (kState + kMainThreads - 1) / kMainThreads;
-        float link_h[kOwn], link_r[kOwn];
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int at = tid + i * kMainThreads;
-            const bool has = at < kState && d0 + at / N < dend;
-            link_h[i] = has ? a.S[(row + d0) * N + at] : 0.f;
-            link_r[i] = has ? a.R[(row + d0) * N + at] : 0.f;
+        if (!arrived(a, s, parity)) return;
+        if (spread<T, N, CH, ALIGNED, ZOH, true, kMainThreads>(a, p, d0, dend, s, s.fac)) s.tiny = 1;
+        if (tid < CH) s.Ds[tid] = (a.Dskip && tid < here) ? s.next_Ds[tid] : 0.f;
+        // this thread's pair of links of the chains over pieces
+        float2 link_h = make_float2(0.f, 0.f), link_r = link_h;
+        if (2 * tid < here * N) {
+            link_h = *reinterpret_cast<const float2 *>(&a.S[(row + d0) * N + 2 * tid]);
+            link_r = *reinterpret_cast<const float2 *>(&a.R[(row + d0) * N + 2 * tid]);
         }
         __syncthreads();
-        if (tile + 1 < p.tiles) request<T, N, CH, kMainThreads>(a, p, d0 + CH, dend, s);
+        if (tile + 1 < p.tiles) request<T, N, CH, ALIGNED, kMainThreads>(a, maps, p, d0 + CH, dend, s);
 #pragma unroll 1
-        for (int c = lane / kLanes; c < CH; c += kPerWarp) {
+        for (int c = cl; c < CH; c += kPerWarp) {
             Decay<ZOH> A[2];
             f2 S[2], R[2], P[2];
-            load_A<T, N, CH, ZOH>(s, c * N + n0, A);
-            run_sums<T, N, CH, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
+            load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
+            run_sums<T, N, CH, ALIGNED, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
             store4x(&s.S[piece][c * N + n0], S);
             store4x(&s.R[piece][c * N + n0], R);
             store4x(&s.P[piece][c * N + n0], P);
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int at = tid + i * kMainThreads;
-            if (at >= kState) break;
-            float P[kPieces], S[kPieces], R[kPieces];
+        if (2 * tid < kState) {
+            f2 P[kPieces], S[kPieces], R[kPieces];
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                P[j] = s.P[j][at];
-                S[j] = s.S[j][at];
-                R[j] = s.R[j][at];
+                P[j] = *reinterpret_cast<const f2 *>(&s.P[j][2 * tid]);
+                S[j] = *reinterpret_cast<const f2 *>(&s.S[j][2 * tid]);
+                R[j] = *reinterpret_cast<const f2 *>(&s.R[j][2 * tid]);
             }
+            f2 h = f2_pack(link_h.x, link_h.y), r = f2_pack(link_r.x, link_r.y);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
                 const int k = kPieces - 1 - j;
-                s.S[j][at] = link_h[i];
-                s.R[k][at] = link_r[i];
-                link_h[i] = fmaf(P[j], link_h[i], S[j]);
-                link_r[i] = fmaf(P[k], link_r[i], R[k]);
+                *reinterpret_cast<f2 *>(&s.S[j][2 * tid]) = h;
+                *reinterpret_cast<f2 *>(&s.R[k][2 * tid]) = r;
+                h = f2_fma(P[j], h, S[j]);
+                r = f2_fma(P[k], r, R[k]);
             }
         }
         __syncthreads();
+        float *dx = a.dx + (p.b * a.L + p.t0 + share0) * a.D + d0 + cl;
+        float *ddt = a.ddt + (dx - a.dx);
 #pragma unroll 1
-        for (int c = lane / kLanes; c < CH; c += kPerWarp) {
+        for (int c = cl; c < CH; c += kPerWarp, dx += kPerWarp, ddt += kPerWarp) {
             Decay<ZOH> A[2];
-            f2 invA[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
-            load_A<T, N, CH, ZOH>(s, c * N + n0, A);
+            f2 invA[2], An[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
+            load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
             load4x(&s.invA[c * N + n0], invA);
-            const float Ds = s.Ds[c];
             load4x(&s.S[piece][c * N + n0], st);
             load4x(&s.R[piece][c * N + n0], carry);
             const float4 x4 = *reinterpret_cast<const float4 *>(&s.x[c][t0]);
@@ -618,109 +683,91 @@ __global__ void __launch_bounds__(kMainThreads, 2) scan_bwd_main(const BwdArgs a
                     accC[t][k] = f2_fma(dy, h, accC[t][k]);
                 }
             }
+            if (!ZOH) load4x(&s.A[c * N + n0], An);
             float vB[kPiece], vA[kPiece];
 #pragma unroll
             for (int k = 0; k < 2; ++k) dA[k] = dA2[k] = none;
-            auto back = [&](auto near_zero) {
 #pragma unroll
-                for (int t = kPiece - 1; t >= 0; --t) {
-                    const f2 x = f2_both(xs[t]), dt = f2_both(ds[t]), dy = f2_both(ys[t]),
-                             u = f2_both(xs[t] * ds[t]);
-                    f2 B[2], C[2], sB = none, sA = none;
-                    load4x(&s.B[t0 + t][n0], B);
-                    load4x(&s.C[t0 + t][n0], C);
+            for (int t = kPiece - 1; t >= 0; --t) {
+                const f2 dt = f2_both(ds[t]), dy = f2_both(ys[t]);
+                const f2 u = f2_both(ZOH ? xs[t] : xs[t] * ds[t]);
+                f2 B[2], C[2], sB = none, sA = none;
+                load4x(&s.B[t0 + t][n0], B);
+                load4x(&s.C[t0 + t][n0], C);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const f2 rv = f2_fma(dy, C[k], carry[k]);
-                        const f2 ra = times_decay<ZOH>(rv, F[t][k]);
-                        if (ZOH) {
-                            const f2 rw = f2_mul(rv, f2_mul(F[t][k], invA[k]));
-                            const f2 in = f2_mul(x, B[k]);
-                            const f2 rt = f2_mul(ra, f2_add(before[t][k], in));
-                            sB = f2_fma(rw, B[k], sB);
-                            accB[t][k] = f2_fma(rw, x, accB[t][k]);
-                            sA = f2_add(sA, rt);
-                            if constexpr (decltype(near_zero)::value) {
-                                // term by term: dt a r h + r x B dw/dA
-                                dA[k] = f2_fma(f2_mul(ra, dt), f2_mul(before[t][k], invA[k]), dA[k]);
-                                dA2[k] = f2_fma(f2_mul(rv, in), slope(ds[t], A[k].A, invA[k], F[t][k]),
-                                                dA2[k]);
-                            } else {
-                                dA[k] = f2_fma(dt, rt, dA[k]);
-                                dA2[k] = f2_fma(rw, in, dA2[k]);
-                            }
-                        } else {
-                            const f2 t1 = f2_mul(ra, before[t][k]);
-                            sB = f2_fma(rv, B[k], sB);
-                            accB[t][k] = f2_fma(rv, u, accB[t][k]);
-                            sA = f2_fma(A[k].A, t1, sA);
-                            dA[k] = f2_fma(dt, t1, dA[k]);
-                        }
-                        carry[k] = ra;
+                for (int k = 0; k < 2; ++k) {
+                    const f2 rv = f2_fma(dy, C[k], carry[k]);
+                    const f2 ra = times_decay<ZOH>(rv, F[t][k]);
+                    if (ZOH) {
+                        const f2 rw = f2_mul(rv, f2_mul(F[t][k], invA[k]));
+                        const f2 in = f2_mul(u, B[k]);
+                        const f2 rt = f2_mul(ra, f2_add(before[t][k], in));
+                        sB = k == 0 ? f2_mul(rw, B[k]) : f2_fma(rw, B[k], sB);
+                        accB[t][k] = f2_fma(rw, u, accB[t][k]);
+                        sA = k == 0 ? rt : f2_add(sA, rt);
+                        dA[k] = f2_fma(dt, rt, dA[k]);
+                        dA2[k] = f2_fma(rw, in, dA2[k]);
+                    } else {
+                        const f2 t1 = f2_mul(ra, before[t][k]);
+                        sB = k == 0 ? f2_mul(rv, B[k]) : f2_fma(rv, B[k], sB);
+                        accB[t][k] = f2_fma(rv, u, accB[t][k]);
+                        sA = k == 0 ? f2_mul(An[k], t1) : f2_fma(An[k], t1, sA);
+                        dA[k] = f2_fma(dt, t1, dA[k]);
                     }
-                    float lo, hi;
-                    f2_unpack(sB, lo, hi);
-                    vB[t] = lo + hi;
-                    f2_unpack(sA, lo, hi);
-                    vA[t] = lo + hi;
+                    carry[k] = ra;
                 }
-            };
-            if (ZOH && s.tiny) {
-                back(std::true_type{});
-#pragma unroll
-                for (int k = 0; k < 2; ++k) dA[k] = f2_add(dA[k], dA2[k]);
-            } else {
-                back(std::false_type{});
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (ZOH) dA[k] = f2_mul(invA[k], f2_sub(dA[k], dA2[k]));
+                float lo, hi;
+                f2_unpack(sB, lo, hi);
+                vB[t] = lo + hi;
+                f2_unpack(sA, lo, hi);
+                vA[t] = lo + hi;
             }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (ZOH) dA[k] = f2_mul(invA[k], f2_sub(dA[k], dA2[k]));
+            store4x(&s.P[piece][c * N + n0], dA);
             // dx and ddt: each lane of the channel ends with the sums of its share of the tokens
             share_sums<kLanes>(vB, vA, lane);
-            constexpr int kShare = kPiece / kLanes;
+            float db = 0.f, dd = 0.f;
+            const float Ds = s.Ds[c];
 #pragma unroll
             for (int j = 0; j < kShare; ++j) {
-                const int t = t0 + (lane % kLanes) * kShare + j;
-                const float sB = vB[j], sA = vA[j];
-                s.dx[c][t] = fmaf(Ds, s.dy[c][t], ZOH ? sB : sB * s.dt[c][t]);
-                s.fac[c][t] *= ZOH ? sA : fmaf(s.x[c][t], sB, sA);  // ddt
+                const float sB = vB[j], x = s.x[c][share0 + j], y = s.dy[c][share0 + j];
+                const float g = s.fac[c][share0 + j] * (ZOH ? vA[j] : fmaf(x, sB, vA[j]));
+                if (share0 + j < p.n && c < here) {
+                    dx[j * a.D] = fmaf(Ds, y, ZOH ? sB : sB * s.dt[c][share0 + j]);
+                    ddt[j * a.D] = g;
+                    db += g;
+                }
+                dd = fmaf(x, y, dd);
             }
-            store4x(&s.P[piece][c * N + n0], dA);
+            db = lanes_sum<kLanes>(db);
+            dd = lanes_sum<kLanes>(dd);
+            if (lane % kLanes == 0) {
+                s.db[piece][c] = db;
+                s.dd[piece][c] = dd;
+            }
         }
+        if (ZOH && s.tiny) near_zero_dA<T, N, CH, ALIGNED>(s, piece, lane);
         __syncthreads();
+        if (2 * tid < here * N) {
+            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int at = tid + i * kMainThreads;
-            if (at >= kState || d0 + at / N >= dend) break;
-            float v = 0.f;
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) v += s.P[j][at];
-            a.dA_part[(row + d0) * N + at] = v;
+            for (int j = 0; j < kPieces; ++j) {
+                const float2 q = *reinterpret_cast<const float2 *>(&s.P[j][2 * tid]);
+                v.x += q.x;
+                v.y += q.y;
+            }
+            *reinterpret_cast<float2 *>(&a.dA_part[(row + d0) * N + 2 * tid]) = v;
         }
-        for (int i = tid; i < kChunk * CH; i += kMainThreads) {
-            const int t = i / CH, c = i % CH;
-            if (t < p.n && d0 + c < dend) {
-                const int64_t off = (p.b * a.L + p.t0 + t) * a.D + d0 + c;
-                a.dx[off] = s.dx[c][t];
-                a.ddt[off] = s.fac[c][t];
-            }
-        }
-        // sums over the chunk's tokens: eight lanes a channel
-        static_assert(kMainThreads == 8 * CH, "lanes of a channel");
-        {
-            const int c = tid / 8, q = tid % 8;
-            float dd = 0.f, db = 0.f;
+        if (tid < here) {
+            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int t = q; t < kChunk; t += 8) {
-                dd = fmaf(s.x[c][t], s.dy[c][t], dd);
-                db += t < p.n ? s.fac[c][t] : 0.f;
+            for (int j = 0; j < kPieces; ++j) {
+                v.x += s.dd[j][tid];
+                v.y += s.db[j][tid];
             }
-            dd = lanes_sum<8>(dd);
-            db = lanes_sum<8>(db);
-            if (q == 0 && d0 + c < dend) {
-                a.d_part[(row + d0 + c) * 2] = dd;
-                a.d_part[(row + d0 + c) * 2 + 1] = db;
-            }
+            *reinterpret_cast<float2 *>(&a.d_part[(row + d0 + tid) * 2]) = v;
         }
     }
     // dB and dC of these channels: summed over the warp's channel lanes
@@ -740,8 +787,7 @@ __global__ void __launch_bounds__(kMainThreads, 2) scan_bwd_main(const BwdArgs a
             if (lane < kLanes && t0 + t < p.n) {
                 const int64_t at =
                     (((int64_t)p.part * a.batch + p.b) * a.L + p.t0 + t0 + t) * a.G + p.g;
-                a.bc_part[(at * N + n0 + k) * 2] = vb;
-                a.bc_part[(at * N + n0 + k) * 2 + 1] = vc;
+                *reinterpret_cast<float2 *>(&a.bc_part[(at * N + n0 + k) * 2]) = make_float2(vb, vc);
             }
         }
 }
@@ -831,34 +877,70 @@ Carved carve(const Problem &pr, const BwdArgs &a) {
     return c;
 }
 
+template <typename T, int N, bool ZOH, bool ALIGNED>
+cudaError_t launch_first(const BwdArgs &first, const Maps &maps, cudaStream_t st) {
+    constexpr auto *sums = scan_bwd_sums<T, N, ZOH, ALIGNED>;
+    const int smem = (int)sizeof(Tile<T, N, kCh, ALIGNED>);
+    const cudaError_t e =
+        cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    launch_begin("scan_bwd_sums", st);
+    sums<<<(unsigned)(first.batch * first.nc * first.G * first.blocks_per_group), kCh * N / kQ, smem,
+           st>>>(first, maps);
+    launch_end(st);
+    return cudaGetLastError();
+}
+template <typename T, int N, bool ZOH, bool ALIGNED>
+cudaError_t launch_main(const BwdArgs &a, const Maps &maps, cudaStream_t st) {
+    constexpr auto *main = scan_bwd_main<T, N, ZOH, ALIGNED>;
+    const int smem = (int)sizeof(MainTile<T, N, kCh, ALIGNED>);
+    const cudaError_t e =
+        cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    launch_begin("scan_bwd_main", st);
+    main<<<(unsigned)(a.batch * a.nc * a.G * a.blocks_per_group), kMainThreads, smem, st>>>(a, maps);
+    launch_end(st);
+    return cudaGetLastError();
+}
+
+// A map over a (b, L, D) tensor whose box is a tile of 32 channels by 32 tokens.
+// False where rows, or groups of channels, do not start on 16 bytes.
+template <typename T>
+bool tile_map(CUtensorMap *m, const void *base, const BwdArgs &a) {
+    const uint64_t row = (uint64_t)a.D * sizeof(T);
+    if (!tensor_map_encoder() || reinterpret_cast<uintptr_t>(base) % 16 != 0 || row % 16 != 0 ||
+        (a.G > 1 && a.gch * (int64_t)sizeof(T) % 16 != 0) || row * (uint64_t)a.L >= 1ull << 40)
+        return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1};
+    const cuuint64_t strides[3] = {row, row * (uint64_t)a.L, row * (uint64_t)a.L};
+    const cuuint32_t box[4] = {kCh, kChunk, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return tensor_map_encoder()(m,
+                                sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                4, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int N, bool ZOH>
 cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *dh_final,
                    float *dA, float *dD, float *ddt_bias, float *dh0, cudaStream_t st) {
-    cudaError_t e;
     BwdArgs first = a;
     split(pr, first, kCh, 8);
-    const unsigned grid = (unsigned)(a.batch * a.nc * a.G * a.blocks_per_group);
-    const unsigned first_grid = (unsigned)(a.batch * a.nc * a.G * first.blocks_per_group);
-    const int sums_smem = (int)sizeof(Tile<T, N, kCh>),
-              main_smem = (int)sizeof(MainTile<T, N, kCh>);
-    if ((e = cudaFuncSetAttribute(scan_bwd_sums<T, N, ZOH>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, sums_smem)) !=
-            cudaSuccess ||
-        (e = cudaFuncSetAttribute(scan_bwd_main<T, N, ZOH>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, main_smem)) !=
-            cudaSuccess)
-        return e;
-    launch_begin("scan_bwd_sums", st);
-    scan_bwd_sums<T, N, ZOH><<<first_grid, kCh * N / kQ, sums_smem, st>>>(first);
-    launch_end(st);
+    Maps maps;
+    const bool aligned = tile_map<T>(&maps.m[0], a.x, a) && tile_map<T>(&maps.m[1], a.dt, a) &&
+                         tile_map<T>(&maps.m[2], a.dy, a);
+    cudaError_t e = aligned ? launch_first<T, N, ZOH, true>(first, maps, st)
+                            : launch_first<T, N, ZOH, false>(first, maps, st);
+    if (e != cudaSuccess) return e;
     const int64_t lanes = a.batch * a.D * N;
     launch_begin("scan_bwd_chain", st);
     scan_bwd_chain<N, ZOH><<<dim3((unsigned)((lanes + 127) / 128), 2), 128, 0, st>>>(a, h0, dh_final,
                                                                                     dh0);
     launch_end(st);
-    launch_begin("scan_bwd_main", st);
-    scan_bwd_main<T, N, ZOH><<<grid, kMainThreads, main_smem, st>>>(a);
-    launch_end(st);
+    e = aligned ? launch_main<T, N, ZOH, true>(a, maps, st) : launch_main<T, N, ZOH, false>(a, maps, st);
+    if (e != cudaSuccess) return e;
     Sums q;
     q.rows = reinterpret_cast<const float2 *>(a.bc_part);
     q.dB = a.dB;
@@ -962,6 +1044,9 @@ ssd_status scan_backward_launch(const Problem &pr, const void *x, const void *dt
     a.nc = chunks(pr);
     a.words = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dt) |
                 reinterpret_cast<uintptr_t>(dy)) & 3) == 0;
+    a.err = device_error_word();
+    a.wait = wait_limit_cycles();
+    if (!a.err) return fail(SSD_ERR_CUDA, "cannot locate the device error word");
     a.step.pre = DtPreArgs{pre.bias, pre.softplus, pre.zoh, pre.dt_min, pre.dt_max};
     a.step.on = pre.bias || pre.softplus || pre.dt_max > 0.f;
     for (int k = 0; k < 2; ++k) a.step.lo[k] = a.step.hi[k] = 0.f;
