@@ -14,9 +14,10 @@
 //   g <- g + E (g + x B)   w = E / A   ddt = sum_n a r (g + x B)
 //   dA = (1/A) sum_t [dt a r (g + x B) - r w x B]
 //
-// (the last difference is taken term by term, from series, where |A| < 2^-5). Every state entry takes an exponential a token and about a dozen
-// fp32 operations, 16 or so times what a token's bytes need: the pass is bound
-// by the arithmetic, and by keeping sums over states (dx, ddt), over channels
+// (the last difference is taken term by term, from series, where |A| < 2^-5).
+// Every state entry takes an exponential a token and about a dozen fp32
+// operations, 16 or so times what a token's bytes need: the pass is bound by the
+// arithmetic, and by keeping sums over states (dx, ddt), over channels
 // (dB, dC) and over tokens (dA) all in registers.
 //
 // Time is cut into chunks of 32 tokens that run side by side:
@@ -107,9 +108,9 @@ __device__ __forceinline__ float prepare_step(float raw, float bias, const StepA
 
 // One pair of state entries at one step: F is exp(dt A) (Euler) or
 // E = exp(dt A) - 1 (hold). With y = dt A log2 e both start from exp2(y); the hold
-// takes E by its series in y where |y| < 3/8 (the sixth term, (y ln 2)^6 / 6!, ends
-// it: the next is below 7e-8 relative), else from exp2, whose error of 2^-22 is
-// then at most 1e-6 of it.
+// takes E by its series in y where |y| < 1/8 (the term (y ln 2)^4 / 4! ends it:
+// the next is below 5e-7 relative), else from exp2, whose error of 2^-22 is then
+// below 3e-6 of it.
 using tc::f2;
 using tc::f2_add;
 using tc::f2_fma;
@@ -129,16 +130,13 @@ struct Decay {
         const f2 e = f2_pack(tc::fast_exp2(y0), tc::fast_exp2(y1));
         if (!ZOH) return e;
         constexpr double k = 0.693147180559945309;  // ln 2
-        f2 p = f2_fma(f2_both((float)(k * k * k * k * k * k / 720)), y,
-                      f2_both((float)(k * k * k * k * k / 120)));
-        p = f2_fma(p, y, f2_both((float)(k * k * k * k / 24)));
-        p = f2_fma(p, y, f2_both((float)(k * k * k / 6)));
+        f2 p = f2_fma(f2_both((float)(k * k * k * k / 24)), y, f2_both((float)(k * k * k / 6)));
         p = f2_fma(p, y, f2_both((float)(k * k / 2)));
         p = f2_fma(p, y, f2_both((float)k));
         float s0, s1, e0, e1;
         f2_unpack(f2_mul(y, p), s0, s1);
         f2_unpack(f2_add(e, f2_both(-1.f)), e0, e1);
-        return f2_pack(fabsf(y0) < 0.375f ? s0 : e0, fabsf(y1) < 0.375f ? s1 : e1);
+        return f2_pack(fabsf(y0) < 0.125f ? s0 : e0, fabsf(y1) < 0.125f ? s1 : e1);
     }
 };
 
@@ -181,7 +179,7 @@ struct __align__(128) Tile {
     __align__(128) unsigned char words[3][kChunk][kPitch];
     float x[CH][kRow], dt[CH][kRow], dy[CH][kRow];
     float B[kChunk][N], C[kChunk][N];
-    float A[kState], Al[kState], invA[kState];
+    float A[kState], Al[kState], invA[kState];  // A, A log2 e, -1 / A (hold)
     float next_A[kState], next_bias[CH], next_Ds[CH];  // as they arrive
     uint64_t bar;
 };
@@ -309,10 +307,10 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
                         v[w][j] = to_f(reinterpret_cast<const T *>(s.words[w][t0 + j])[c]);
                     } else {
                         const T *row = static_cast<const T *>(src[w]) + base + (t0 + j) * a.D;
-                        if (words)
-                            row = reinterpret_cast<const T *>(
-                                &s.words[w][t0 + j][reinterpret_cast<uintptr_t>(row) & 3]);
-                        v[w][j] = to_f(row[c]);
+                        const uintptr_t in_word = reinterpret_cast<uintptr_t>(row) & 3;
+                        v[w][j] = words ? to_f(reinterpret_cast<const T *>(
+                                              &s.words[w][t0 + j][in_word])[c])
+                                        : to_f(row[c]);
                     }
                 }
                 v[1][j] = prepare_step<GRAD>(v[1][j], bias, a.step, f[j]);
@@ -330,7 +328,7 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
         tiny = tiny || fabsf(v) < 0x1p-5f;
         s.A[i] = v;
         s.Al[i] = v * kLog2eB;
-        if (ZOH) s.invA[i] = 1.f / v;
+        if (ZOH) s.invA[i] = -1.f / v;
     }
     return tiny;
 }
@@ -553,7 +551,7 @@ __device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int pi
     for (int c = lane / kLanes; c < CH; c += 32 / kLanes)
         for (int k = 0; k < kQ; ++k) {
             const int n = (lane % kLanes) * kQ + k, at = c * N + n;
-            const float A = s.A[at], invA = s.invA[at];
+            const float A = s.A[at], invA = -s.invA[at];
             float g[kPiece], E[kPiece], st = s.S[piece][at], carry = s.R[piece][at], dA = 0.f;
             for (int t = 0; t < kPiece; ++t) {
                 const int tok = piece * kPiece + t;
@@ -576,7 +574,7 @@ __device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int pi
                                                      : (fmaf(dt, E[t], dt) - E[t] * invA) * invA;
                 dA = fmaf(dt * carry, g[t] * invA, fmaf(r * in, slope, dA));
             }
-            s.P[piece][at] = dA;
+            s.P[piece][at] = -dA;
         }
 }
 
@@ -658,7 +656,10 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
 #pragma unroll 1
         for (int c = cl; c < CH; c += kPerWarp, dx += kPerWarp, ddt += kPerWarp) {
             Decay<ZOH> A[2];
-            f2 invA[2], An[2], st[2], carry[2], dA[2], dA2[2], F[kPiece][2], before[kPiece][2];
+            // the hold's 1 / A enters with its sign turned, so that dA's difference is a sum:
+            // accB, accC, sB and dA come out turned too
+            f2 invA[2], An[2], st[2], carry[2], dA[2], F[kPiece][2];
+            f2 before[kPiece][2];  // a token's state before it; with the hold g + x B
             load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
             load4x(&s.invA[c * N + n0], invA);
             load4x(&s.S[piece][c * N + n0], st);
@@ -677,16 +678,21 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     F[t][k] = A[k].at(dt);
-                    before[t][k] = st[k];
-                    st[k] = move<ZOH>(F[t][k], st[k], f2_mul(in, B[k]));
-                    const f2 h = ZOH ? f2_mul(st[k], invA[k]) : st[k];
-                    accC[t][k] = f2_fma(dy, h, accC[t][k]);
+                    if (ZOH) {
+                        before[t][k] = f2_fma(in, B[k], st[k]);
+                        st[k] = f2_fma(F[t][k], before[t][k], st[k]);
+                        accC[t][k] = f2_fma(dy, f2_mul(st[k], invA[k]), accC[t][k]);
+                    } else {
+                        before[t][k] = st[k];
+                        st[k] = f2_fma(F[t][k], st[k], f2_mul(in, B[k]));
+                        accC[t][k] = f2_fma(dy, st[k], accC[t][k]);
+                    }
                 }
             }
             if (!ZOH) load4x(&s.A[c * N + n0], An);
             float vB[kPiece], vA[kPiece];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) dA[k] = dA2[k] = none;
+            for (int k = 0; k < 2; ++k) dA[k] = none;
 #pragma unroll
             for (int t = kPiece - 1; t >= 0; --t) {
                 const f2 dt = f2_both(ds[t]), dy = f2_both(ys[t]);
@@ -700,13 +706,11 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                     const f2 ra = times_decay<ZOH>(rv, F[t][k]);
                     if (ZOH) {
                         const f2 rw = f2_mul(rv, f2_mul(F[t][k], invA[k]));
-                        const f2 in = f2_mul(u, B[k]);
-                        const f2 rt = f2_mul(ra, f2_add(before[t][k], in));
-                        sB = k == 0 ? f2_mul(rw, B[k]) : f2_fma(rw, B[k], sB);
+                        const f2 rt = f2_mul(ra, before[t][k]), rwB = f2_mul(rw, B[k]);
+                        sB = k == 0 ? rwB : f2_add(sB, rwB);
                         accB[t][k] = f2_fma(rw, u, accB[t][k]);
                         sA = k == 0 ? rt : f2_add(sA, rt);
-                        dA[k] = f2_fma(dt, rt, dA[k]);
-                        dA2[k] = f2_fma(rw, in, dA2[k]);
+                        dA[k] = f2_fma(dt, rt, f2_fma(u, rwB, dA[k]));
                     } else {
                         const f2 t1 = f2_mul(ra, before[t][k]);
                         sB = k == 0 ? f2_mul(rv, B[k]) : f2_fma(rv, B[k], sB);
@@ -724,7 +728,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                if (ZOH) dA[k] = f2_mul(invA[k], f2_sub(dA[k], dA2[k]));
+                if (ZOH) dA[k] = f2_mul(invA[k], dA[k]);
             store4x(&s.P[piece][c * N + n0], dA);
             // dx and ddt: each lane of the channel ends with the sums of its share of the tokens
             share_sums<kLanes>(vB, vA, lane);
@@ -735,7 +739,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                 const float sB = vB[j], x = s.x[c][share0 + j], y = s.dy[c][share0 + j];
                 const float g = s.fac[c][share0 + j] * (ZOH ? vA[j] : fmaf(x, sB, vA[j]));
                 if (share0 + j < p.n && c < here) {
-                    dx[j * a.D] = fmaf(Ds, y, ZOH ? sB : sB * s.dt[c][share0 + j]);
+                    dx[j * a.D] = fmaf(Ds, y, ZOH ? -sB : sB * s.dt[c][share0 + j]);
                     ddt[j * a.D] = g;
                     db += g;
                 }
@@ -758,6 +762,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                 v.x += q.x;
                 v.y += q.y;
             }
+            if (ZOH) v = make_float2(-v.x, -v.y);
             *reinterpret_cast<float2 *>(&a.dA_part[(row + d0) * N + 2 * tid]) = v;
         }
         if (tid < here) {
@@ -787,7 +792,8 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             if (lane < kLanes && t0 + t < p.n) {
                 const int64_t at =
                     (((int64_t)p.part * a.batch + p.b) * a.L + p.t0 + t0 + t) * a.G + p.g;
-                *reinterpret_cast<float2 *>(&a.bc_part[(at * N + n0 + k) * 2]) = make_float2(vb, vc);
+                *reinterpret_cast<float2 *>(&a.bc_part[(at * N + n0 + k) * 2]) =
+                    ZOH ? make_float2(-vb, -vc) : make_float2(vb, vc);
             }
         }
 }
