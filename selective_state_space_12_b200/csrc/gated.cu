@@ -88,12 +88,11 @@ __device__ __forceinline__ unsigned load_relaxed(const unsigned *p) {
 }
 
 struct __align__(16) Tile {
-    int64_t row0;  // offset of (b, first token, 0) in a (b, L, D) tensor
+    int64_t row0;     // offset of (b, first token, 0) in a (b, L, D) tensor
     int64_t flat;     // its first token's row in a (b L, D) tensor
     int64_t blocks0;  // and of (b, blk, 0) in a (b, nb, D) one
     int b, blk, d0, n;  // batch, block of tokens, first channel, tokens
-    unsigned id;   // its ticket, and the index of its record
-    bool last;     // of the tensor
+    unsigned id;      // its ticket, and the index of its record
 };
 template <bool BACK>
 __device__ __forceinline__ Tile tile_of(const GatedArgs &a, unsigned ticket) {
@@ -109,7 +108,6 @@ __device__ __forceinline__ Tile tile_of(const GatedArgs &a, unsigned ticket) {
     const int64_t left = a.L - (int64_t)t.blk * kBlock;
     t.n = (int)(left < kBlock ? left : kBlock);
     t.id = ticket;
-    t.last = t.b == a.batch - 1 && t.blk == a.nb - 1 && t.d0 + kTileCh >= a.D;
     return t;
 }
 
@@ -627,6 +625,8 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         bool ok = true;
         if (chained && !EAGER) {
             if (pos < kGroup - 1 && step + 1 < a.nb) {
+                // who has read the maps may write a.last, which may be a.first: our read is done
+                if (!waits) __threadfence();
                 store_word(&a.maps[(t.id * 32 + lane) * 2], all.x, all.y);
                 store_word(&a.maps[(t.id * 32 + lane) * 2 + 1], all.z, all.w);
             }

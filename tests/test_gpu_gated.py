@@ -11,6 +11,8 @@ signs (32 x 6e-8 = 2e-6); a factor of ten is left for the largest of many.
 (A share of the rms alone would not hold: a bf16 value of 14 rms is rounded by
 up to 14 x 2^-8 = 0.055 rms, and a token after a reset, where m = 1, has such
 gradients.)"""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -417,6 +419,39 @@ def test_repeats_to_the_bit_and_h_final_may_be_h0():
         g2 = ssd.ssd_gated_scan_backward(s["x"], s["r"], s["i"], s["lam"], st, s["dy"], s["dhf"])
         for k in g:
             assert torch.equal(g2[k], g[k]), k
+
+
+@pytest.mark.parametrize("batch,L,D", [(1, 40, 70), (1, 65, 128), (2, 500, 64), (1, 513, 200),
+                                       (1, 4000, 64), (40, 130, 1024)])
+def test_the_end_may_take_the_starts_place(batch, L, D):
+    """h_final in h0's memory and dh0 in dh_final's, with one block of tokens, one
+    group of blocks, several, and more lanes than thread blocks."""
+    import selective_state_space_12_b200 as ssd
+    from selective_state_space_12_b200 import _lib
+    from selective_state_space_12_b200.ssd import make_dims
+
+    s = make(batch, L, D, dtype=BF16, seed=92)
+    args = (s["x"], s["r"], s["i"], s["lam"])
+    y, hf, st = forward(s)
+    g = ssd.ssd_gated_scan_backward(*args, st, s["dy"], s["dhf"])
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    at = lambda t: t.data_ptr()
+    dims = ctypes.byref(make_dims(batch, L, D, 1, 1, 1, BF16))
+    need = lib.ssd_gated_scan_backward_workspace_size(dims)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        h = s["h0"].clone()
+        y2, _ = ssd.ssd_gated_scan(*args, h0=h, h_final=h)
+        assert torch.equal(y2, y) and torch.equal(h, hf)
+        d = s["dhf"].clone()
+        out = {k: torch.empty_like(g[k]) for k in ("dx", "dr", "di", "dlam")}
+        assert lib.ssd_gated_scan_backward(
+            *(at(t) for t in args[:3]), None, None, at(s["lam"]), C, None, at(st), at(s["dy"]),
+            at(d), at(out["dx"]), at(out["dr"]), at(out["di"]), at(out["dlam"]), at(d), dims,
+            at(ws), need, stream) == 0
+        assert torch.equal(d, g["dh0"])
+        for k in out:
+            assert torch.equal(out[k], g[k]), k
 
 
 def test_prefill_then_steps_and_a_split_sequence():

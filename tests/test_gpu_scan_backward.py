@@ -288,3 +288,64 @@ def test_unaligned_inputs_another_stream_graph_and_bits():
 def test_many_blocks_of_channels():
     """Wide enough that a CUDA block walks several tiles of channels."""
     check(make(2, 200, 5120, 16, dtype=BF16, h0=False, seed=31), softplus=True, zoh=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_layers_as_trained(dtype):
+    """A gated recurrence whose output a selective scan takes, forward and
+    backward, against autograd over both definitions in 64 bits; the first
+    layer's backward pass from its 8-bit copies too, against the same on the
+    values that they stand for. Each operator holds 2e-4, and what one hands on
+    the other passes with a gain of a few: 2e-3. In bf16 what is handed on is
+    rounded as well, each way, and some results: 16 half steps. The last
+    comparison is of one operator: 2e-4, and a half step where it rounds."""
+    import selective_state_space_12_b200 as ssd
+
+    b, L, D, N = 2, 150, 96, 8
+    half = 0.0 if dtype == F32 else torch.finfo(dtype).eps / 2
+    s = make(b, L, D, N, dtype=dtype, h0=False, seed=97)
+    g = np.random.default_rng(98)
+    put = lambda a, t: torch.from_numpy(a.astype(np.float32)).cuda().to(t)
+    r, i = (put(g.standard_normal((b, L, D)), dtype) for _ in range(2))
+    lam = put(np.log(np.expm1(-np.log(g.uniform(0.9, 0.99, D)) / 8)), F32)
+    options = dict(dt_bias=s["bias"], dt_softplus=True, zoh=True)
+
+    states = torch.empty((b, ssd.gated_blocks(L), D), device="cuda")
+    u, _ = ssd.ssd_gated_scan(s["x"], r, i, lam, states=states)
+    y, _ = ssd.ssd_selective_scan(u, s["dt"], s["A"], s["B"], s["C"], s["Dskip"], **options)
+    second = ssd.ssd_selective_scan_backward(u, s["dt"], s["A"], s["B"], s["C"], s["Dskip"], None,
+                                             s["dy"], **options)
+    du = second["dx"].to(dtype)
+    first = ssd.ssd_gated_scan_backward(s["x"], r, i, lam, states, du)
+    saved = ssd.GatedCheckpoint8(b, L, D)
+    u8, _ = ssd.ssd_gated_scan(s["x"], r, i, lam, checkpoint=saved)
+    from8 = ssd.ssd_gated_scan_backward_ckpt8(saved, lam, du)
+    assert ssd.ssd_device_status() == 0, ssd.ssd_last_error()
+    assert torch.equal(u8, u) and torch.equal(saved.states, states)
+
+    leaf = lambda v: v.detach().double().cpu().requires_grad_()
+    v = dict(x=leaf(s["x"]), r=leaf(r), i=leaf(i), lam=leaf(lam), dt=leaf(s["dt"]), A=leaf(s["A"]),
+             B=leaf(s["B"]), C=leaf(s["C"]), Dskip=leaf(s["Dskip"]), bias=leaf(s["bias"]))
+    soft = torch.nn.functional.softplus
+    a = torch.exp(-8 * soft(v["lam"]) * torch.sigmoid(v["r"]))
+    w = torch.sqrt(1 - a * a) * torch.sigmoid(v["i"]) * v["x"]
+    h, state, outs = torch.zeros(b, D).double(), torch.zeros(b, D, N).double(), []
+    step = soft(v["dt"] + v["bias"])[..., None]
+    for t in range(L):
+        h = a[:, t] * h + w[:, t]
+        decay = torch.exp(step[:, t] * v["A"])
+        state = decay * state + (decay - 1) / v["A"] * h[..., None] * v["B"][:, t]
+        outs.append((state * v["C"][:, t]).sum(-1) + v["Dskip"] * h)
+    want = torch.stack(outs, 1)
+    (want * s["dy"].double().cpu()).sum().backward()
+    tol = 2e-3 + 16 * half
+    assert off(y, f64(want)) <= tol
+    for k, got in (("x", first["dx"]), ("r", first["dr"]), ("i", first["di"]),
+                   ("lam", first["dlam"]), ("dt", second["ddt"]), ("A", second["dA"]),
+                   ("B", second["dB"]), ("C", second["dC"]), ("Dskip", second["dD"]),
+                   ("bias", second["ddt_bias"])):
+        assert off(got, f64(v[k].grad)) <= tol, k
+    values = saved.values()
+    want8 = ssd.ssd_gated_scan_backward(*(q.float() for q in values), lam, states, du.float())
+    for k in ("dx", "dr", "di", "dlam"):
+        assert off(from8[k], f64(want8[k])) <= TOL + (half if k != "dlam" else 0), k
