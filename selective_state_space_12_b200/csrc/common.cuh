@@ -108,6 +108,32 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A chain of kernels whose launches overlap: each but the first is started by
+// launch_after and begins with after_previous(), before which it touches nothing
+// that an earlier kernel writes and from which no thread may be exempt; one that
+// calls let_next() has the next one's thread blocks brought in as it ends.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... Q>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         const Q &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Sum of the rows first, first + step, ... of column d of a (rows, width) array
 // (0 past the last column), eight loads in flight.
 __device__ __forceinline__ float column_sum(const float *part, int64_t rows, int64_t width,

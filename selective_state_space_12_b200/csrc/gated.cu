@@ -55,6 +55,7 @@ constexpr int kCompute = 32 * kWarps;
 constexpr int kThreads = kCompute + 32;    // and the one that folds and looks back
 constexpr int kRun = kBlock / kWarps;  // tokens of a warp
 constexpr int kTileCh = 64;            // channels of a tile, two a lane
+constexpr int kStepThreads = 128;
 constexpr int kGroup = 8;              // consecutive tiles that fold each other's maps
 
 // Barriers of the compute warps and the chain warp.
@@ -701,6 +702,8 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
 // The first tickets of this thread block, and its barriers.
 template <bool ALIGNED, bool BACK, bool EAGER>
 __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsigned tiles) {
+    after_previous();
+    if (BACK) let_next();
     if (threadIdx.x == 0) {
         s.stop[0] = s.stop[1] = 0;
         // one block of tokens: a tile a thread block
@@ -1104,6 +1107,7 @@ __global__ void __launch_bounds__(1024)
 gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
                   float *__restrict__ dlam, int64_t rows, int64_t D) {
     __shared__ float red[32][33];
+    after_previous();
     const int64_t d = (int64_t)blockIdx.x * 32 + threadIdx.x;
     const float s = column_sum(part, rows, D, d, threadIdx.y, 32);
     red[threadIdx.y][threadIdx.x] = s;
@@ -1113,17 +1117,35 @@ gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
     if (threadIdx.x == 0 && mine < D) dlam[mine] = v * lam_ratio(lam[mine]);
 }
 
-template <typename T>
-__global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x,
-                                  const T *__restrict__ r, const T *__restrict__ i,
-                                  const float *__restrict__ lam, float c, T *__restrict__ y,
-                                  int64_t D, int64_t n) {
-    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (at >= n) return;
-    const Gate g = gate(to_f(r[at]), to_f(i[at]), c * softplus_full(lam[at % D]));
-    const float v = fmaf(g.a, h[at], g.m * g.si * to_f(x[at]));
-    h[at] = v;
-    y[at] = from_f<T>(v);
+// One token: V neighbouring channels a thread. A row of channels takes `row_blocks`
+// thread blocks.
+template <typename T, int V>
+__global__ void __launch_bounds__(kStepThreads)
+gated_step_kernel(float *__restrict__ h, const T *__restrict__ x, const T *__restrict__ r,
+                  const T *__restrict__ i, const float *__restrict__ lam, float c,
+                  T *__restrict__ y, int64_t D, unsigned row_blocks) {
+    const unsigned row = blockIdx.x / row_blocks;
+    const int64_t d = ((int64_t)(blockIdx.x - row * row_blocks) * kStepThreads + threadIdx.x) * V;
+    if (d >= D) return;
+    struct __align__(sizeof(T) * V) In {
+        T v[V];
+    };
+    struct __align__(4 * V) State {
+        float v[V];
+    };
+    const int64_t at = row * D + d;
+    const In xs = *reinterpret_cast<const In *>(x + at), rs = *reinterpret_cast<const In *>(r + at),
+             is = *reinterpret_cast<const In *>(i + at);
+    State hs = *reinterpret_cast<const State *>(h + at);
+    In ys;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const Gate g = gate(to_f(rs.v[j]), to_f(is.v[j]), c * softplus_full(lam[d + j]));
+        hs.v[j] = fmaf(g.a, hs.v[j], g.m * g.si * to_f(xs.v[j]));
+        ys.v[j] = from_f<T>(hs.v[j]);
+    }
+    *reinterpret_cast<State *>(h + at) = hs;
+    *reinterpret_cast<In *>(y + at) = ys;
 }
 
 // ------------------------------------------------------------ host
@@ -1131,6 +1153,7 @@ __global__ void gated_step_kernel(float *__restrict__ h, const T *__restrict__ x
 // Clears the words that tiles publish and the counter, and prepares the gate
 // scales k = c softplus(lam).
 __global__ void gated_open_kernel(const GatedArgs a, int64_t ends, int64_t maps) {
+    let_next();
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i == 0) *a.counter = *a.abort = 0;
     if (i < a.D) a.scale[i] = a.c * softplus_full(a.lam[i]);
@@ -1182,9 +1205,9 @@ cudaError_t start(const char *name, size_t smem, bool eager, const GatedArgs &a,
     gated_open_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, ends, words);
     launch_end(st);
     launch_begin(name, st);
-    K<<<(unsigned)grid, kThreads, smem, st>>>(a, maps);
+    e = launch_after(K, (unsigned)grid, kThreads, smem, st, a, maps);
     launch_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
@@ -1315,10 +1338,28 @@ cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     cudaError_t e = aligned ? backward_c<T, true>(a, maps, st) : backward_c<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);
-    gated_dlam_kernel<<<(unsigned)((a.D + 31) / 32), dim3(32, 32), 0, st>>>(
-        a.dlam_part, a.lam, dlam, a.batch * a.nb, a.D);
+    e = launch_after(gated_dlam_kernel, (unsigned)((a.D + 31) / 32), dim3(32, 32), 0, st,
+                     a.dlam_part, a.lam, dlam, a.batch * a.nb, a.D);
     launch_end(st);
-    return cudaGetLastError();
+    return e;
+}
+
+// Pairs of channels where rows allow them and there is work for every SM all the
+// same.
+template <typename T>
+void step_v(const Problem &pr, float *h, const void *x, const void *r, const void *i,
+            const float *lam, float c, void *y, cudaStream_t st) {
+    const int64_t D = pr.nheads;
+    const bool pairs = D % 2 == 0 && on(h, 8) && on(x, 2 * sizeof(T)) && on(r, 2 * sizeof(T)) &&
+                       on(i, 2 * sizeof(T)) && on(y, 2 * sizeof(T)) &&
+                       pr.batch * D >= 148 * 2 * kStepThreads;
+    const int64_t block = kStepThreads * (pairs ? 2 : 1);
+    const unsigned row_blocks = (unsigned)((D + block - 1) / block);
+    const unsigned grid = (unsigned)(pr.batch * row_blocks);
+    auto *kernel = pairs ? gated_step_kernel<T, 2> : gated_step_kernel<T, 1>;
+    kernel<<<grid, kStepThreads, 0, st>>>(h, static_cast<const T *>(x), static_cast<const T *>(r),
+                                          static_cast<const T *>(i), lam, c, static_cast<T *>(y), D,
+                                          row_blocks);
 }
 
 // The workspace: the tile counter and the abort word, the tiles' ends and
@@ -1416,17 +1457,11 @@ ssd_status gated_backward_launch(const Problem &pr, GatedArgs a, const float *dh
 
 ssd_status gated_step_launch(const Problem &pr, float *h, const void *x, const void *r,
                              const void *i, const float *lam, float c, void *y, cudaStream_t st) {
-    const int64_t n = pr.batch * pr.nheads;
-    const unsigned grid = (unsigned)((n + 127) / 128);
-    using bf = __nv_bfloat16;
     launch_begin("gated_step", st);
     if (pr.dtype == SSD_F32)
-        gated_step_kernel<float><<<grid, 128, 0, st>>>(h, (const float *)x, (const float *)r,
-                                                       (const float *)i, lam, c, (float *)y,
-                                                       pr.nheads, n);
+        step_v<float>(pr, h, x, r, i, lam, c, y, st);
     else
-        gated_step_kernel<bf><<<grid, 128, 0, st>>>(h, (const bf *)x, (const bf *)r, (const bf *)i,
-                                                    lam, c, (bf *)y, pr.nheads, n);
+        step_v<__nv_bfloat16>(pr, h, x, r, i, lam, c, y, st);
     launch_end(st);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SSD_OK : cuda_fail(e, "gated step launch");

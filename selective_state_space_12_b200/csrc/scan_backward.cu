@@ -463,6 +463,8 @@ scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
 template <int N, bool ZOH>
 __global__ void __launch_bounds__(128)
 scan_bwd_chain(const BwdArgs a, const float *h0, const float *dh_final, float *dh0) {
+    after_previous();
+    let_next();
     constexpr int kBatch = 8;
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t lane_len = a.D * N;
@@ -581,6 +583,8 @@ __device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int pi
 template <typename T, int N, bool ZOH, bool ALIGNED>
 __global__ void __launch_bounds__(kMainThreads, 2)
 scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
+    after_previous();
+    let_next();
     constexpr int CH = kCh, kLanes = N / kQ, kPerWarp = 32 / kLanes, kState = CH * N;
     constexpr int kShare = kPiece / kLanes;  // tokens of a piece whose dx and ddt a lane ends with
     extern __shared__ __align__(128) unsigned char raw[];
@@ -812,6 +816,7 @@ struct Sums {
     unsigned row_blocks, A_blocks;
 };
 __global__ void __launch_bounds__(512) scan_bwd_finish(const Sums q) {
+    after_previous();
     const int x = threadIdx.x, y = threadIdx.y, tid = y * 32 + x;
     if (blockIdx.x < q.row_blocks) {
         const int64_t i = (int64_t)blockIdx.x * 512 + tid;
@@ -904,9 +909,10 @@ cudaError_t launch_main(const BwdArgs &a, const Maps &maps, cudaStream_t st) {
         cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     launch_begin("scan_bwd_main", st);
-    main<<<(unsigned)(a.batch * a.nc * a.G * a.blocks_per_group), kMainThreads, smem, st>>>(a, maps);
+    const cudaError_t l = launch_after(
+        main, (unsigned)(a.batch * a.nc * a.G * a.blocks_per_group), kMainThreads, smem, st, a, maps);
     launch_end(st);
-    return cudaGetLastError();
+    return l;
 }
 
 // A map over a (b, L, D) tensor whose box is a tile of 32 channels by 32 tokens.
@@ -942,9 +948,10 @@ cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *d
     if (e != cudaSuccess) return e;
     const int64_t lanes = a.batch * a.D * N;
     launch_begin("scan_bwd_chain", st);
-    scan_bwd_chain<N, ZOH><<<dim3((unsigned)((lanes + 127) / 128), 2), 128, 0, st>>>(a, h0, dh_final,
-                                                                                    dh0);
+    e = launch_after(scan_bwd_chain<N, ZOH>, dim3((unsigned)((lanes + 127) / 128), 2), 128, 0, st, a,
+                     h0, dh_final, dh0);
     launch_end(st);
+    if (e != cudaSuccess) return e;
     e = aligned ? launch_main<T, N, ZOH, true>(a, maps, st) : launch_main<T, N, ZOH, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     Sums q;
@@ -964,10 +971,10 @@ cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *d
     q.row_blocks = (unsigned)((q.n + 511) / 512);
     q.A_blocks = (unsigned)((q.wide_A + 31) / 32);
     launch_begin("scan_bwd_finish", st);
-    scan_bwd_finish<<<q.row_blocks + q.A_blocks + (unsigned)((q.wide_d + 31) / 32), dim3(32, 16), 0,
-                      st>>>(q);
+    e = launch_after(scan_bwd_finish, q.row_blocks + q.A_blocks + (unsigned)((q.wide_d + 31) / 32),
+                     dim3(32, 16), 0, st, q);
     launch_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, int N>
