@@ -905,6 +905,13 @@ __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w
                    t.d0 + c1 < a.D ? __uint_as_float((uint32_t)e[c1] << 23) : 0.f);
 }
 
+// Bytes of shared memory in which sigmoid(i) waits for the gradients. Spilled registers
+// would wait in L2, which these kernels load most: at b8 L2048, D5121 380 us for 459
+// and from copies (D5120) 333 for 415; plain rows, where fewer registers are
+// spilled, take 284 us with it and 271 without.
+template <bool ALIGNED, bool CK>
+constexpr int kBackwardKeep = ALIGNED && !CK ? 0 : kRun * kCompute * 8;
+
 template <typename T, bool ALIGNED, bool CK, bool EAGER>
 __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
@@ -945,6 +952,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     f2 k = gate_scales<ALIGNED>(a, t.d0);
     const int tok0 = warp * kRun;
     const f2 none = f2_both(0.f), one = f2_both(1.f);
+    constexpr bool kKeep = kBackwardKeep<ALIGNED, CK> > 0;
+    f2 *const kept = reinterpret_cast<f2 *>(staged + In::kBytes + (CK ? Copies::kBytes : 0)) +
+                     warp * kRun * 32 + lane;
     const bool chained = a.nb > 1;
     constexpr bool kAhead = In::kAhead;
     bool ahead = false;
@@ -952,10 +962,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
         const bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
-        // kept until the gradients: dy, x (as stored) and the two sigmoids
+        // kept until the gradients: dy, x (as stored) and the two sigmoids, some in shared memory
         std::conditional_t<CK, uint16_t, P2> xr[kRun];
         P2 dyr[kRun];
         f2 sr[kRun], si[kRun];
+        auto sigmoid_i = [&](int j) -> f2 & { return kKeep ? kept[j * 32] : si[j]; };
         bool here = in.wait(a.wait);
         if constexpr (CK) here = copies.wait(a.wait) && here;
         if (!here) give_up(a, &s.stop[n & 1]);
@@ -979,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 }
                 const Gate2 g = gate2<kPlain>(rv, iv, k);
                 sr[j] = g.sr;
-                si[j] = g.si;
+                sigmoid_i(j) = g.si;
                 const f2 vx = f2_mul(g.si, x);
                 if (kPlain || (j < left && !(marks >> j & 1))) {
                     H = j == 0 ? f2_mul(g.m, vx) : f2_fma(g.a, H, f2_mul(g.m, vx));
@@ -1057,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 Gate2 g;
                 decay_from2(F[j], g);
                 const f2 x = CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]);
-                const f2 srj = sr[j], sij = si[j];
+                const f2 srj = sr[j], sij = sigmoid_i(j);
                 const f2 vx = f2_mul(sij, x);  // sigmoid(i) x
                 const f2 gm = cut ? G[j] : f2_mul(G[j], g.m);
                 // q dm/dq = q a^2 / m: finite where q -> 0
@@ -1307,7 +1318,8 @@ cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
 template <typename T, bool ALIGNED, bool CK>
 cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     constexpr size_t smem =
-        Stage<T, ALIGNED, CK ? 1 : 4>::kBytes + (CK ? Stage<int8_t, ALIGNED, 3>::kBytes : 0);
+        Stage<T, ALIGNED, CK ? 1 : 4>::kBytes + (CK ? Stage<int8_t, ALIGNED, 3>::kBytes : 0) +
+        kBackwardKeep<ALIGNED, CK>;
     constexpr auto *many = gated_backward_kernel<T, ALIGNED, CK, true>;
     constexpr auto *few = gated_backward_kernel<T, ALIGNED, CK, false>;
     cudaError_t e = cudaSuccess;
