@@ -21,13 +21,11 @@
 // number of lanes (batch times tiles of channels), each with one fixed order of
 // sums:
 //
-//  - many lanes (at least one for each thread block): a tile waits for what
-//    leaves the tile before, which was handed out a whole round earlier and is
-//    hardly ever late. Thread blocks hold a ticket ahead, so that the next
-//    tile's inputs arrive meanwhile.
+//  - many lanes (one for every other SM or more): a tile waits for what leaves the
+//    tile before, which was handed out a round of the lanes earlier. Thread blocks
+//    hold a ticket ahead, so that the next tile's inputs arrive meanwhile.
 //  - few lanes: thread blocks work on many consecutive tiles of a lane at once,
-//    and a chain of waits from tile to tile would be the whole time (0.4 us a
-//    step). Tiles form groups of kGroup; each publishes its (P, H), folds those
+//    and a chain of waits from tile to tile would be the whole time (1 us a step). Tiles form groups of kGroup; each publishes its (P, H), folds those
 //    before it in its group, and waits only for what leaves the group before,
 //    so the chain has one step a group. A ticket held ahead could then block
 //    the chain behind its holder's wait, so none is: the inputs that the next
@@ -1272,12 +1270,18 @@ void make_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &
     }
 }
 
-// Many lanes or few (see the top): whether every thread block of the kernel
-// that holds tickets ahead has a lane of its own.
-template <auto K>
-bool many_lanes(const GatedArgs &a, size_t smem, cudaError_t *e) {
-    const int64_t fit = resident_blocks<K>(smem, e);
-    return *e == cudaSuccess && a.nb > 1 && a.batch * a.dblocks >= fit;
+// Many lanes or few (see the top). A step of the waiting chain takes 0.9 us (forward)
+// to 1.5 us (backward from copies), in which a GPU full of thread blocks gets through
+// 64 to 90 tiles the other way: lanes for half the SMs pay. Both ways at one row of
+// 16384 tokens, bf16: 80 lanes 212 against 232 us (backward 312 against 346), 128
+// lanes 263 against 330; at b4 L4096 and 64 lanes 59 against 56; at b1 L65536 and 32
+// lanes 1314 against 375.
+bool many_lanes(const GatedArgs &a, cudaError_t *e) {
+    int dev = 0, sms = 0;
+    if ((*e = cudaGetDevice(&dev)) != cudaSuccess ||
+        (*e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return false;
+    return a.nb > 1 && 2 * a.batch * a.dblocks >= sms;
 }
 
 template <typename T, bool ALIGNED, bool CK>
@@ -1287,7 +1291,7 @@ cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     constexpr auto *many = gated_forward_kernel<T, ALIGNED, CK, true>;
     constexpr auto *few = gated_forward_kernel<T, ALIGNED, CK, false>;
     cudaError_t e = cudaSuccess;
-    const bool eager = many_lanes<many>(a, ahead, &e);
+    const bool eager = many_lanes(a, &e);
     if (e != cudaSuccess) return e;
     return eager ? start<many>("gated_forward", ahead, true, a, maps, st)
                  : start<few>("gated_forward", kept, false, a, maps, st);
@@ -1323,7 +1327,7 @@ cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     constexpr auto *many = gated_backward_kernel<T, ALIGNED, CK, true>;
     constexpr auto *few = gated_backward_kernel<T, ALIGNED, CK, false>;
     cudaError_t e = cudaSuccess;
-    const bool eager = many_lanes<many>(a, smem, &e);
+    const bool eager = many_lanes(a, &e);
     if (e != cudaSuccess) return e;
     return eager ? start<many>("gated_backward", smem, true, a, maps, st)
                  : start<few>("gated_backward", smem, false, a, maps, st);

@@ -421,6 +421,28 @@ def test_repeats_to_the_bit_and_h_final_may_be_h0():
             assert torch.equal(g2[k], g[k]), k
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("batch,L,D", [(4, 1100, 1024), (5, 1100, 1030), (2, 700, 2600)])
+def test_as_many_lanes_as_half_the_sms(batch, L, D, dtype):
+    """Lanes (of 64 channels) just below and above half the SMs, fewer than thread
+    blocks: the chain of waits is as long as the sequence."""
+    import selective_state_space_12_b200 as ssd
+
+    s = make(batch, L, D, dtype=dtype, reset=True, seed=93)
+    y, hf, st = forward(s)
+    g = ssd.ssd_gated_scan_backward(s["x"], s["r"], s["i"], s["lam"], st, s["dy"], s["dhf"],
+                                    reset=s["reset"])
+    saved = ssd.GatedCheckpoint8(batch, L, D)
+    y8, _ = ssd.ssd_gated_scan(s["x"], s["r"], s["i"], s["lam"], reset=s["reset"], h0=s["h0"],
+                               checkpoint=saved)
+    assert ssd.ssd_device_status() == 0, ssd.ssd_last_error()
+    assert torch.equal(y8, y)
+    ref, grads = reference(s["x"], s["r"], s["i"], s["lam"], s["reset"], s["h0"], s["dy"], s["dhf"])
+    assert off(y, ref) <= TOL and off(hf, ref[:, -1]) <= TOL
+    for k in grads:
+        assert off(g[k], grads[k]) <= TOL, k
+
+
 @pytest.mark.parametrize("batch,L,D", [(1, 40, 70), (1, 65, 128), (2, 500, 64), (1, 513, 200),
                                        (1, 4000, 64), (40, 130, 1024)])
 def test_the_end_may_take_the_starts_place(batch, L, D):
