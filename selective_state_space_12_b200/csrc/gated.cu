@@ -1126,15 +1126,16 @@ gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
     if (threadIdx.x == 0 && mine < D) dlam[mine] = v * lam_ratio(lam[mine]);
 }
 
-// One token: V neighbouring channels a thread. A row of channels takes `row_blocks`
-// thread blocks.
+// One token: V neighbouring channels a thread, of `rows` batch rows after one
+// another (the scale c softplus(lam) once for all of them). A row of channels takes
+// `row_blocks` thread blocks.
 template <typename T, int V>
 __global__ void __launch_bounds__(kStepThreads)
 gated_step_kernel(float *__restrict__ h, const T *__restrict__ x, const T *__restrict__ r,
                   const T *__restrict__ i, const float *__restrict__ lam, float c,
-                  T *__restrict__ y, int64_t D, unsigned row_blocks) {
-    const unsigned row = blockIdx.x / row_blocks;
-    const int64_t d = ((int64_t)(blockIdx.x - row * row_blocks) * kStepThreads + threadIdx.x) * V;
+                  T *__restrict__ y, int64_t D, int64_t batch, int rows, unsigned row_blocks) {
+    const unsigned part = blockIdx.x / row_blocks;
+    const int64_t d = ((int64_t)(blockIdx.x - part * row_blocks) * kStepThreads + threadIdx.x) * V;
     if (d >= D) return;
     struct __align__(sizeof(T) * V) In {
         T v[V];
@@ -1142,19 +1143,26 @@ gated_step_kernel(float *__restrict__ h, const T *__restrict__ x, const T *__res
     struct __align__(4 * V) State {
         float v[V];
     };
-    const int64_t at = row * D + d;
-    const In xs = *reinterpret_cast<const In *>(x + at), rs = *reinterpret_cast<const In *>(r + at),
-             is = *reinterpret_cast<const In *>(i + at);
-    State hs = *reinterpret_cast<const State *>(h + at);
-    In ys;
+    float k[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const Gate g = gate(to_f(rs.v[j]), to_f(is.v[j]), c * softplus_full(lam[d + j]));
-        hs.v[j] = fmaf(g.a, hs.v[j], g.m * g.si * to_f(xs.v[j]));
-        ys.v[j] = from_f<T>(hs.v[j]);
+    for (int j = 0; j < V; ++j) k[j] = c * softplus_full(lam[d + j]);
+    const int64_t first = (int64_t)part * rows;
+    const int64_t end = first + rows < batch ? first + rows : batch;
+#pragma unroll 2
+    for (int64_t at = first * D + d; at < end * D; at += D) {
+        const In xs = *reinterpret_cast<const In *>(x + at), rs = *reinterpret_cast<const In *>(r + at),
+                 is = *reinterpret_cast<const In *>(i + at);
+        State hs = *reinterpret_cast<const State *>(h + at);
+        In ys;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const Gate g = gate(to_f(rs.v[j]), to_f(is.v[j]), k[j]);
+            hs.v[j] = fmaf(g.a, hs.v[j], g.m * g.si * to_f(xs.v[j]));
+            ys.v[j] = from_f<T>(hs.v[j]);
+        }
+        *reinterpret_cast<State *>(h + at) = hs;
+        *reinterpret_cast<In *>(y + at) = ys;
     }
-    *reinterpret_cast<State *>(h + at) = hs;
-    *reinterpret_cast<In *>(y + at) = ys;
 }
 
 // ------------------------------------------------------------ host
@@ -1370,12 +1378,14 @@ void step_v(const Problem &pr, float *h, const void *x, const void *r, const voi
                        on(i, 2 * sizeof(T)) && on(y, 2 * sizeof(T)) &&
                        pr.batch * D >= 148 * 2 * kStepThreads;
     const int64_t block = kStepThreads * (pairs ? 2 : 1);
-    const unsigned row_blocks = (unsigned)((D + block - 1) / block);
-    const unsigned grid = (unsigned)(pr.batch * row_blocks);
+    const int64_t row_blocks = (D + block - 1) / block;
+    const int64_t fill = pr.batch * row_blocks / (148 * 8);  // eight thread blocks an SM all the same
+    const int64_t rows = fill < 1 ? 1 : fill < 8 ? fill : 8;
+    const unsigned grid = (unsigned)((pr.batch + rows - 1) / rows * row_blocks);
     auto *kernel = pairs ? gated_step_kernel<T, 2> : gated_step_kernel<T, 1>;
     kernel<<<grid, kStepThreads, 0, st>>>(h, static_cast<const T *>(x), static_cast<const T *>(r),
                                           static_cast<const T *>(i), lam, c, static_cast<T *>(y), D,
-                                          row_blocks);
+                                          pr.batch, (int)rows, (unsigned)row_blocks);
 }
 
 // The workspace: the tile counter and the abort word, the tiles' ends and

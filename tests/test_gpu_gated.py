@@ -263,7 +263,8 @@ def test_checkpoint_of_infinities_reads_as_nan():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("shape", [(1, 1), (1, 2560), (3, 1001), (256, 130)])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 2560), (3, 1001), (256, 130), (301, 2602),
+                                   (301, 2601)])
 def test_step(shape, dtype):
     import selective_state_space_12_b200 as ssd
 
