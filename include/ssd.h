@@ -325,8 +325,9 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A,
  *   workspace, workspace_bytes as for ssd_forward, sized by
  *            ssd_selective_scan_backward_workspace_size
  *
- * Tensors need the alignment of their element type; no output may alias an
- * input, but for dh0 and dh_final. Sums over tokens, batch and channels are
+ * Tensors need the alignment of their element type; 16-byte alignment and rows
+ * of 16 bytes' multiples are faster. No output may alias an input, but for dh0
+ * and dh_final. Sums over tokens, batch and channels are
  * fp32, in an order that does not change between calls. seqlen 0 gives zeros,
  * and dh0 = dh_final.
  */
@@ -377,9 +378,10 @@ ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const floa
  *   workspace, workspace_bytes as for ssd_forward, sized by
  *             ssd_gated_scan_workspace_size
  *
- * Tensors need the alignment of their element type; 16-byte alignment and an
- * even D (fp32) or D a multiple of 2 (bf16) are faster. Outputs may not alias
- * inputs, but for h_final and h0. seqlen 0 copies h0 to h_final.
+ * Tensors need the alignment of their element type; 16-byte alignment and rows
+ * of 16 bytes' multiples (D a multiple of 8 in bf16, of 4 in fp32, of 16 with
+ * 8-bit copies) are faster. Outputs may not alias inputs, but for h_final and
+ * h0. A workspace serves one call at a time. seqlen 0 copies h0 to h_final.
  */
 #define SSD_GATED_BLOCK 64
 
@@ -478,7 +480,8 @@ const char *ssd_last_error(void);
  * work; every such wait is bounded, and a wait that runs out makes the kernel
  * stop its own work, let its copies and tensor-core operations in flight
  * finish, free its tensor memory, store nothing, and report SSD_ERR_TIMEOUT
- * through ssd_device_status. `cycles` is that bound in SM clock cycles for
+ * through ssd_device_status. The waits of the gated scan's kernels and of the
+ * selective scan's backward pass are bounded in the same way. `cycles` is that bound in SM clock cycles for
  * kernels launched after the call, process-wide; 0 (or a negative value)
  * restores the default of about 2 s. A bound of a few cycles makes the next
  * forward or backward give up at its first wait that is not already

@@ -31,6 +31,14 @@
 //    the chain behind its holder's wait, so none is: the inputs that the next
 //    round of tiles needs are brought to L2 instead.
 //
+// What bounds it: bytes (8 forward and 14 backward a token and channel in bf16, 0.67
+// and 1.17 GB at b8 L2048 D5120) and, nearly as much, issue: about 100 instructions a
+// pair of channels forward and 140 backward, at 45 to 60 % of the issue slots with 18
+// to 36 warps an SM. Measured there, B200, bf16: forward 140 us (4.8 TB/s), backward
+// 271 us (4.3 TB/s), forward with 8-bit copies 244 us and
+// backward from them 332 us. One row of 65536 tokens by 2048 channels, few lanes:
+// 375 and 577 us. Rows that start anywhere (D5121): 181 and 379 us.
+//
 // A published word is 64 bits, cleared to all ones before the kernel, and is
 // complete once it differs from that: readers poll the data itself, and no
 // fence stands between data and flag. Waits are bounded; one that runs out
@@ -546,7 +554,7 @@ struct Largest<__nv_bfloat16> {
 };
 
 // Two values as int8 steps, in the low bytes: adding 1.5 2^23 rounds to the
-// nearest step, ties to even, and leaves it in the low byte.
+// nearest step, ties to even, and leaves it in the low byte (the copy's one rounding).
 __device__ __forceinline__ uint32_t in_steps(f2 v, f2 inv, uint32_t keep) {
     float lo, hi;
     f2_unpack(f2_fma(v, inv, f2_both(12582912.f)), lo, hi);
@@ -717,19 +725,24 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
 }
 
 // The plain case of a warp's eight tokens (all there, with all the tile's
-// channels, no reset, slow decays) is
-// straight code; every other case runs a general copy with a branch a token.
+// channels, no reset, slow decays) is straight code; every other case runs a
+// general copy with a branch a token.
 struct PlainRun : std::true_type {};
 struct AnyRun : std::false_type {};
 
 // ------------------------------------------------------------ forward
 
-// Bytes that a warp keeps in its rows' place while it waits: a and u.
+// Bytes that a warp keeps in its rows' place while it waits: a and u. Few lanes wait
+// longest, and need no room for rows ahead: four thread blocks an SM fit for three (b1
+// L65536 D2048 373 us for 388).
 template <bool ALIGNED, bool CK, bool EAGER>
 constexpr int kForwardKeep = ALIGNED && !EAGER && !CK ? 2 * kRun * 32 * 8 : 0;
 
+// x, r, i (and with CK their 8-bit copies, from the values as stored) to y, the end
+// state and the states that enter the blocks.
 template <typename T, bool ALIGNED, bool CK, bool EAGER>
-__global__ void __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) gated_forward_kernel(
+__global__ void
+__launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) gated_forward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(128) unsigned char staged[];
     __shared__ Shared s;
@@ -910,6 +923,10 @@ __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w
 template <bool ALIGNED, bool CK>
 constexpr int kBackwardKeep = ALIGNED && !CK ? 0 : kRun * kCompute * 8;
 
+// dy, r, i, x (CK: the copies) and the blocks' states to dx, dr, di, dh0 and each
+// block's sums of dlam. The gates are computed once: two sigmoids, dy and x stay in
+// registers between the maps and the gradients (96 registers, two thread blocks an
+// SM; three, with all of it in shared memory, was slower).
 template <typename T, bool ALIGNED, bool CK, bool EAGER>
 __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     const GatedArgs a, const __grid_constant__ Maps maps) {
@@ -1111,7 +1128,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
     }
 }
 
-// dlam: the blocks' sums over batch and blocks, times the channel's factor.
+// dlam: the blocks' sums over batch and blocks, times the channel's factor. 1/64 of a
+// tensor's fp32 bytes; about 5 us at b8 L2048 D5120, most of it latency.
 __global__ void __launch_bounds__(1024)
 gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
                   float *__restrict__ dlam, int64_t rows, int64_t D) {
@@ -1126,7 +1144,9 @@ gated_dlam_kernel(const float *__restrict__ part, const float *__restrict__ lam,
     if (threadIdx.x == 0 && mine < D) dlam[mine] = v * lam_ratio(lam[mine]);
 }
 
-// One token: V neighbouring channels a thread, of `rows` batch rows after one
+// One token. Bytes: 16 a channel in bf16 (5 us at b256 D8192, measured 8.3; a state
+// that the last step left in L2 comes from there); at one row the launch is all of it.
+// V neighbouring channels a thread, of `rows` batch rows after one
 // another (the scale c softplus(lam) once for all of them). A row of channels takes
 // `row_blocks` thread blocks.
 template <typename T, int V>
@@ -1168,7 +1188,8 @@ gated_step_kernel(float *__restrict__ h, const T *__restrict__ x, const T *__res
 // ------------------------------------------------------------ host
 
 // Clears the words that tiles publish and the counter, and prepares the gate
-// scales k = c softplus(lam).
+// scales k = c softplus(lam). 1/32 of a bf16 tensor's bytes; about 2 us, partly
+// behind the launch of the kernel that follows.
 __global__ void gated_open_kernel(const GatedArgs a, int64_t ends, int64_t maps) {
     let_next();
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -1369,7 +1390,8 @@ cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
 }
 
 // Pairs of channels where rows allow them and there is work for every SM all the
-// same.
+// same (b256 D8192: 10.3 us for 12.3), and up to eight rows a thread while eight
+// thread blocks an SM are left (8.3 us).
 template <typename T>
 void step_v(const Problem &pr, float *h, const void *x, const void *r, const void *i,
             const float *lam, float c, void *y, cudaStream_t st) {
@@ -1379,7 +1401,7 @@ void step_v(const Problem &pr, float *h, const void *x, const void *r, const voi
                        pr.batch * D >= 148 * 2 * kStepThreads;
     const int64_t block = kStepThreads * (pairs ? 2 : 1);
     const int64_t row_blocks = (D + block - 1) / block;
-    const int64_t fill = pr.batch * row_blocks / (148 * 8);  // eight thread blocks an SM all the same
+    const int64_t fill = pr.batch * row_blocks / (148 * 8);
     const int64_t rows = fill < 1 ? 1 : fill < 8 ? fill : 8;
     const unsigned grid = (unsigned)((pr.batch + rows - 1) / rows * row_blocks);
     auto *kernel = pairs ? gated_step_kernel<T, 2> : gated_step_kernel<T, 1>;

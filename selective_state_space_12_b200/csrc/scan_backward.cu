@@ -31,6 +31,13 @@
 //   4. scan_bwd_finish: sums of dB and dC over blocks of channels, and of dA, dDskip
 //      and the bias's gradient over batch and chunks. No atomics: every sum has
 //      one order.
+//
+// Measured, B200, bf16, b8 L2048 D5120 N16 with softplus: hold 3730 us (0.36 T state
+// entries a second), of which the sums take 782 us, the chain 167, the main kernel
+// 2730 and the last sums 53; Euler 2860 us (614, 165, 2030, 53). The main kernel
+// issues about 80 instructions for each pair of entries and token in 52 % of its
+// issue slots: 16 warps an SM at 128 registers a thread, whose latencies (exp2,
+// shared memory, the packed arithmetic) they do not quite hide.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -411,6 +418,8 @@ __device__ __forceinline__ void load_A(const Tile<T, N, CH, ALIGNED> &s, int at,
     A[1].Al = l[1];
 }
 
+// A thread walks a chunk's 32 tokens for four states of a channel; one exponential and
+// five packed operations a pair of entries.
 template <typename T, int N, bool ZOH, bool ALIGNED>
 __global__ void __launch_bounds__(kCh *N / kQ, 640 / (kCh * N / kQ))
 scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
@@ -458,7 +467,8 @@ scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
     }
 }
 
-// The chains over chunks: blockIdx.y 0 the states (with the hold g = A h), 1
+// The chains over chunks, bound by their bytes (read and written: 671 MB of S and R at
+// b8 L2048 D5120 N16, 167 us, 4 TB/s): blockIdx.y 0 the states (with the hold g = A h), 1
 // the gradients. Eight chunks' words are loaded at a time.
 template <int N, bool ZOH>
 __global__ void __launch_bounds__(128)
@@ -580,6 +590,12 @@ __device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int pi
         }
 }
 
+// A warp has a piece of four tokens, a lane four states of one channel at a time: sums
+// over channels (dB, dC) stay in the lane over all its channels, sums over states (dx,
+// ddt) are shared out over a channel's lanes, sums over tokens (dA) are the lane's own.
+// Four tokens are what two thread blocks an SM have registers for: the exponentials
+// and states of a piece are computed again rather than kept (kept in shared memory,
+// with half the channels a tile, was slower).
 template <typename T, int N, bool ZOH, bool ALIGNED>
 __global__ void __launch_bounds__(kMainThreads, 2)
 scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
