@@ -869,18 +869,25 @@ __global__ void __launch_bounds__(512) scan_bwd_finish(const Sums q) {
 
 int64_t chunks(const Problem &pr) { return (pr.seqlen + kChunk - 1) / kChunk; }
 
-// Tiles of `ch` channels that one CUDA block walks: as many as leave four
-// blocks for each SM, up to `most` (fewer sums of dB and dC, inputs a tile ahead).
-void split(const Problem &pr, BwdArgs &a, int ch, int most) {
+// Tiles of channels that one thread block walks, up to eight (fewer sums of dB and dC,
+// inputs a tile ahead): those that take the fewest rounds of `resident` thread blocks,
+// each as long as its tiles and half a tile to begin and end.
+void split(const Problem &pr, BwdArgs &a, int resident) {
     a.gch = pr.nheads / pr.ngroups;
-    a.tiles_per_group = (int)((a.gch + ch - 1) / ch);
+    a.tiles_per_group = (int)((a.gch + kCh - 1) / kCh);
     const int64_t rows = pr.batch * chunks(pr) * pr.ngroups;
-    int k = most;
-    while (k > 1 && rows * ((a.tiles_per_group + k - 1) / k) < 4 * 148) --k;
-    a.tiles_per_block = k;
-    a.blocks_per_group = (a.tiles_per_group + k - 1) / k;
+    int64_t least = INT64_MAX;
+    for (int k = 8; k >= 1; --k) {
+        const int64_t blocks = (a.tiles_per_group + k - 1) / k;
+        const int64_t cost = (rows * blocks + resident - 1) / resident * (2 * k + 1);
+        if (cost >= least) continue;
+        least = cost;
+        a.tiles_per_block = k;
+        a.blocks_per_group = (int)blocks;
+    }
 }
-void split_main(const Problem &pr, BwdArgs &a) { split(pr, a, kCh, 8); }
+constexpr int kSms = 148;
+void split_main(const Problem &pr, BwdArgs &a) { split(pr, a, 2 * kSms); }
 
 struct Carved {
     size_t S, R, steps, bc, dA, d, total;
@@ -955,7 +962,7 @@ template <typename T, int N, bool ZOH>
 cudaError_t launch(const Problem &pr, BwdArgs a, const float *h0, const float *dh_final,
                    float *dA, float *dD, float *ddt_bias, float *dh0, cudaStream_t st) {
     BwdArgs first = a;
-    split(pr, first, kCh, 8);
+    split(pr, first, kSms * (640 / (kCh * N / kQ)));
     Maps maps;
     const bool aligned = tile_map<T>(&maps.m[0], a.x, a) && tile_map<T>(&maps.m[1], a.dt, a) &&
                          tile_map<T>(&maps.m[2], a.dy, a);
