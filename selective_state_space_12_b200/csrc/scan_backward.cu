@@ -35,7 +35,7 @@
 // Measured, B200, bf16, b8 L2048 D5120 N16 with softplus: hold 3730 us (0.36 T state
 // entries a second), of which the sums take 782 us, the chain 167, the main kernel
 // 2730 and the last sums 53; Euler 2860 us (614, 165, 2030, 53). The main kernel
-// issues about 80 instructions for each pair of entries and token in 52 % of its
+// issues about 85 instructions for each pair of entries and token in 55 % of its
 // issue slots: 16 warps an SM at 128 registers a thread, whose latencies (exp2,
 // shared memory, the packed arithmetic) they do not quite hide.
 #include <cudaTypedefs.h>
