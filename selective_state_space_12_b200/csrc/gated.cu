@@ -1268,7 +1268,8 @@ bool encode(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4],
 template <typename T>
 bool warp_map(CUtensorMap *m, const void *base, const GatedArgs &a) {
     const uint64_t row = (uint64_t)a.D * sizeof(T);
-    if (!tensor_map_encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40) return false;
+    if (!tensor_map_encoder() || !on(base, 16) || row % 16 != 0 || row * (uint64_t)a.L >= 1ull << 40)
+        return false;
     return encode<T>(m, base, {(cuuint64_t)a.D, (cuuint64_t)a.L, (cuuint64_t)a.batch, 1},
                      {row, row * (uint64_t)a.L, row * (uint64_t)a.L}, {kTileCh, kRun, 1, 1});
 }
@@ -1288,15 +1289,18 @@ bool flat_map(CUtensorMap *m, const void *base, int64_t rows, const GatedArgs &a
                      {kTileCh + F::kUnit, F::kSlotRows, 1, 1});
 }
 
-// The maps of `n` tensors; whether their rows are aligned, and if not, whether
-// the flat maps are there.
+// The maps of `n` tensors, of warps' rows or flat ones; whether they are there.
 template <typename T>
-void make_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &a, bool aligned,
-               bool *flat) {
-    for (int w = 0; w < n; ++w) {
-        if (aligned) warp_map<T>(m + w, base[w], a);
-        else *flat = flat_map<T>(m + w, base[w], a.batch * a.L, a) && *flat;
-    }
+bool warp_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &a) {
+    for (int w = 0; w < n; ++w)
+        if (!warp_map<T>(m + w, base[w], a)) return false;
+    return true;
+}
+template <typename T>
+bool flat_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &a) {
+    for (int w = 0; w < n; ++w)
+        if (!flat_map<T>(m + w, base[w], a.batch * a.L, a)) return false;
+    return true;
 }
 
 // Many lanes or few (see the top). A step of the waiting chain takes 0.9 us (forward)
@@ -1329,22 +1333,12 @@ template <typename T, bool ALIGNED>
 cudaError_t forward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     return a.q ? forward_t<T, ALIGNED, true>(a, maps, st) : forward_t<T, ALIGNED, false>(a, maps, st);
 }
-// Whether TMA boxes of one warp's rows can be taken from a tensor.
-template <typename T>
-bool rows_aligned(const void *base, const GatedArgs &a) {
-    return on(base, 16) && a.D * (int64_t)sizeof(T) % 16 == 0 &&
-           (double)a.D * (double)a.L * sizeof(T) < 1.0e12;
-}
-
 template <typename T>
 cudaError_t forward_v(GatedArgs a, cudaStream_t st) {
     Maps maps;
     const void *const in[3] = {a.x, a.r, a.i};
-    if (!tensor_map_encoder()) return cudaErrorNotSupported;
-    bool aligned = on(a.y, 8) && on(a.q, 4);
-    for (const void *p : in) aligned = aligned && rows_aligned<T>(p, a);
-    a.flat = true;
-    make_maps<T>(maps.m, in, 3, a, aligned, &a.flat);
+    const bool aligned = on(a.y, 8) && on(a.q, 4) && warp_maps<T>(maps.m, in, 3, a);
+    if (!aligned) a.flat = flat_maps<T>(maps.m, in, 3, a);
     return aligned ? forward_c<T, true>(a, maps, st) : forward_c<T, false>(a, maps, st);
 }
 
@@ -1369,17 +1363,16 @@ cudaError_t backward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
 template <typename T>
 cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
     Maps maps;
-    if (!tensor_map_encoder()) return cudaErrorNotSupported;
     const int64_t n = a.batch * a.L * a.D;
     const void *const in[4] = {a.dy, a.r, a.i, a.x};
     const void *const copies[3] = {a.q, a.q + n, a.q + 2 * n};
-    bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) && rows_aligned<T>(a.dy, a);
-    for (int w = 0; w < 3; ++w)
-        aligned = aligned && (a.q ? rows_aligned<int8_t>(copies[w], a) : rows_aligned<T>(in[1 + w], a));
-    a.flat = true;
-    make_maps<T>(maps.m, in, a.q ? 1 : 4, a, aligned, &a.flat);
-    if (a.q && aligned) make_maps<int8_t>(maps.m + 1, copies, 3, a, aligned, &a.flat);
-    if (a.q && !aligned) a.flat = flat_map<int8_t>(&maps.m[1], a.q, 3 * a.batch * a.L, a) && a.flat;
+    const int own = a.q ? 1 : 4;
+    const bool aligned = on(a.dx, 8) && on(a.dr, 8) && on(a.di, 8) &&
+                         warp_maps<T>(maps.m, in, own, a) &&
+                         (!a.q || warp_maps<int8_t>(maps.m + 1, copies, 3, a));
+    if (!aligned)
+        a.flat = flat_maps<T>(maps.m, in, own, a) &&
+                 (!a.q || flat_map<int8_t>(&maps.m[1], a.q, 3 * a.batch * a.L, a));
     cudaError_t e = aligned ? backward_c<T, true>(a, maps, st) : backward_c<T, false>(a, maps, st);
     if (e != cudaSuccess) return e;
     launch_begin("gated_dlam", st);

@@ -516,6 +516,35 @@ def test_a_large_problem_past_32_bit_offsets():
         assert end <= TOL * np.sqrt(np.mean(ref * ref))
 
 
+@pytest.mark.parametrize("batch,L,D", [(2, 4000, 2600), (2, 4000, 2601)])
+def test_waits_run_out_with_many_lanes_then_recover(batch, L, D):
+    """The same with a lane for every other SM, rows ahead on their way."""
+    import selective_state_space_12_b200 as ssd
+
+    s = make(batch, L, D, dtype=BF16, seed=112)
+    want, _, st = forward(s)
+    args = (s["x"], s["r"], s["i"], s["lam"])
+    g = ssd.ssd_gated_scan_backward(*args, st, s["dy"])
+    saved = ssd.GatedCheckpoint8(batch, L, D)
+    ssd.ssd_gated_scan(*args, checkpoint=saved)
+    for call in (lambda: ssd.ssd_gated_scan(*args, h0=s["h0"]),
+                 lambda: ssd.ssd_gated_scan_backward(*args, st, s["dy"]),
+                 lambda: ssd.ssd_gated_scan_backward_ckpt8(saved, s["lam"], s["dy"])):
+        ssd.ssd_set_wait_limit(16)
+        try:
+            call()
+            status, msg = ssd.ssd_device_status(), ssd.ssd_last_error()
+        finally:
+            ssd.ssd_set_wait_limit(0)
+        assert status == 5 and "gave up" in msg
+        assert ssd.ssd_device_status() == 0
+    y, _, _ = forward(s)
+    assert torch.equal(y, want)
+    again = ssd.ssd_gated_scan_backward(*args, st, s["dy"])
+    for k in g:
+        assert torch.equal(g[k], again[k]), k
+
+
 def test_look_back_wait_runs_out_then_recovers():
     """Few channels and a long sequence: thread blocks wait for the ones before
     them. With a bound of a few cycles the call reports a time-out; the next one
