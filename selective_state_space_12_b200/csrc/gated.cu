@@ -555,10 +555,10 @@ struct Largest<__nv_bfloat16> {
 
 // Two values as int8 steps, in the low bytes: adding 1.5 2^23 rounds to the
 // nearest step, ties to even, and leaves it in the low byte (the copy's one rounding).
-__device__ __forceinline__ uint32_t in_steps(f2 v, f2 inv, uint32_t keep) {
+__device__ __forceinline__ uint32_t in_steps(f2 v, f2 inv) {
     float lo, hi;
     f2_unpack(f2_fma(v, inv, f2_both(12582912.f)), lo, hi);
-    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040) & keep;
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
 }
 
 // ------------------------------------------------------------ chain warp
@@ -860,37 +860,34 @@ __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) g
             }
         }
         if (CK) {
+            const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
+            auto copy = [&](auto run) {
+                constexpr bool kPlain = decltype(run)::value;
 #pragma unroll
-            for (int w = 0; w < 3; ++w) {
-                const int c0 = channel<ALIGNED>(0), c1 = channel<ALIGNED>(1);
-                const uint32_t k0 = s.code[w][c0], k1 = s.code[w][c1];
-                const f2 inv = f2_pack(k0 == 255 ? 0.f : __uint_as_float((254u - k0) << 23),
-                                       k1 == 255 ? 0.f : __uint_as_float((254u - k1) << 23));
-                const uint32_t keep = (k0 == 255 ? 0u : 0xffu) | (k1 == 255 ? 0u : 0xff00u);
-                int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok0 * a.D + t.d0;
-                if (ALIGNED && left >= kRun) {
-                    int8_t *to = q + (lane & 1) * a.D + (c0 & ~3);
-                    // four bytes a lane: of two neighbours' pairs of two rows, one takes the
-                    // even row's and the other the odd row's
-#pragma unroll
-                    for (int j = 0; j < kRun; j += 2, to += 2 * a.D) {
-                        const uint32_t even = in_steps(widen(v[w][j]), inv, keep);
-                        const uint32_t odd = in_steps(widen(v[w][j + 1]), inv, keep);
-                        const bool up = lane & 1;
-                        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, up ? even : odd, 1);
-                        const uint32_t word = up ? (theirs | odd << 16) : (even | theirs << 16);
-                        if (y.has0) *reinterpret_cast<uint32_t *>(to) = word;
-                    }
-                } else {
+                for (int w = 0; w < 3; ++w) {
+                    const uint32_t k0 = s.code[w][c0], k1 = s.code[w][c1];
+                    const f2 inv = f2_pack(!kPlain && k0 == 255 ? 0.f : __uint_as_float((254u - k0) << 23),
+                                           !kPlain && k1 == 255 ? 0.f : __uint_as_float((254u - k1) << 23));
+                    int8_t *q = a.q + w * a.batch * a.L * a.D + t.row0 + tok0 * a.D + t.d0 + c0;
 #pragma unroll
                     for (int j = 0; j < kRun; ++j, q += a.D) {
-                        if (j >= left) break;
-                        const uint32_t both = in_steps(widen(v[w][j]), inv, keep);
-                        if (y.has0) q[c0] = (int8_t)(both & 0xff);
-                        if (y.has1) q[c1] = (int8_t)(both >> 8);
+                        if (!kPlain && j >= left) break;
+                        uint32_t both = in_steps(widen(v[w][j]), inv);
+                        if (!kPlain) both &= (k0 == 255 ? 0u : 0xffu) | (k1 == 255 ? 0u : 0xff00u);
+                        if (kPlain && ALIGNED) {
+                            *reinterpret_cast<uint16_t *>(q) = (uint16_t)both;
+                        } else {
+                            if (kPlain || y.has0) q[0] = (int8_t)(both & 0xff);
+                            if (kPlain || y.has1) q[c1 - c0] = (int8_t)(both >> 8);
+                        }
                     }
                 }
-            }
+            };
+            bool number = true;  // no infinity or NaN in this lane's blocks
+#pragma unroll
+            for (int w = 0; w < 3; ++w) number = number && s.code[w][c0] != 255 && s.code[w][c1] != 255;
+            if (__all_sync(0xffffffffu, number) && left >= kRun && t.d0 + kTileCh <= a.D) copy(PlainRun());
+            else copy(AnyRun());
         }
         if (chained && !EAGER) {
             bar_sync(kTicketReady);
