@@ -25,19 +25,20 @@
 //    tile before, which was handed out a round of the lanes earlier. Thread blocks
 //    hold a ticket ahead, so that the next tile's inputs arrive meanwhile.
 //  - few lanes: thread blocks work on many consecutive tiles of a lane at once,
-//    and a chain of waits from tile to tile would be the whole time (1 us a step). Tiles form groups of kGroup; each publishes its (P, H), folds those
-//    before it in its group, and waits only for what leaves the group before,
-//    so the chain has one step a group. A ticket held ahead could then block
-//    the chain behind its holder's wait, so none is: the inputs that the next
-//    round of tiles needs are brought to L2 instead.
+//    and a chain of waits from tile to tile would be the whole time (1 us a step).
+//    Tiles form groups of four or eight; each publishes its (P, H), folds those
+//    before it in its group, and waits only for what leaves the group before, so
+//    the chain has one step a group. A ticket held ahead would block the chain
+//    behind its holder's wait (backward at 32 lanes 698 us for 578), so none is:
+//    the inputs that the next round of tiles needs are brought to L2 instead.
 //
 // What bounds it: bytes (8 forward and 14 backward a token and channel in bf16, 0.67
 // and 1.17 GB at b8 L2048 D5120) and, nearly as much, issue: about 100 instructions a
 // pair of channels forward and 140 backward, at 45 to 60 % of the issue slots with 18
 // to 36 warps an SM. Measured there, B200, bf16: forward 140 us (4.8 TB/s), backward
-// 271 us (4.3 TB/s), forward with 8-bit copies 244 us and
-// backward from them 332 us. One row of 65536 tokens by 2048 channels, few lanes:
-// 375 and 577 us. Rows that start anywhere (D5121): 181 and 379 us.
+// 271 us (4.3 TB/s), forward with 8-bit copies 223 us and backward from them 332 us.
+// One row of 65536 tokens by 2048 channels, few lanes: 366 and 551 us. Rows that
+// start anywhere (D5121): 181 and 379 us.
 //
 // A published word is 64 bits, cleared to all ones before the kernel, and is
 // complete once it differs from that: readers poll the data itself, and no
@@ -62,7 +63,6 @@ constexpr int kThreads = kCompute + 32;    // and the one that folds and looks b
 constexpr int kRun = kBlock / kWarps;  // tokens of a warp
 constexpr int kTileCh = 64;            // channels of a tile, two a lane
 constexpr int kStepThreads = 128;
-constexpr int kGroup = 8;              // consecutive tiles that fold each other's maps
 
 // Barriers of the compute warps and the chain warp.
 enum { kMapsReady = 1, kEntryReady = 2, kTicketReady = 3 };
@@ -598,11 +598,11 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
             if (lane == 0) after = atomicAdd(a.counter, 1u);
             after = __shfl_sync(0xffffffffu, after, 0);
         }
-        const int pos = (int)(step % kGroup);
-        const bool leaves = EAGER || pos == kGroup - 1;  // publishes what leaves it
-        const bool waits = EAGER ? step > 0 : step >= kGroup;
+        const int last_pos = (1 << a.group_bits) - 1, pos = (int)step & last_pos;
+        const bool leaves = EAGER || pos == last_pos;  // publishes what leaves it
+        const bool waits = EAGER ? step > 0 : (int)step > last_pos;
         const int64_t slot =
-            EAGER ? t.id : (int64_t)(step / kGroup) * lanes + t.id % (unsigned)lanes;
+            EAGER ? t.id : (int64_t)(step >> a.group_bits) * lanes + t.id % (unsigned)lanes;
         f2 in = 0, h = 0;
         word before = kEmpty;
         if (waits) before = load_word(&a.ends[(slot - lanes) * 32 + lane]);
@@ -631,7 +631,7 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         for (int w = 1; w < kWarps; ++w) all = then(all, m[BACK ? kWarps - 1 - w : w]);
         bool ok = true;
         if (chained && !EAGER) {
-            if (pos < kGroup - 1 && step + 1 < a.nb) {
+            if (pos < last_pos && step + 1 < a.nb) {
                 // who has read the maps may write a.last, which may be a.first: our read is done
                 if (!waits) __threadfence();
                 store_word(&a.maps[(t.id * 32 + lane) * 2], all.x, all.y);
@@ -734,7 +734,7 @@ struct AnyRun : std::false_type {};
 
 // Bytes that a warp keeps in its rows' place while it waits: a and u. Few lanes wait
 // longest, and need no room for rows ahead: four thread blocks an SM fit for three (b1
-// L65536 D2048 373 us for 388).
+// L65536 D2048 366 us for 388 without).
 template <bool ALIGNED, bool CK, bool EAGER>
 constexpr int kForwardKeep = ALIGNED && !EAGER && !CK ? 2 * kRun * 32 * 8 : 0;
 
@@ -1222,16 +1222,20 @@ int resident_blocks(size_t smem, cudaError_t *err) {
 // A persistent kernel's launch: as many thread blocks as fit, fewer where there
 // are fewer tiles; with one block of tokens one per tile.
 template <auto K>
-cudaError_t start(const char *name, size_t smem, bool eager, const GatedArgs &a, const Maps &maps,
+cudaError_t start(const char *name, size_t smem, bool eager, GatedArgs a, const Maps &maps,
                   cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const int64_t lanes = a.batch * a.dblocks, tiles = lanes * a.nb;
     int64_t grid = tiles, ends = 0, words = 0;
+    // few lanes: groups of four tiles cost less to fold, of eight make half the chain.
+    // Backward at 32 lanes (b1 L65536 D2048) 551 us in fours, 580 in eights and 640 in
+    // sixteens; at 16 lanes, b1 L20000, forward 103, 75 and 80.
+    a.group_bits = lanes >= 32 ? 2 : 3;
     const int64_t fit = resident_blocks<K>(smem, &e);
     if (e != cudaSuccess) return e;
     if (a.nb > 1) {
         if (fit < grid) grid = fit;
-        ends = (eager ? tiles : lanes * (a.nb / kGroup)) * 32;
+        ends = (eager ? tiles : lanes * (a.nb >> a.group_bits)) * 32;
         words = eager ? 0 : tiles * 64;
     }
     int64_t n = ends > words ? ends / 2 : words / 2;
@@ -1302,10 +1306,10 @@ bool flat_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &
 
 // Many lanes or few (see the top). A step of the waiting chain takes 0.9 us (forward)
 // to 1.5 us (backward from copies), in which a GPU full of thread blocks gets through
-// 64 to 90 tiles the other way: lanes for half the SMs pay. Both ways at one row of
-// 16384 tokens, bf16: 80 lanes 212 against 232 us (backward 312 against 346), 128
-// lanes 263 against 330; at b4 L4096 and 64 lanes 59 against 56; at b1 L65536 and 32
-// lanes 1314 against 375.
+// 64 to 90 tiles the other way: lanes for half the SMs pay. Both ways (groups of
+// eight) at one row of 16384 tokens, bf16: 80 lanes 212 against 232 us (backward 312
+// against 346), 128 lanes 263 against 330; at b4 L4096 and 64 lanes 59 against 56; at
+// b1 L65536 and 32 lanes 1314 against 375.
 bool many_lanes(const GatedArgs &a, cudaError_t *e) {
     int dev = 0, sms = 0;
     if ((*e = cudaGetDevice(&dev)) != cudaSuccess ||

@@ -146,6 +146,7 @@ struct GatedArgs {
     float *last = nullptr;         // h_final, or dh0
     float *dlam_part = nullptr;    // (b, nb, D)
     float *scale = nullptr;        // (D): c softplus(lam)
+    int group_bits = 0;            // few lanes: 2^group_bits tiles fold each other's maps
     bool flat = false;             // rows that start anywhere come by TMA too
     unsigned *counter = nullptr, *abort = nullptr, *err = nullptr;
     unsigned long long *ends = nullptr, *maps = nullptr;  // what tiles publish
