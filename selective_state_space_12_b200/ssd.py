@@ -350,13 +350,13 @@ def ssd_selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tens
     for name, t in (("h0", h0), ("dh_final", dh_final)):
         if t is not None:
             _check_all(((name, t),), (batch, Dc, N), torch.float32, dev)
-    f = dict(dtype=torch.float32, device=dev)
     dims, need = _call_sizes(batch, L, Dc, N, G, io, "ssd_selective_scan_backward_workspace_size")
-    out = dict(dx=torch.empty((batch, L, Dc), **f), ddt=torch.empty((batch, L, Dc), **f),
-               dA=torch.empty((Dc, N), **f), dB=torch.empty((batch, L, G, N), **f),
-               dC=torch.empty((batch, L, G, N), **f), dD=torch.empty((Dc,), **f),
-               ddt_bias=torch.empty((Dc,), **f),
-               dh0=torch.empty((batch, Dc, N), **f) if want_dh0 else None)
+    out = dict(dx=_like32(x), ddt=_like32(x), dA=_like32(A), dB=_like32(B), dC=_like32(B),
+               dD=torch.empty(Dc, dtype=torch.float32, device=dev))
+    out["ddt_bias"] = _like32(out["dD"])
+    out["dh0"] = None
+    if want_dh0:
+        out["dh0"] = torch.empty((batch, Dc, N), dtype=torch.float32, device=dev)
     opts = make_options(dt_bias, dt_softplus, dt_limit, zoh)
     workspace, ws_given = _workspace(need, workspace, dev)
     _call(lib.ssd_selective_scan_backward, dev, stream, "ssd_selective_scan_backward", _at(x),
@@ -386,6 +386,13 @@ def _check_all(tensors, shape, dtype, device):
         if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
                 and t.is_cuda and t.get_device() == index and t.is_contiguous()):
             _check_tensor(name, t, shape, dtype, device)
+
+
+def _like32(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised float32 tensor of t's shape (cheaper on the host than torch.empty)."""
+    if t.dtype is torch.float32:
+        return torch.empty_like(t)
+    return torch.empty_like(t, dtype=torch.float32)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
