@@ -566,3 +566,35 @@ def test_look_back_wait_runs_out_then_recovers():
         assert ssd.ssd_device_status() == 0
     y, _, _ = forward(s)
     assert torch.equal(y, want)
+
+
+def test_calls_at_once_on_several_streams():
+    """Calls of both ways of chaining overlap on three streams, thread blocks of
+    one waiting while the others' run: the same results to the bit."""
+    import selective_state_space_12_b200 as ssd
+
+    cases = [make(1, 9000, 512, dtype=BF16, seed=121), make(2, 1500, 2600, dtype=BF16, seed=122),
+             make(1, 7000, 333, reset=True, seed=123)]
+
+    def call(s):
+        st = torch.empty((s["x"].shape[0], ssd.gated_blocks(s["x"].shape[1]), s["x"].shape[2]),
+                         device="cuda")
+        args = (s["x"], s["r"], s["i"], s["lam"])
+        y, hf = ssd.ssd_gated_scan(*args, reset=s["reset"], h0=s["h0"], states=st)
+        g = ssd.ssd_gated_scan_backward(*args, st, s["dy"], s["dhf"], reset=s["reset"])
+        return [y, hf, st] + [g[k] for k in ("dx", "dr", "di", "dlam", "dh0")]
+
+    want = [call(s) for s in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for k, (s, stream) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(stream):
+                got[k].append(call(s))
+    torch.cuda.synchronize()
+    assert ssd.ssd_device_status() == 0, ssd.ssd_last_error()
+    for w, runs in zip(want, got):
+        for run in runs:
+            for a, b in zip(w, run):
+                assert torch.equal(a, b)
