@@ -496,7 +496,8 @@ struct Shared {
     unsigned code[3][kTileCh];
     uint64_t bars[2 * kWarps];
     Tile tile[2];              // this thread block's next tiles
-    Tile later;                // without tickets ahead: one to bring to L2
+    Tile later[2];             // without tickets ahead: one to bring to L2, by turns: nothing
+                               // keeps a warp that reads one from the next being written
     int stop[2];
 };
 
@@ -687,7 +688,9 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
         if (chained && !EAGER) {
             if (lane == 0) next = atomicAdd(a.counter, 1u);
             next = __shfl_sync(0xffffffffu, next, 0);
-            if (lane < 2) (lane ? s.later : s.tile[0]) = tile_of<BACK>(a, lane ? round_on(next) : next);
+            if (lane < 2)
+                (lane ? s.later[(n + 1) & 1] : s.tile[0]) =
+                    tile_of<BACK>(a, lane ? round_on(next) : next);
             __syncwarp();
             bar_arrive(kTicketReady);
         }
@@ -716,7 +719,7 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
         const unsigned first = a.nb > 1 ? atomicAdd(a.counter, 1u) : blockIdx.x;
         s.tile[0] = tile_of<BACK>(a, first);
         s.tile[1] = tile_of<BACK>(a, EAGER ? atomicAdd(a.counter, 1u) : tiles);
-        s.later = tile_of<BACK>(a, round_on(first));
+        s.later[0] = tile_of<BACK>(a, round_on(first));
         // a barrier a warp and stage, or one a stage that every warp arrives at
         for (int w = 0; w < 2 * kWarps; ++w) tc::mbar_init(&s.bars[w], ALIGNED ? 1 : kWarps);
         tc::fence_mbar_init();
@@ -835,7 +838,7 @@ __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) g
             tn = s.tile[(n + 1) & 1];
             ahead = here && tn.id < tiles;
             if (ahead && kAhead) advance();
-        } else if (chained) in.prefetch(a, maps.m, tiles, s.later, src);
+        } else if (chained) in.prefetch(a, maps.m, tiles, s.later[n & 1], src);
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
             if (!here) in.wait(kDrain);
@@ -1041,8 +1044,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
             ahead = here && tn.id < tiles;
             if (ahead && kAhead) advance();
         } else if (chained) {
-            in.prefetch(a, maps.m, tiles, s.later, src);
-            if constexpr (CK) copies.prefetch(a, maps.m + 1, tiles, s.later, csrc);
+            in.prefetch(a, maps.m, tiles, s.later[n & 1], src);
+            if constexpr (CK) copies.prefetch(a, maps.m + 1, tiles, s.later[n & 1], csrc);
         }
         bar_sync(kEntryReady);
         if (s.stop[n & 1]) {
