@@ -94,6 +94,11 @@ __device__ __forceinline__ unsigned load_relaxed(const unsigned *p) {
     return v;
 }
 
+// Where a lane's two words of tile `id`'s map are: past 2^32 from 2^26 tiles on (5 rows
+// of 2^30 tokens).
+constexpr int64_t map_word(int64_t id, int lane) { return (id * 32 + lane) * 2; }
+static_assert(map_word(1u << 26, 3) == (int64_t{1} << 32) + 6, "in 64 bits");
+
 struct __align__(16) Tile {
     int64_t row0;     // offset of (b, first token, 0) in a (b, L, D) tensor
     int64_t flat;     // its first token's row in a (b L, D) tensor
@@ -449,7 +454,7 @@ __device__ __forceinline__ bool group_map(const GatedArgs &a, int64_t id, int co
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const bool has = first + j < count;
-                const word *at = &a.maps[((id - (count - first - j) * lanes) * 32 + lane) * 2];
+                const word *at = &a.maps[map_word(id - (count - first - j) * lanes, lane)];
                 m0[j] = has ? load_word(at) : 0;
                 m1[j] = has ? load_word(at + 1) : 0;
             }
@@ -635,8 +640,9 @@ __device__ __forceinline__ void chain_warp(const GatedArgs &a, Shared &s, unsign
             if (pos < last_pos && step + 1 < a.nb) {
                 // who has read the maps may write a.last, which may be a.first: our read is done
                 if (!waits) __threadfence();
-                store_word(&a.maps[(t.id * 32 + lane) * 2], all.x, all.y);
-                store_word(&a.maps[(t.id * 32 + lane) * 2 + 1], all.z, all.w);
+                word *mine = &a.maps[map_word(t.id, lane)];
+                store_word(mine, all.x, all.y);
+                store_word(mine + 1, all.z, all.w);
             }
             float4 ahead;
             ok = group_map(a, t.id, pos, lanes, ahead);
