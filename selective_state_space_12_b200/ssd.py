@@ -38,6 +38,38 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> ctypes.c_void
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _elsewhere(stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether a call's stream is another than torch's current one."""
+    return (stream is not None and
+            stream.cuda_stream != torch.cuda.current_stream(stream.device).cuda_stream)
+
+
+def _on_stream(fn, args: dict):
+    """fn(**args) with args["stream"] as torch's current stream. The scratch and
+    outputs that fn takes then come from that stream's memory, which torch hands
+    out again to work behind the call's own only; taken from another stream's,
+    scratch that fn drops would be handed out while the call still runs. The
+    caller's tensors are kept until the call is done with them, the outputs until
+    the caller's stream is."""
+    stream = args["stream"]
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = fn(**args)
+    for t in _tensors(args.values()):
+        t.record_stream(stream)
+    for t in _tensors(out.values() if isinstance(out, dict) else out):
+        t.record_stream(caller)
+    return out
+
+
+def _tensors(values):
+    for v in (values,) if isinstance(values, torch.Tensor) else values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, GatedCheckpoint8):
+            yield from (v.q, v.e, v.states)
+
+
 def make_dims(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) -> _lib.Dims:
     if isinstance(dtype, torch.dtype):
         if dtype not in _DTYPES:
@@ -75,6 +107,8 @@ def ssd_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
 
     x (b,L,H,P), dt (b,L,H), B/C (b,L,G,N) share one dtype (float32 or
     bfloat16); A, D (H,) and h0, h_final (b,H,P,N) are float32."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_forward, locals())
     lib = _lib.load()
     batch, L, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -135,6 +169,8 @@ def ssd_forward_ex(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """ssd_forward on RAW steps dt, prepared in the kernels by the step options
     (see make_options)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_forward_ex, locals())
     lib = _lib.load()
     batch, L, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -180,6 +216,8 @@ def ssd_step_ex(h: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: torch.Ten
                 y: Optional[torch.Tensor] = None,
                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """ssd_step on a RAW step dt (b,H) with the step options (see make_options)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_step_ex, locals())
     lib = _lib.load()
     batch, H, P, N = h.shape
     G = B.shape[1]
@@ -219,6 +257,8 @@ def ssd_forward_state(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: tor
     """(end state (b,H,P,N), total decay (b,H)) of each lane's sequence from a
     zero initial state: the local step of sequence parallelism. dt is raw when
     step options are given (as for ssd_forward_ex)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_forward_state, locals())
     lib = _lib.load()
     batch, L, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -259,6 +299,8 @@ def ssd_state_chain(states: torch.Tensor, decays: torch.Tensor, part: int,
     """(h_in, h_total): the state entering piece ``part`` from the pieces' end
     states (R,b,H,P,N) and decays (R,b,H), and (want_total) the chain over all
     pieces."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_state_chain, locals())
     lib = _lib.load()
     R, batch, H, P, N = states.shape
     dev = states.device
@@ -291,6 +333,8 @@ def ssd_selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     """The selective scan with a diagonal A per channel: x, dt (b,L,D), A (D,N),
     B/C (b,L,G,N), Dskip (D,), h0/h_final (b,D,N); step options as for
     ssd_forward_ex (dt_bias per channel)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_selective_scan, locals())
     lib = _lib.load()
     batch, L, Dc = x.shape
     N = A.shape[1]
@@ -336,6 +380,8 @@ def ssd_selective_scan_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tens
     """Gradients of sum dy . y + sum dh_final . h_final for ssd_selective_scan
     with its step options: a dict of fp32 tensors dx, ddt (of the raw step),
     dA, dB, dC, dD, ddt_bias, dh0."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_selective_scan_backward, locals())
     lib = _lib.load()
     batch, L, Dc = x.shape
     N = A.shape[1]
@@ -486,6 +532,8 @@ def ssd_gated_scan(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch
     begins. For training, ``states`` (b,gated_blocks(L),D) float32 receives the
     state entering each block of 64 tokens, and ``checkpoint`` the inputs in 8
     bits together with those states."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_gated_scan, locals())
     lib = _lib.load()
     batch, L, D = x.shape
     dev, io = x.device, x.dtype
@@ -522,6 +570,8 @@ def ssd_gated_scan(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch
 
 def _gated_backward(x, r, i, ckpt, lam, states, dy, dh_final, c, reset, want_dh0, workspace,
                     stream, where) -> dict:
+    if _elsewhere(stream):
+        return _on_stream(_gated_backward, locals())
     lib = _lib.load()
     batch, L, D = dy.shape
     dev, io = dy.device, dy.dtype
@@ -582,6 +632,8 @@ def ssd_gated_step(h: torch.Tensor, x: torch.Tensor, r: torch.Tensor, i: torch.T
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One token of the gated recurrence: updates h (b,D) float32 in place,
     returns y (b,D) in the dtype of x, r, i (b,D)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_gated_step, locals())
     lib = _lib.load()
     batch, D = h.shape
     dev, io = x.device, x.dtype
@@ -605,6 +657,8 @@ def ssd_backward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
                  stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Gradients of sum dy . y + sum dh_final . h_final for ssd_forward's
     plain layer: a dict of fp32 tensors dx, ddt, dA, dB, dC, dD, dh0."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_backward, locals())
     lib = _lib.load()
     batch, L, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -645,6 +699,8 @@ def ssd_step(h: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor
              y: Optional[torch.Tensor] = None,
              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """One decode step: updates h (b,H,P,N) float32 in place, returns y (b,H,P)."""
+    if _elsewhere(stream):
+        return _on_stream(ssd_step, locals())
     lib = _lib.load()
     batch, H, P, N = h.shape
     G = B.shape[1]
