@@ -12,7 +12,7 @@
 // remainder is below q^5/720 < 5e-8 relative; above, one minus exp2 of the
 // special-function unit (relative error about 2^-22), where F > 0.11. The
 // series takes no special-function operation; those bind these kernels beside
-// the memory (16 a clock and SM), so both sigmoids also share one reciprocal.
+// the memory (16 a clock and SM).
 #pragma once
 
 #include "common.cuh"
@@ -24,6 +24,7 @@ namespace gated {
 constexpr int kBlock = 64;          // SSD_GATED_BLOCK: tokens per saved state and 8-bit scale
 constexpr float kSeries = 0.125f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTiny = 1.2e-38f;   // keeps a root off zero (a normal number)
 
 __device__ __forceinline__ float rcp_approx(float v) {
     float y;
@@ -35,12 +36,6 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {  // a NaN stays one
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
 // softplus(lam), and sigmoid(lam) / softplus(lam) (its limit 1 where
 // softplus underflows), by which the gradient of lam follows from that of log a.
 __device__ __forceinline__ float softplus_full(float v) {
@@ -51,14 +46,13 @@ __device__ __forceinline__ float lam_ratio(float lam) {
     return sp > 0.f ? 1.f / ((1.f + expf(-lam)) * sp) : (lam == lam ? 1.f : lam);
 }
 
-// sigmoid(r) and sigmoid(i) from one reciprocal: 1/p = q/(pq). Exponents stop
-// at 2^63, so that the product stays finite: a gate below 2^-63 reads 2^-63.
-__device__ __forceinline__ void two_sigmoids(float r, float i, float &sr, float &si) {
-    const float p = 1.f + tc::fast_exp2(min_nan(-r * kLog2e, 63.f));
-    const float q = 1.f + tc::fast_exp2(min_nan(-i * kLog2e, 63.f));
-    const float R = rcp_approx(p * q);
-    sr = q * R;
-    si = p * R;
+// exp2 overflows to infinity and its reciprocal is then 0: a gate is right down to
+// 2^-126 and shut below. (One reciprocal for a token's two gates would need bounded
+// exponents, 2^63 each. A gate that does not shut lets a long masked stretch drift, and
+// to look for such gates costs what it saves: b8 L2048 D5120 151 us for 154, b1 L65536
+// D2048 379 us for 366.)
+__device__ __forceinline__ float sigmoid(float v) {
+    return rcp_approx(1.f + tc::fast_exp2(-v * kLog2e));
 }
 
 // F = 1 - exp(-q) for q = -log a >= 0.
@@ -90,12 +84,11 @@ struct Gate {
 };
 __device__ __forceinline__ Gate gate(float r, float i, float k) {
     Gate g;
-    float sr;
-    two_sigmoids(r, i, sr, g.si);
-    const float F = forget(k * sr);
+    const float F = forget(k * sigmoid(r));
+    g.si = sigmoid(i);
     g.a = 1.f - F;
-    const float m2 = fmaf(F, g.a, F) + 1e-36f;
-    g.m = m2 * rsqrt_approx(m2);
+    const float m2 = fmaf(F, g.a, F);
+    g.m = m2 * rsqrt_approx(m2 + kTiny);
     return g;
 }
 
@@ -116,19 +109,11 @@ struct Gate2 {
     f2 m, rm;   // sqrt(1 - a^2) and its reciprocal (large where m = 0)
 };
 
-__device__ __forceinline__ f2 exp2_gate2(f2 v) {  // exp2(min(-v log2 e, 63))
+__device__ __forceinline__ f2 sigmoid2(f2 v) {
     float lo, hi;
     f2_unpack(f2_mul(v, f2_both(-kLog2e)), lo, hi);
-    return f2_pack(tc::fast_exp2(min_nan(lo, 63.f)), tc::fast_exp2(min_nan(hi, 63.f)));
-}
-__device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si) {
-    const f2 one = f2_both(1.f);
-    const f2 p = f2_add(one, exp2_gate2(r)), q = f2_add(one, exp2_gate2(i));
-    float lo, hi;
-    f2_unpack(f2_mul(p, q), lo, hi);
-    const f2 R = f2_pack(rcp_approx(lo), rcp_approx(hi));
-    sr = f2_mul(q, R);
-    si = f2_mul(p, R);
+    f2_unpack(f2_add(f2_both(1.f), f2_pack(tc::fast_exp2(lo), tc::fast_exp2(hi))), lo, hi);
+    return f2_pack(rcp_approx(lo), rcp_approx(hi));
 }
 // F = 1 - exp(-q), q = -log a >= 0.
 template <bool FAST>
@@ -146,20 +131,21 @@ __device__ __forceinline__ f2 forget2(f2 q) {
     return f2_pack(q0 <= kSeries ? f0 : 1.f - tc::fast_exp2(-q0 * kLog2e),
                    q1 <= kSeries ? f1 : 1.f - tc::fast_exp2(-q1 * kLog2e));
 }
-// a, m and 1 / m from F = 1 - a: m^2 = F (1 + a) = F + F a, kept off zero by
-// 1e-36 (m = 1e-18 where a = 1).
+// a, m and 1 / m from F = 1 - a: m^2 = F (1 + a) = F + F a. Under the root it is kept
+// off zero: m = 0 where a = 1, and within 1e-5 of its value from 3e-17 on.
 __device__ __forceinline__ void decay_from2(f2 F, Gate2 &g) {
     g.a = f2_sub(f2_both(1.f), F);
-    const f2 m2 = f2_add(f2_fma(F, g.a, F), f2_both(1e-36f));
+    const f2 m2 = f2_fma(F, g.a, F);
     float lo, hi;
-    f2_unpack(m2, lo, hi);
+    f2_unpack(f2_add(m2, f2_both(kTiny)), lo, hi);
     g.rm = f2_pack(rsqrt_approx(lo), rsqrt_approx(hi));
     g.m = f2_mul(m2, g.rm);
 }
 template <bool FAST>
 __device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
     Gate2 g;
-    two_sigmoids2(r, i, g.sr, g.si);
+    g.sr = sigmoid2(r);
+    g.si = sigmoid2(i);
     decay_from2(forget2<FAST>(f2_mul(k, g.sr)), g);
     return g;
 }
