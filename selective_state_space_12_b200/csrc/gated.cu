@@ -1100,7 +1100,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 dl = f2_add(dl, e);
                 const f2 gv = f2_mul(gm, vx);
                 dx.template put<kPlain>(f2_mul(gm, sij));
-                dr.template put<kPlain>(f2_mul(e, f2_sub(one, srj)));
+                // a reset token's decay gate counts for nothing, whatever it holds
+                dr.template put<kPlain>(cut ? none : f2_mul(e, f2_sub(one, srj)));
                 di.template put<kPlain>(f2_mul(gv, f2_sub(one, sij)));
                 h = cut ? vx : f2_fma(g.a, h, f2_mul(g.m, vx));
             }

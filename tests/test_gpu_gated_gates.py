@@ -95,3 +95,21 @@ def test_gates_that_are_all_but_shut(D):
     assert off_by_channel(y, ref) <= TOL
     for k in ("dx", "di"):
         assert off_by_channel(g[k], grads[k]) <= TOL, k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [10, 64])
+def test_a_reset_tokens_decay_gate_counts_for_nothing(D, dtype):
+    """Whatever r holds at a reset, NaN and infinities too."""
+    s = make(3, 200, D, dtype=dtype, seed=8)
+    reset = torch.zeros((3, 200), dtype=torch.uint8, device="cuda")
+    reset[0, 17] = reset[1, 64] = reset[2, 199] = reset[0, 128] = 1
+    s["reset"] = reset
+    y, hf, g = both(s)
+    for v in (float("nan"), float("inf"), float("-inf")):
+        s["r"][reset != 0] = v
+        y2, hf2, g2 = both(s)
+        assert torch.equal(y, y2) and torch.equal(hf, hf2)
+        for k in g:
+            assert torch.equal(g[k], g2[k]), k
+    assert not g["dr"][reset != 0].any()
