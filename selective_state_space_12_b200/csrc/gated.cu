@@ -1069,16 +1069,16 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
             const int64_t row = t.row0 + tok0 * a.D;
             Rows<T, ALIGNED> dx(a.dx, row, t.d0, a.D), dr(a.dr, row, t.d0, a.D),
                 di(a.di, row, t.d0, a.D);
-            f2 F[kRun], G[kRun];
+            f2 decay[kRun], G[kRun];
             f2 c = s.grad[warp][lane];
 #pragma unroll
             for (int j = kRun - 1; j >= 0; --j) {
                 if (kPlain || j < left) {
-                    F[j] = forget2<kPlain>(f2_mul(k, sr[j]));  // a = 1 - F
+                    decay[j] = decay2<kPlain>(f2_mul(k, sr[j]));
                     G[j] = f2_add(widen(dyr[j]), c);
-                    c = (!kPlain && (marks >> j & 1)) ? none : f2_mul(f2_sub(one, F[j]), G[j]);
+                    c = (!kPlain && (marks >> j & 1)) ? none : f2_mul(decay_of<kPlain>(decay[j]), G[j]);
                 } else {
-                    F[j] = G[j] = none;
+                    decay[j] = G[j] = none;
                 }
             }
             f2 h = s.entry[warp][lane];
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_backward_kernel(
                 if (!kPlain && j >= left) break;
                 const bool cut = !kPlain && (marks >> j & 1);
                 Gate2 g;
-                decay_from2(F[j], g);
+                decay_from2<kPlain>(decay[j], f2_mul(k, sr[j]), g);
                 const f2 x = CK ? f2_mul(widen(xr[j]), steps[0]) : widen(xr[j]);
                 const f2 srj = sr[j], sij = sigmoid_i(j);
                 const f2 vx = f2_mul(sij, x);  // sigmoid(i) x

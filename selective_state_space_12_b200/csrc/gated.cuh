@@ -6,13 +6,13 @@
 //   h <- a h + m sigmoid(i) x              (a reset token: a = 0, m = 1)
 //
 // a is close to 1 for channels that remember long, and an error of a is
-// multiplied by that memory, so nothing here forms 1 - a by subtraction:
-// with F = 1 - exp(-q), a = 1 - F (one rounding) and m^2 = F (1 + a). For
-// q <= kSeries, F is its Taylor series q (1 - q/2 + ... + q^4/120), whose
-// remainder is below q^5/720 < 5e-8 relative; above, one minus exp2 of the
-// special-function unit (relative error about 2^-22), where F > 0.11. The
-// series takes no special-function operation; those bind these kernels beside
-// the memory (16 a clock and SM).
+// multiplied by that memory, while of a small a the gradient of log a needs the
+// leading bits. So of a and F = 1 - a the smaller is not formed from the other:
+// for q <= kSeries, F is its Taylor series q (1 - q/2 + ... + q^4/120), whose
+// remainder is below q^5/720 < 5e-8 relative, and a = 1 - F; above, a is exp2 of
+// the special-function unit (relative error about 2^-22) and F = 1 - a > 0.11.
+// m^2 = F (1 + a). The series takes no special-function operation; those bind
+// these kernels beside the memory (16 a clock and SM).
 #pragma once
 
 #include "common.cuh"
@@ -55,14 +55,18 @@ __device__ __forceinline__ float sigmoid(float v) {
     return rcp_approx(1.f + tc::fast_exp2(-v * kLog2e));
 }
 
-// F = 1 - exp(-q) for q = -log a >= 0.
-__device__ __forceinline__ float forget(float q) {
+// a = exp(-q) and F = 1 - a, q >= 0.
+struct Decay1 {
+    float a, F;
+};
+__device__ __forceinline__ Decay1 decay(float q) {
     float p = 1.f / 120.f;
     p = fmaf(p, q, -1.f / 24.f);
     p = fmaf(p, q, 1.f / 6.f);
     p = fmaf(p, q, -0.5f);
     p = fmaf(p, q, 1.f);
-    return q <= kSeries ? q * p : 1.f - tc::fast_exp2(-q * kLog2e);
+    const float F = q * p, a = tc::fast_exp2(-q * kLog2e);
+    return q <= kSeries ? Decay1{1.f - F, F} : Decay1{a, 1.f - a};
 }
 
 // A reset's decay is written -0: it passes nothing on, whatever stands before
@@ -84,10 +88,10 @@ struct Gate {
 };
 __device__ __forceinline__ Gate gate(float r, float i, float k) {
     Gate g;
-    const float F = forget(k * sigmoid(r));
+    const Decay1 d = decay(k * sigmoid(r));
     g.si = sigmoid(i);
-    g.a = 1.f - F;
-    const float m2 = fmaf(F, g.a, F);
+    g.a = d.a;
+    const float m2 = fmaf(d.F, d.a, d.F);
     g.m = m2 * rsqrt_approx(m2 + kTiny);
     return g;
 }
@@ -115,26 +119,43 @@ __device__ __forceinline__ f2 sigmoid2(f2 v) {
     f2_unpack(f2_add(f2_both(1.f), f2_pack(tc::fast_exp2(lo), tc::fast_exp2(hi))), lo, hi);
     return f2_pack(rcp_approx(lo), rcp_approx(hi));
 }
-// F = 1 - exp(-q), q = -log a >= 0.
-template <bool FAST>
+// F = 1 - exp(-q) by its series.
 __device__ __forceinline__ f2 forget2(f2 q) {
     f2 p = f2_both(1.f / 120.f);
     p = f2_fma(p, q, f2_both(-1.f / 24.f));
     p = f2_fma(p, q, f2_both(1.f / 6.f));
     p = f2_fma(p, q, f2_both(-0.5f));
     p = f2_fma(p, q, f2_both(1.f));
-    const f2 series = f2_mul(q, p);
-    if (FAST) return series;
-    float f0, f1, q0, q1;
-    f2_unpack(series, f0, f1);
-    f2_unpack(q, q0, q1);
-    return f2_pack(q0 <= kSeries ? f0 : 1.f - tc::fast_exp2(-q0 * kLog2e),
-                   q1 <= kSeries ? f1 : 1.f - tc::fast_exp2(-q1 * kLog2e));
+    return f2_mul(q, p);
 }
-// a, m and 1 / m from F = 1 - a: m^2 = F (1 + a) = F + F a. Under the root it is kept
-// off zero: m = 0 where a = 1, and within 1e-5 of its value from 3e-17 on.
-__device__ __forceinline__ void decay_from2(f2 F, Gate2 &g) {
-    g.a = f2_sub(f2_both(1.f), F);
+// What is not formed from the other: F where all q <= kSeries (FAST), else a.
+template <bool FAST>
+__device__ __forceinline__ f2 decay2(f2 q) {
+    const f2 F = forget2(q);
+    if (FAST) return F;
+    float q0, q1, a0, a1;
+    f2_unpack(q, q0, q1);
+    f2_unpack(f2_sub(f2_both(1.f), F), a0, a1);
+    return f2_pack(q0 <= kSeries ? a0 : tc::fast_exp2(-q0 * kLog2e),
+                   q1 <= kSeries ? a1 : tc::fast_exp2(-q1 * kLog2e));
+}
+template <bool FAST>
+__device__ __forceinline__ f2 decay_of(f2 v) {  // a from decay2's result
+    return FAST ? f2_sub(f2_both(1.f), v) : v;
+}
+// a, m and 1 / m from decay2's result: m^2 = F (1 + a) = F + F a. Under the root it is
+// kept off zero: m = 0 where a = 1, and within 1e-5 of its value from 3e-17 on.
+template <bool FAST>
+__device__ __forceinline__ void decay_from2(f2 v, f2 q, Gate2 &g) {
+    f2 F = v;
+    g.a = decay_of<FAST>(v);
+    if (!FAST) {
+        float q0, q1, s0, s1, d0, d1;
+        f2_unpack(q, q0, q1);
+        f2_unpack(forget2(q), s0, s1);
+        f2_unpack(f2_sub(f2_both(1.f), v), d0, d1);
+        F = f2_pack(q0 <= kSeries ? s0 : d0, q1 <= kSeries ? s1 : d1);
+    }
     const f2 m2 = f2_fma(F, g.a, F);
     float lo, hi;
     f2_unpack(f2_add(m2, f2_both(kTiny)), lo, hi);
@@ -146,7 +167,8 @@ __device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
     Gate2 g;
     g.sr = sigmoid2(r);
     g.si = sigmoid2(i);
-    decay_from2(forget2<FAST>(f2_mul(k, g.sr)), g);
+    const f2 q = f2_mul(k, g.sr);
+    decay_from2<FAST>(decay2<FAST>(q), q, g);
     return g;
 }
 

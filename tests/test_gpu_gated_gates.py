@@ -113,3 +113,50 @@ def test_a_reset_tokens_decay_gate_counts_for_nothing(D, dtype):
         for k in g:
             assert torch.equal(g[k], g2[k]), k
     assert not g["dr"][reset != 0].any()
+
+
+def fast_tolerance(lam):
+    """The bound, and for a = exp(-q) what an error of q makes of it: q is within
+    about 5e-7 of its value (c softplus(lam) 2e-7, its gate 2e-7, their product
+    and the exponent's rounding 1e-7), so a within 5e-7 q, q <= c softplus(lam)."""
+    return TOL + 5e-7 * 8.0 * float(np.log1p(np.exp(lam)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [40, 96, 5130])
+@pytest.mark.parametrize("lam", [0.0, 2.0, 4.0])
+def test_channels_that_forget_fast(lam, D, dtype):
+    """Decays of e^-3 to e^-32 a token in every channel: the gradients of the
+    decay gate and of lam, which are in proportion to them, keep their bits."""
+    s = make(2, 150, D, dtype=dtype, reset=True, seed=9)
+    s["lam"].fill_(lam)
+    s["r"] = (2 + 0.25 * s["r"].float()).to(dtype)
+    tol = fast_tolerance(lam)
+    y, hf, g = both(s)
+    ref, grads = reference(s["x"], s["r"], s["i"], s["lam"], s["reset"], s["h0"], s["dy"], s["dhf"])
+    assert off_by_channel(y, ref) <= tol and off_by_channel(hf, ref[:, -1], ref) <= tol
+    for k in ("dx", "dr", "di", "dh0"):
+        assert off_by_channel(g[k], grads[k]) <= tol, k
+    gap = np.abs(g["dlam"].double().cpu().numpy() - np.asarray(grads["dlam"]))
+    assert np.all(gap <= tol * grads["dlam"].magnitude)
+
+
+@pytest.mark.parametrize("lam", [-3.0, 0.0, 2.0, 4.0])
+def test_a_decay_by_itself(lam):
+    """Without input a state is multiplied by its decays, down to e^-96: by the
+    scan and by the step."""
+    import selective_state_space_12_b200 as ssd
+
+    s = make(2, 3, 130, seed=10)
+    s["lam"].fill_(lam)
+    s["x"].zero_()
+    ref, _ = reference(s["x"], s["r"], s["i"], s["lam"], None, s["h0"])
+    y, _, _ = both(s)
+    h = s["h0"].clone()
+    for t in range(3):
+        x, r, i = (s[k][:, t].contiguous() for k in ("x", "r", "i"))
+        y1 = ssd.ssd_gated_step(h, x, r, i, s["lam"])
+        tol = (t + 1) * fast_tolerance(lam)
+        for got in (y[:, t], y1, h):
+            gap = np.abs(got.double().cpu().numpy() - ref[:, t])
+            assert np.all(gap <= tol * np.abs(ref[:, t]) + 2.0 ** -126)  # below: not held
