@@ -326,8 +326,8 @@ ssd_status ssd_selective_scan(const void *x, const void *dt, const float *A,
  *            ssd_selective_scan_backward_workspace_size
  *
  * Tensors need the alignment of their element type; 16-byte alignment and rows
- * of 16 bytes' multiples are faster. No output may alias an input, but for dh0
- * and dh_final. Sums over tokens, batch and channels are
+ * of 16 bytes' multiples are faster. No output may alias an input or another
+ * output, but for dh0 and dh_final. Sums over tokens, batch and channels are
  * fp32, in an order that does not change between calls. seqlen 0 gives zeros,
  * and dh0 = dh_final.
  */
@@ -380,8 +380,9 @@ ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const floa
  *
  * Tensors need the alignment of their element type; 16-byte alignment and rows
  * of 16 bytes' multiples (D a multiple of 8 in bf16, of 4 in fp32, of 16 with
- * 8-bit copies) are faster. Outputs may not alias inputs, but for h_final and
- * h0. A workspace serves one call at a time. seqlen 0 copies h0 to h_final.
+ * 8-bit copies) are faster. Outputs may not alias inputs or one another, but
+ * for h_final and h0. A workspace serves one call at a time. seqlen 0 copies h0
+ * to h_final.
  */
 #define SSD_GATED_BLOCK 64
 
@@ -407,8 +408,8 @@ ssd_status ssd_gated_scan(const void *x, const void *r, const void *i, const flo
  *             that does not change between calls
  *   dh0       (batch, D) fp32, written, or NULL; may alias dh_final
  *
- * c and reset as in the forward. Outputs may not alias inputs, but for dh0 and
- * dh_final. seqlen 0 gives dlam = 0 and dh0 = dh_final.
+ * c and reset as in the forward. Outputs may not alias inputs or one another,
+ * but for dh0 and dh_final. seqlen 0 gives dlam = 0 and dh0 = dh_final.
  */
 size_t ssd_gated_scan_backward_workspace_size(const ssd_dims *dims);
 ssd_status ssd_gated_scan_backward(const void *x, const void *r, const void *i,

@@ -177,13 +177,20 @@ struct Named {
     const char *name;
 };
 
-// No output may be one of the inputs (NULLs aside).
+// No output may be one of the inputs or another output (NULLs aside), but `last`, where
+// it is given, may be `first`: the end state that takes the initial one's place.
 template <int NO, int NI>
-ssd_status check_aliases(const Named (&outs)[NO], const Named (&ins)[NI]) {
-    for (const Named &o : outs)
+ssd_status check_aliases(const Named (&outs)[NO], const Named (&ins)[NI],
+                         const void *last = nullptr, const void *first = nullptr) {
+    for (int o = 0; o < NO; ++o) {
+        if (!outs[o].p) continue;
         for (const Named &i : ins)
-            if (o.p && o.p == i.p)
-                return fail(SSD_ERR_INVALID_ARG, "%s aliases %s", o.name, i.name);
+            if (outs[o].p == i.p && !(outs[o].p == last && i.p == first))
+                return fail(SSD_ERR_INVALID_ARG, "%s aliases %s", outs[o].name, i.name);
+        for (int k = 0; k < o; ++k)
+            if (outs[o].p == outs[k].p)
+                return fail(SSD_ERR_INVALID_ARG, "%s aliases %s", outs[o].name, outs[k].name);
+    }
     return SSD_OK;
 }
 
@@ -539,13 +546,11 @@ ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const floa
                         {ddt_bias, "ddt_bias"}, {dh0, "dh0"}};
     if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
     const Named outs[] = {{dx, "dx"}, {ddt, "ddt"}, {dA, "dA"}, {dB, "dB"}, {dC, "dC"},
-                          {dD, "dD"}, {ddt_bias, "ddt_bias"}};
+                          {dD, "dD"}, {ddt_bias, "ddt_bias"}, {dh0, "dh0"}};
     const Named ins[] = {{x, "x"}, {dt, "dt"}, {A, "A"}, {B, "B"}, {C, "C"}, {Dskip, "Dskip"},
                          {h0, "h0"}, {dy, "dy"}, {dh_final, "dh_final"},
                          {pre.bias, "options.dt_bias"}};
-    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
-    if (dh0 && (dh0 == h0 || dh0 == A))
-        return fail(SSD_ERR_INVALID_ARG, "dh0 aliases an input");
+    if ((s = check_aliases(outs, ins, dh0, dh_final)) != SSD_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
     bool owned;
@@ -583,9 +588,10 @@ ssd_status ssd_gated_scan(const void *x, const void *r, const void *i, const flo
     const Named io[] = {{x, "x"}, {r, "r"}, {i, "i"}, {y, "y"}};
     const Named f4[] = {{lam, "lam"}, {h0, "h0"}, {h_final, "h_final"}, {states, "states"}};
     if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
-    const Named outs[] = {{y, "y"}, {states, "states"}, {ckpt_q, "ckpt_q"}, {ckpt_e, "ckpt_e"}};
+    const Named outs[] = {{y, "y"}, {states, "states"}, {ckpt_q, "ckpt_q"}, {ckpt_e, "ckpt_e"},
+                          {h_final, "h_final"}};
     const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}, {h0, "h0"}, {reset, "reset"}};
-    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    if ((s = check_aliases(outs, ins, h_final, h0)) != SSD_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
     bool owned;
@@ -631,11 +637,11 @@ ssd_status ssd_gated_scan_backward(const void *x, const void *r, const void *i,
     const Named f4[] = {{lam, "lam"}, {states, "states"}, {dh_final, "dh_final"}, {dlam, "dlam"},
                         {dh0, "dh0"}};
     if ((s = check_aligned(io, esz)) != SSD_OK || (s = check_aligned(f4, 4)) != SSD_OK) return s;
-    const Named outs[] = {{dx, "dx"}, {dr, "dr"}, {di, "di"}, {dlam, "dlam"}};
+    const Named outs[] = {{dx, "dx"}, {dr, "dr"}, {di, "di"}, {dlam, "dlam"}, {dh0, "dh0"}};
     const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {ckpt_q, "ckpt_q"}, {ckpt_e, "ckpt_e"},
                          {lam, "lam"}, {states, "states"}, {dy, "dy"}, {dh_final, "dh_final"},
                          {reset, "reset"}};
-    if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
+    if ((s = check_aliases(outs, ins, dh0, dh_final)) != SSD_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
     bool owned;
@@ -674,7 +680,6 @@ ssd_status ssd_gated_step(float *h, const void *x, const void *r, const void *i,
     const Named outs[] = {{y, "y"}, {h, "h"}};
     const Named ins[] = {{x, "x"}, {r, "r"}, {i, "i"}, {lam, "lam"}};
     if ((s = check_aliases(outs, ins)) != SSD_OK) return s;
-    if (y == (void *)h) return fail(SSD_ERR_INVALID_ARG, "y aliases h");
     return gated_step_launch(pr, h, x, r, i, lam, c, y, reinterpret_cast<cudaStream_t>(stream));
 }
 
