@@ -355,6 +355,8 @@ ssd_status ssd_selective_scan_backward(const void *x, const void *dt, const floa
  * in either direction. dims->nheads is the number of channels D; headdim,
  * dstate and ngroups must be 1. dims->dtype is the type of x, r, i, y and of
  * their gradients; states and parameters are fp32, sums are held in fp32.
+ * Gates are held down to 2^-126 and are 0 below (a shut decay gate leaves the
+ * state as it was); sqrt(1 - a^2) is held from 3e-17 on and goes to 0 below.
  *
  *   x, r, i   (batch, seqlen, D)  I/O type: input, and the raw gates
  *   lam       (D) fp32
@@ -482,9 +484,11 @@ const char *ssd_last_error(void);
  * stop its own work, let its copies and tensor-core operations in flight
  * finish, free its tensor memory, store nothing, and report SSD_ERR_TIMEOUT
  * through ssd_device_status. The waits of the gated scan's kernels and of the
- * selective scan's backward pass are bounded in the same way. `cycles` is that bound in SM clock cycles for
- * kernels launched after the call, process-wide; 0 (or a negative value)
- * restores the default of about 2 s. A bound of a few cycles makes the next
+ * selective scan's backward pass are bounded and reported in the same way, but
+ * what those calls had computed by then is stored, and their later kernels run
+ * on what is there: all outputs of the call are undefined. `cycles` is that
+ * bound in SM clock cycles for kernels launched after the call, process-wide; 0
+ * (or a negative value) restores the default of about 2 s. A bound of a few cycles makes the next
  * forward or backward give up at its first wait that is not already
  * satisfied: its outputs are then undefined, and a later call with the
  * default bound computes normally.

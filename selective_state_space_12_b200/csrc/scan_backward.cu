@@ -72,8 +72,9 @@ __device__ __forceinline__ float div_approx(float a, float b) {
     return y;
 }
 
-// log(1 + e), e in [0, 1], as 2 atanh(z), z = e / (2 + e) <= 1/3: the series
-// to z^13 (the next term is below 2 z^15 / 15 < 1e-8 relative to z).
+// log(1 + e), e in [0, 1], as 2 atanh(z), z = e / (2 + e) <= 1/3: the series to
+// z^13, whose remainder is below 1.6e-8 of the result (at e = 1; 2 z^15 (1/15 +
+// z^2/17 + ...) of 2 z (1 + z^2/3 + ...)).
 __device__ __forceinline__ float log1p_unit(float e) {
     const float z = div_approx(e, 2.f + e), q = z * z;
     float p = 1.f / 13.f;
