@@ -11,10 +11,17 @@
 // softplus. With the hold, the state is carried as g = A h, which moves by
 // E = exp(dt A) - 1 alone, without the cancellation of 1 - a:
 //
-//   g <- g + E (g + x B)   w = E / A   ddt = sum_n a r (g + x B)
-//   dA = (1/A) sum_t [dt a r (g + x B) - r w x B]
+//   g <- g + E (g + x B)   w = E / A   ddt = sum_n a r (g + x B) = sum_n r (g' + x B)
 //
-// (the last difference is taken term by term, from series, where |A| < 2^-5).
+// where g' is the state after the token. dA = sum_t r [dt a h + (dw/dA) x B] by these is
+//
+//   dA = (1/A) sum_t r [dt g' - (w - dt) x B]
+//
+// w - dt is about z dt / 2, z = dt A; from w it keeps 1 / z of its bits, so for small E it
+// is dt E (1/2 - z/12) (w - dt = dt E (1/z - 1/E), and 1/z - 1/E = 1/2 - z/12 + z^3/720 -
+// ...). For large -z both forms lose: g' + x B is a (g + x B), a difference of a's size,
+// and dt g' nearly cancels dt x B. Channels that come to such steps are done by
+// far_channel, from a itself.
 // Every state entry takes an exponential a token and about a dozen fp32
 // operations, 16 or so times what a token's bytes need: the pass is bound by the
 // arithmetic, and by keeping sums over states (dx, ddt), over channels
@@ -154,6 +161,16 @@ __device__ __forceinline__ float off_zero(float A) {
     return fabsf(A) < 0x1p-40f ? (A > 0.f ? 0x1p-40f : -0x1p-40f) : A;
 }
 
+// Steps at which the hold's forms in the main loop lose bits: -z above kFar for one state (they
+// lose z 2^-24), or above kFast for all of a channel's (ddt is then of a's size, and loses
+// 2^-24 / a).
+constexpr float kFar = 24.f, kFast = 4.f;
+// For a step dt of a channel with -A in [least, most].
+__device__ __forceinline__ bool far_step(float dt, float least, float most) {
+    const float lo = dt < 0.f ? dt * most : dt * least, hi = dt < 0.f ? dt * least : dt * most;
+    return hi > kFar || lo > kFast;
+}
+
 struct BwdArgs {
     const void *x, *dt, *B, *C, *dy;
     const float *A, *Dskip;
@@ -197,7 +214,7 @@ struct MainTile : Tile<T, N, CH, ALIGNED> {
     float S[kPieces][CH * N], R[kPieces][CH * N], P[kPieces][CH * N];
     float dd[kPieces][CH], db[kPieces][CH];
     float Ds[CH];
-    int tiny;
+    unsigned far;  // channels with steps that far_channel is for
 };
 
 struct Place {
@@ -293,9 +310,11 @@ __device__ __forceinline__ bool arrived(const BwdArgs &a, Tile<T, N, CH, ALIGNED
 
 // The requested tile as floats, dt prepared; channels and tokens past the end
 // are zeros (dt = 0: a = 1, w = 0). Also A and what follows from it.
+// GRAD: fac, and with the hold the channels of `far` are for the main kernel.
 template <typename T, int N, int CH, bool ALIGNED, bool ZOH, bool GRAD, int THREADS>
-__device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
-                                       Tile<T, N, CH, ALIGNED> &s, float (*fac)[kRow]) {
+__device__ __forceinline__ void spread(const BwdArgs &a, const Place &p, int64_t d0, int64_t dend,
+                                       Tile<T, N, CH, ALIGNED> &s, float (*fac)[kRow],
+                                       unsigned *far) {
     const void *const src[3] = {a.x, a.dt, a.dy};
     const bool words = ALIGNED || by_words<T, CH>(a, p, d0);
     // eight channels by four runs of four tokens a warp: rows are written 16 bytes at a time
@@ -328,17 +347,25 @@ __device__ __forceinline__ bool spread(const BwdArgs &a, const Place &p, int64_t
         *reinterpret_cast<float4 *>(&s.dt[c][t0]) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
         *reinterpret_cast<float4 *>(&s.dy[c][t0]) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
         if (GRAD) *reinterpret_cast<float4 *>(&fac[c][t0]) = make_float4(f[0], f[1], f[2], f[3]);
+        if (GRAD && ZOH && has) {
+            float least = -s.next_A[c * N], most = least;
+#pragma unroll
+            for (int n = 1; n < N; ++n) {
+                least = fminf(least, -s.next_A[c * N + n]);
+                most = fmaxf(most, -s.next_A[c * N + n]);
+            }
+            if (far_step(fmaxf(fmaxf(v[1][0], v[1][1]), fmaxf(v[1][2], v[1][3])), least, most) ||
+                far_step(fminf(fminf(v[1][0], v[1][1]), fminf(v[1][2], v[1][3])), least, most))
+                atomicOr(far, 1u << c);
+        }
     }
-    bool tiny = false;
     for (int i = threadIdx.x; i < CH * N; i += THREADS) {
         float v = d0 + i / N < dend ? s.next_A[i] : -1.f;
         if (ZOH) v = off_zero(v);
-        tiny = tiny || fabsf(v) < 0x1p-5f;
         s.A[i] = v;
         s.Al[i] = v * kLog2eB;
         if (ZOH) s.invA[i] = -1.f / v;
     }
-    return tiny;
 }
 template <typename T, int N, int CH, bool ALIGNED, int THREADS>
 __device__ __forceinline__ void stage_rows(const BwdArgs &a, const Place &p, Tile<T, N, CH, ALIGNED> &s) {
@@ -442,7 +469,7 @@ scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
     for (int k = 0; k < p.tiles; ++k) {
         const int64_t d0 = dstart + (int64_t)k * CH;
         if (!arrived(a, s, parity)) return;
-        spread<T, N, CH, ALIGNED, ZOH, false, kThreads>(a, p, d0, dend, s, nullptr);
+        spread<T, N, CH, ALIGNED, ZOH, false, kThreads>(a, p, d0, dend, s, nullptr, nullptr);
         __syncthreads();
         if (k + 1 < p.tiles) request<T, N, CH, ALIGNED, kThreads>(a, maps, p, d0 + CH, dend, s);
         const bool has = d0 + c < dend;
@@ -554,41 +581,50 @@ __device__ __forceinline__ void share_sums(float (&u)[kPiece], float (&v)[kPiece
     }
 }
 
-// The hold's dA of one piece, term by term, dt a r h + r x B dw/dA, where some |A|
-// is near zero: dw/dA = (dt e^z - w) / A is dt^2 (phi1 - phi2), with
-// phi1 = (e^z - 1) / z and phi2 = (phi1 - 1) / z, where |z| < 1/4 from the series of
-// phi2 (remainder below z^5/5040 < 2e-7). Replaces what the main loop left in P.
+// -(w - dt) and its bits, by the size of E: kNear is where what the one form leaves out
+// (z^3/360 of it: 2e-5) is as much as the other loses (an error of E of 2^-22).
+constexpr float kNear = 1.f / 6.f;
+__device__ __forceinline__ f2 dt_less_w(f2 dt, f2 E, f2 wn, f2 A12) {
+    const f2 near = f2_mul(f2_mul(dt, E), f2_fma(dt, A12, f2_both(-0.5f)));
+    float e0, e1, n0, n1, f0, f1;
+    f2_unpack(E, e0, e1);
+    f2_unpack(near, n0, n1);
+    f2_unpack(f2_add(dt, wn), f0, f1);
+    return f2_pack(fabsf(e0) < kNear ? n0 : f0, fabsf(e1) < kNear ? n1 : f1);
+}
+
+// The hold for one lane's states of a channel with such steps: dA (its sign turned, as
+// from the main loop) to s.P, and the lane's sums for ddt, a r (g + x B) with a from exp2.
 template <typename T, int N, int CH, bool ALIGNED>
-__device__ __noinline__ void near_zero_dA(MainTile<T, N, CH, ALIGNED> &s, int piece, int lane) {
-    constexpr int kLanes = N / kQ;
-    for (int c = lane / kLanes; c < CH; c += 32 / kLanes)
-        for (int k = 0; k < kQ; ++k) {
-            const int n = (lane % kLanes) * kQ + k, at = c * N + n;
-            const float A = s.A[at], invA = -s.invA[at];
-            float g[kPiece], E[kPiece], st = s.S[piece][at], carry = s.R[piece][at], dA = 0.f;
-            for (int t = 0; t < kPiece; ++t) {
-                const int tok = piece * kPiece + t;
-                float unused;
-                f2_unpack(Decay<true>{f2_both(s.Al[at])}.at(f2_both(s.dt[c][tok])), E[t], unused);
-                g[t] = st;
-                st = fmaf(E[t], st + s.x[c][tok] * s.B[tok][n], st);
-            }
-            for (int t = kPiece - 1; t >= 0; --t) {
-                const int tok = piece * kPiece + t;
-                const float dt = s.dt[c][tok], in = s.x[c][tok] * s.B[tok][n], z = dt * A;
-                const float r = fmaf(s.dy[c][tok], s.C[tok][n], carry);
-                carry = fmaf(r, E[t], r);
-                float phi2 = 1.f / 720.f;
-                phi2 = fmaf(phi2, z, 1.f / 120.f);
-                phi2 = fmaf(phi2, z, 1.f / 24.f);
-                phi2 = fmaf(phi2, z, 1.f / 6.f);
-                phi2 = fmaf(phi2, z, 0.5f);
-                const float slope = fabsf(z) < 0.25f ? dt * dt * (fmaf(z, phi2, 1.f) - phi2)
-                                                     : (fmaf(dt, E[t], dt) - E[t] * invA) * invA;
-                dA = fmaf(dt * carry, g[t] * invA, fmaf(r * in, slope, dA));
-            }
-            s.P[piece][at] = -dA;
+__device__ __noinline__ float4 far_channel(MainTile<T, N, CH, ALIGNED> &s, int piece, int c, int n0) {
+    float v[kPiece] = {};
+    for (int k = 0; k < kQ; ++k) {
+        const int n = n0 + k, at = c * N + n;
+        const float Al = s.Al[at], invA = s.invA[at];
+        float E[kPiece], after[kPiece], decayed[kPiece];
+        float st = s.S[piece][at], carry = s.R[piece][at], dA = 0.f, unused;
+#pragma unroll
+        for (int t = 0; t < kPiece; ++t) {
+            const int tok = piece * kPiece + t;
+            const float dt = s.dt[c][tok], before = fmaf(s.x[c][tok], s.B[tok][n], st);
+            f2_unpack(Decay<true>{f2_both(Al)}.at(f2_both(dt)), E[t], unused);
+            decayed[t] = tc::fast_exp2(dt * Al) * before;
+            after[t] = st = fmaf(E[t], before, st);
         }
+#pragma unroll
+        for (int t = kPiece - 1; t >= 0; --t) {
+            const int tok = piece * kPiece + t;
+            const float dt = s.dt[c][tok], in = s.x[c][tok] * s.B[tok][n];
+            const float r = fmaf(s.dy[c][tok], s.C[tok][n], carry), wn = E[t] * invA;
+            const float near = dt * E[t] * fmaf(dt, s.A[at] * (1.f / 12.f), -0.5f);
+            const bool is_near = fabsf(E[t]) < kNear;
+            dA = fmaf(r, fmaf(dt, is_near ? after[t] : decayed[t], in * (is_near ? near : wn)), dA);
+            v[t] = fmaf(r, decayed[t], v[t]);
+            carry = fmaf(r, E[t], r);
+        }
+        s.P[piece][at] = invA * dA;
+    }
+    return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // A warp has a piece of four tokens, a lane four states of one channel at a time: sums
@@ -630,9 +666,9 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
     for (int tile = 0; tile < p.tiles; ++tile) {
         const int64_t d0 = dstart + (int64_t)tile * CH;
         const int here = (int)(dend - d0 < CH ? dend - d0 : CH);  // channels
-        if (tid == 0) s.tiny = 0;
+        if (tid == 0) s.far = 0;
         if (!arrived(a, s, parity)) return;
-        if (spread<T, N, CH, ALIGNED, ZOH, true, kMainThreads>(a, p, d0, dend, s, s.fac)) s.tiny = 1;
+        spread<T, N, CH, ALIGNED, ZOH, true, kMainThreads>(a, p, d0, dend, s, s.fac, &s.far);
         if (tid < CH) s.Ds[tid] = (a.Dskip && tid < here) ? s.next_Ds[tid] : 0.f;
         // this thread's pair of links of the chains over pieces
         float2 link_h = make_float2(0.f, 0.f), link_r = link_h;
@@ -680,7 +716,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             // the hold's 1 / A enters with its sign turned, so that dA's difference is a sum:
             // accB, accC, sB and dA come out turned too
             f2 invA[2], An[2], st[2], carry[2], dA[2], F[kPiece][2];
-            f2 before[kPiece][2];  // a token's state before it; with the hold g + x B
+            f2 state[kPiece][2];  // the state before each token; with the hold g after it
             load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
             load4x(&s.invA[c * N + n0], invA);
             load4x(&s.S[piece][c * N + n0], st);
@@ -700,17 +736,20 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                 for (int k = 0; k < 2; ++k) {
                     F[t][k] = A[k].at(dt);
                     if (ZOH) {
-                        before[t][k] = f2_fma(in, B[k], st[k]);
-                        st[k] = f2_fma(F[t][k], before[t][k], st[k]);
+                        st[k] = f2_fma(F[t][k], f2_fma(in, B[k], st[k]), st[k]);
+                        state[t][k] = st[k];
                         accC[t][k] = f2_fma(dy, f2_mul(st[k], invA[k]), accC[t][k]);
                     } else {
-                        before[t][k] = st[k];
+                        state[t][k] = st[k];
                         st[k] = f2_fma(F[t][k], st[k], f2_mul(in, B[k]));
                         accC[t][k] = f2_fma(dy, st[k], accC[t][k]);
                     }
                 }
             }
-            if (!ZOH) load4x(&s.A[c * N + n0], An);
+            load4x(&s.A[c * N + n0], An);
+            if (ZOH)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) An[k] = f2_mul(An[k], f2_both(1.f / 12.f));
             float vB[kPiece], vA[kPiece];
 #pragma unroll
             for (int k = 0; k < 2; ++k) dA[k] = none;
@@ -718,7 +757,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             for (int t = kPiece - 1; t >= 0; --t) {
                 const f2 dt = f2_both(ds[t]), dy = f2_both(ys[t]);
                 const f2 u = f2_both(ZOH ? xs[t] : xs[t] * ds[t]);
-                f2 B[2], C[2], sB = none, sA = none;
+                f2 B[2], C[2], sB = none, sA = none, sAB = none;
                 load4x(&s.B[t0 + t][n0], B);
                 load4x(&s.C[t0 + t][n0], C);
 #pragma unroll
@@ -726,14 +765,16 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                     const f2 rv = f2_fma(dy, C[k], carry[k]);
                     const f2 ra = times_decay<ZOH>(rv, F[t][k]);
                     if (ZOH) {
-                        const f2 rw = f2_mul(rv, f2_mul(F[t][k], invA[k]));
-                        const f2 rt = f2_mul(ra, before[t][k]), rwB = f2_mul(rw, B[k]);
-                        sB = k == 0 ? rwB : f2_add(sB, rwB);
-                        accB[t][k] = f2_fma(rw, u, accB[t][k]);
-                        sA = k == 0 ? rt : f2_add(sA, rt);
-                        dA[k] = f2_fma(dt, rt, f2_fma(u, rwB, dA[k]));
+                        const f2 wn = f2_mul(F[t][k], invA[k]), ru = f2_mul(rv, u);
+                        const f2 rg = f2_mul(rv, state[t][k]), rB = f2_mul(rv, B[k]);
+                        sB = k == 0 ? f2_mul(rB, wn) : f2_fma(rB, wn, sB);
+                        accB[t][k] = f2_fma(ru, wn, accB[t][k]);
+                        sA = k == 0 ? rg : f2_add(sA, rg);
+                        sAB = k == 0 ? rB : f2_add(sAB, rB);
+                        dA[k] = f2_fma(dt, rg, f2_fma(f2_mul(ru, B[k]),
+                                                      dt_less_w(dt, F[t][k], wn, An[k]), dA[k]));
                     } else {
-                        const f2 t1 = f2_mul(ra, before[t][k]);
+                        const f2 t1 = f2_mul(ra, state[t][k]);
                         sB = k == 0 ? f2_mul(rv, B[k]) : f2_fma(rv, B[k], sB);
                         accB[t][k] = f2_fma(rv, u, accB[t][k]);
                         sA = k == 0 ? f2_mul(An[k], t1) : f2_fma(An[k], t1, sA);
@@ -744,13 +785,17 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                 float lo, hi;
                 f2_unpack(sB, lo, hi);
                 vB[t] = lo + hi;
-                f2_unpack(sA, lo, hi);
+                f2_unpack(ZOH ? f2_fma(u, sAB, sA) : sA, lo, hi);
                 vA[t] = lo + hi;
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 if (ZOH) dA[k] = f2_mul(invA[k], dA[k]);
             store4x(&s.P[piece][c * N + n0], dA);
+            if (ZOH && (s.far >> c & 1)) {
+                const float4 v = far_channel<T, N, CH, ALIGNED>(s, piece, c, n0);
+                vA[0] = v.x, vA[1] = v.y, vA[2] = v.z, vA[3] = v.w;
+            }
             // dx and ddt: each lane of the channel ends with the sums of its share of the tokens
             share_sums<kLanes>(vB, vA, lane);
             float db = 0.f, dd = 0.f;
@@ -773,7 +818,6 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
                 s.dd[piece][c] = dd;
             }
         }
-        if (ZOH && s.tiny) near_zero_dA<T, N, CH, ALIGNED>(s, piece, lane);
         __syncthreads();
         if (2 * tid < here * N) {
             float2 v = make_float2(0.f, 0.f);
