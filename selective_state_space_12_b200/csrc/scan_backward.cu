@@ -139,10 +139,14 @@ template <bool ZOH>
 struct Decay {
     f2 Al;  // A log2 e (hold: A kept off zero)
     __device__ __forceinline__ f2 at(f2 dt) const {
+        f2 a;
+        return at(dt, a);
+    }
+    __device__ __forceinline__ f2 at(f2 dt, f2 &e) const {  // e: exp(dt A) in both cases
         const f2 y = f2_mul(dt, Al);
         float y0, y1;
         f2_unpack(y, y0, y1);
-        const f2 e = f2_pack(tc::fast_exp2(y0), tc::fast_exp2(y1));
+        e = f2_pack(tc::fast_exp2(y0), tc::fast_exp2(y1));
         if (!ZOH) return e;
         constexpr double k = 0.693147180559945309;  // ln 2
         f2 p = f2_fma(f2_both((float)(k * k * k * k / 24)), y, f2_both((float)(k * k * k / 6)));
@@ -429,9 +433,10 @@ __device__ __forceinline__ void run_sums(const Tile<T, N, CH, ALIGNED> &s, int c
             load4x(&s.C[t4 + j][n0], C);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const f2 F = A[k].at(dt);
+                f2 e;
+                const f2 F = A[k].at(dt, e);
                 S[k] = move<ZOH>(F, S[k], f2_mul(in, B[k]));
-                P[k] = times_decay<ZOH>(P[k], F);
+                P[k] = f2_mul(P[k], e);  // not by 1 + E: dh0 is of the size of the decays
                 R[k] = f2_fma(P[k], f2_mul(dy, C[k]), R[k]);
             }
         }
@@ -601,14 +606,16 @@ __device__ __noinline__ float4 far_channel(MainTile<T, N, CH, ALIGNED> &s, int p
     for (int k = 0; k < kQ; ++k) {
         const int n = n0 + k, at = c * N + n;
         const float Al = s.Al[at], invA = s.invA[at];
-        float E[kPiece], after[kPiece], decayed[kPiece];
+        float E[kPiece], decay[kPiece], after[kPiece], decayed[kPiece];
         float st = s.S[piece][at], carry = s.R[piece][at], dA = 0.f, unused;
 #pragma unroll
         for (int t = 0; t < kPiece; ++t) {
             const int tok = piece * kPiece + t;
             const float dt = s.dt[c][tok], before = fmaf(s.x[c][tok], s.B[tok][n], st);
-            f2_unpack(Decay<true>{f2_both(Al)}.at(f2_both(dt)), E[t], unused);
-            decayed[t] = tc::fast_exp2(dt * Al) * before;
+            f2 e;
+            f2_unpack(Decay<true>{f2_both(Al)}.at(f2_both(dt), e), E[t], unused);
+            f2_unpack(e, decay[t], unused);
+            decayed[t] = decay[t] * before;
             after[t] = st = fmaf(E[t], before, st);
         }
 #pragma unroll
@@ -620,7 +627,7 @@ __device__ __noinline__ float4 far_channel(MainTile<T, N, CH, ALIGNED> &s, int p
             const bool is_near = fabsf(E[t]) < kNear;
             dA = fmaf(r, fmaf(dt, is_near ? after[t] : decayed[t], in * (is_near ? near : wn)), dA);
             v[t] = fmaf(r, decayed[t], v[t]);
-            carry = fmaf(r, E[t], r);
+            carry = r * decay[t];
         }
         s.P[piece][at] = invA * dA;
     }

@@ -37,7 +37,9 @@ def by_channel(got, ref):
 
 def holds(s, **o):
     g, ref = run(s, zoh=True, **o), reference(s, zoh=True, **o)
-    far = {k: off(g[k], v) for k, v in ref.items() if np.any(v) and k != "dh0"}
+    # what lies below fp32's least normal number (dh0 after a hundred fast decays) is not held
+    ref = {k: np.where(np.abs(v) < 2.0 ** -126, 0, v) for k, v in ref.items()}
+    far = {k: off(g[k], v) for k, v in ref.items() if np.any(v)}
     far["ddt of each channel"] = by_channel(g["ddt"], ref["ddt"])
     assert all(v <= TOL for v in far.values()), {k: v for k, v in far.items() if v > TOL}
 
