@@ -26,7 +26,7 @@
 //    hold a ticket ahead, so that the next tile's inputs arrive meanwhile.
 //  - few lanes: thread blocks work on many consecutive tiles of a lane at once,
 //    and a chain of waits from tile to tile would be the whole time (1 us a step).
-//    Tiles form groups of four or eight; each publishes its (P, H), folds those
+//    Tiles form groups of four or eight (start()); each publishes its (P, H), folds those
 //    before it in its group, and waits only for what leaves the group before, so
 //    the chain has one step a group. A ticket held ahead would block the chain
 //    behind its holder's wait (backward at 32 lanes 698 us for 578), so none is:
@@ -1232,15 +1232,16 @@ int resident_blocks(size_t smem, cudaError_t *err) {
 // A persistent kernel's launch: as many thread blocks as fit, fewer where there
 // are fewer tiles; with one block of tokens one per tile.
 template <auto K>
-cudaError_t start(const char *name, size_t smem, bool eager, GatedArgs a, const Maps &maps,
-                  cudaStream_t st) {
+cudaError_t start(const char *name, size_t smem, bool back, bool eager, GatedArgs a,
+                  const Maps &maps, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const int64_t lanes = a.batch * a.dblocks, tiles = lanes * a.nb;
     int64_t grid = tiles, ends = 0, words = 0;
-    // few lanes: groups of four tiles cost less to fold, of eight make half the chain.
-    // Backward at 32 lanes (b1 L65536 D2048) 551 us in fours, 580 in eights and 640 in
-    // sixteens; at 16 lanes, b1 L20000, forward 103, 75 and 80.
-    a.group_bits = lanes >= 32 ? 2 : 3;
+    // few lanes: groups of four tiles cost less to fold, of eight make half the chain. One
+    // row of 16384 tokens, bf16, fours / eights: forward at 16 lanes 82 / 60 us, 24 85 / 79,
+    // 28 91 / 89, 32 98 / 99, 48 134 / 139; backward at 4 lanes 48 / 32, 8 53 / 52, 12 69 /
+    // 70, 24 119 / 123, 48 215 / 223 (65536 tokens, 32 lanes: 573 / 601, sixteens 640).
+    a.group_bits = lanes >= (back ? 9 : 32) ? 2 : 3;
     const int64_t fit = resident_blocks<K>(smem, &e);
     if (e != cudaSuccess) return e;
     if (a.nb > 1) {
@@ -1314,12 +1315,18 @@ bool flat_maps(CUtensorMap *m, const void *const *base, int n, const GatedArgs &
     return true;
 }
 
-// Many lanes or few (see the top). A step of the waiting chain takes 0.9 us (forward)
-// to 1.5 us (backward from copies), in which a GPU full of thread blocks gets through
-// 64 to 90 tiles the other way: lanes for half the SMs pay. Both ways (groups of
-// eight) at one row of 16384 tokens, bf16: 80 lanes 212 against 232 us (backward 312
-// against 346), 128 lanes 263 against 330; at b4 L4096 and 64 lanes 59 against 56; at
-// b1 L65536 and 32 lanes 1314 against 375.
+// Many lanes or few (see the top): the chain of waits takes 0.7 to 1.3 us a step (a tile
+// of each lane), which a GPU full of thread blocks spends on other lanes' tiles from about
+// lanes for half the SMs on. Groups of four / waiting, one row of 8192 tokens, us:
+//   lanes            64          80          96          128
+//   bf16 forward     89 / 101    107 / 112   125 / 123   157 / 145
+//   bf16 backward    143 / 145   175 / 167   206 / 194   268 / 248
+//   bf16 copies      121 / 140   146 / 146   173 / 161   228 / 198, backward 169 / 163 ... 322 / 284
+//   fp32 forward     109 / 107   130 / 118   152 / 132   199 / 164
+//   fp32 backward    202 / 196   248 / 246   295 / 292   394 / 378
+// Rows that start anywhere: bf16 as these, but fp32's backward pass (262 / 282 at 80 lanes)
+// and those from copies (249 / 264) lose 4 to 12 % by waiting at all counts. At 32 lanes
+// and 65536 tokens waiting takes 1314 us and groups 365.
 bool many_lanes(const GatedArgs &a, cudaError_t *e) {
     int dev = 0, sms = 0;
     if ((*e = cudaGetDevice(&dev)) != cudaSuccess ||
@@ -1337,8 +1344,8 @@ cudaError_t forward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const bool eager = many_lanes(a, &e);
     if (e != cudaSuccess) return e;
-    return eager ? start<many>("gated_forward", ahead, true, a, maps, st)
-                 : start<few>("gated_forward", kept, false, a, maps, st);
+    return eager ? start<many>("gated_forward", ahead, false, true, a, maps, st)
+                 : start<few>("gated_forward", kept, false, false, a, maps, st);
 }
 template <typename T, bool ALIGNED>
 cudaError_t forward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
@@ -1363,8 +1370,8 @@ cudaError_t backward_t(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const bool eager = many_lanes(a, &e);
     if (e != cudaSuccess) return e;
-    return eager ? start<many>("gated_backward", smem, true, a, maps, st)
-                 : start<few>("gated_backward", smem, false, a, maps, st);
+    return eager ? start<many>("gated_backward", smem, true, true, a, maps, st)
+                 : start<few>("gated_backward", smem, true, false, a, maps, st);
 }
 template <typename T, bool ALIGNED>
 cudaError_t backward_c(const GatedArgs &a, const Maps &maps, cudaStream_t st) {
@@ -1395,7 +1402,8 @@ cudaError_t backward_v(GatedArgs a, float *dlam, cudaStream_t st) {
 
 // Pairs of channels where rows allow them and there is work for every SM all the
 // same (b256 D8192: 10.3 us for 12.3), and up to eight rows a thread while eight
-// thread blocks an SM are left (8.3 us).
+// thread blocks an SM are left (8.3 us). 148 SMs: the B200's; asking the device would
+// cost the host more than a call's kernel takes, and nothing but speed hangs on it.
 template <typename T>
 void step_v(const Problem &pr, float *h, const void *x, const void *r, const void *i,
             const float *lam, float c, void *y, cudaStream_t st) {

@@ -938,7 +938,7 @@ void split(const Problem &pr, BwdArgs &a, int resident) {
         a.blocks_per_group = (int)blocks;
     }
 }
-constexpr int kSms = 148;
+constexpr int kSms = 148;  // the B200's: the workspace's size must not hang on a device
 void split_main(const Problem &pr, BwdArgs &a) { split(pr, a, 2 * kSms); }
 
 struct Carved {
