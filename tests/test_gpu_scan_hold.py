@@ -4,7 +4,7 @@ scan's other tests, held to their bound, 2e-4.
 
 What the kernel's forms lose, of a term's size: near 0 the form of w - dt leaves
 out z^3/360 of it, 1.7e-5 where the other takes over, which loses 2^-22 / (z^2/2)
-there, 1.4e-5; at z = -24 that loses 24 x 2^-24 a rounding, 6e-6 for four; and
+there, 1.4e-5; at z = -96 that loses 96 x 2^-24 a rounding, 2.3e-5 for four; and
 with a = exp(z) above e^-4 a sum of a's size keeps 2^-24 / a, 3e-6 a rounding."""
 import numpy as np
 import pytest
@@ -96,7 +96,8 @@ def test_one_token_at_every_step(N, A):
     each state, so each entry is held to its own size. dA = r x B dt^2 (z e^z -
     (e^z - 1)) / z^2 and ddt = r x B e^z."""
     D = 512
-    z = np.sign(A) * np.exp(np.linspace(np.log(1e-7), np.log(60.0), D))
+    z = np.sign(A) * np.exp(np.linspace(np.log(1e-7), np.log(60.0 if A > 0 else 200.0), D))
+    hold = z > -80  # exp(z) is a normal number, for ddt
     s = make(1, 1, D, N, softplus=False, h0=False, seed=4, Dskip=False)
     s["A"].fill_(A)
     s["dt"] = put(z / A)[None, None]
@@ -105,4 +106,5 @@ def test_one_token_at_every_step(N, A):
     g, ref = run(s, zoh=True), reference(s, zoh=True)
     for k in ("dA", "ddt", "dx", "dB", "dC"):
         rel = np.abs(f64(g[k]) - ref[k]) / np.abs(ref[k])
+        rel = rel[..., hold] if k == "ddt" else rel
         assert rel.max() <= TOL, (k, rel.max())
