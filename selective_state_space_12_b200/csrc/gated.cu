@@ -734,8 +734,9 @@ __device__ __forceinline__ void open_block(const GatedArgs &a, Shared &s, unsign
 }
 
 // The plain case of a warp's eight tokens (all there, with all the tile's
-// channels, no reset, slow decays) is straight code; every other case runs a
-// general copy with a branch a token.
+// channels, no reset, slow decays, and with a shared reciprocal no gate all but
+// shut) is straight code; every other case runs a general copy with a branch a
+// token.
 struct PlainRun : std::true_type {};
 struct AnyRun : std::false_type {};
 
@@ -773,23 +774,32 @@ __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) g
     const int tok0 = warp * kRun;
     const bool chained = a.nb > 1;
     constexpr bool kAhead = decltype(in)::kAhead;
+    // one reciprocal for both gates, and the plain case done again where that is not right:
+    // b8 L2048 D5120 138 us for 147. Rows that start anywhere take 181 us with it and 177
+    // without, few lanes 379 for 366 (b1 L65536 D2048), and the backward kernel, whose
+    // registers it costs, 286 for 285. With copies 228 us for 225, but the outputs are to be
+    // those without copies to the bit.
+    constexpr bool kShared = ALIGNED && EAGER;
     bool ahead = false;  // copies are on their way
     for (int n = 0;; ++n) {
         const unsigned marks = __ballot_sync(0xffffffffu, mark != 0);
         const int left = t.n - tok0;
-        const bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
+        bool plain = all_fast(k) && marks == 0 && left >= kRun && t.d0 + kTileCh <= a.D;
         const bool here = in.wait(a.wait);
         if (!here) give_up(a, &s.stop[n & 1]);
         typename Pair<T>::type v[3][kRun];
         f2 av[kRun], u[kRun];
-        f2 P = f2_both(1.f), H = f2_both(0.f);
+        f2 P, H, top = f2_both(0.f);
         auto gates = [&](auto run) {
             constexpr bool kPlain = decltype(run)::value;
+            P = f2_both(1.f);
+            H = f2_both(0.f);
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
 #pragma unroll
                 for (int w = 0; w < 3; ++w) v[w][j] = in.get(w, j);
-                const Gate2 g = gate2<kPlain>(widen(v[1][j]), widen(v[2][j]), k);
+                const Gate2 g =
+                    gate2<kPlain, kPlain && kShared>(widen(v[1][j]), widen(v[2][j]), k, top);
                 const f2 ix = f2_mul(g.si, widen(v[0][j]));
                 if (kPlain || (j < left && !(marks >> j & 1))) {
                     av[j] = g.a;
@@ -807,8 +817,11 @@ __launch_bounds__(kThreads, CK ? 2 : kForwardKeep<ALIGNED, CK, EAGER> ? 4 : 3) g
                 }
             }
         };
-        if (plain) gates(PlainRun());
-        else gates(AnyRun());
+        if (plain) {
+            gates(PlainRun());
+            if (kShared) plain = gates_open(top);
+        }
+        if (!plain) gates(AnyRun());
         if (CK) {
 #pragma unroll
             for (int w = 0; w < 3; ++w) {

@@ -47,10 +47,7 @@ __device__ __forceinline__ float lam_ratio(float lam) {
 }
 
 // exp2 overflows to infinity and its reciprocal is then 0: a gate is right down to
-// 2^-126 and shut below. (One reciprocal for a token's two gates would need bounded
-// exponents, 2^63 each. A gate that does not shut lets a long masked stretch drift, and
-// to look for such gates costs what it saves: b8 L2048 D5120 151 us for 154, b1 L65536
-// D2048 379 us for 366.)
+// 2^-126 and shut below.
 __device__ __forceinline__ float sigmoid(float v) {
     return rcp_approx(1.f + tc::fast_exp2(-v * kLog2e));
 }
@@ -119,6 +116,31 @@ __device__ __forceinline__ f2 sigmoid2(f2 v) {
     f2_unpack(f2_add(f2_both(1.f), f2_pack(tc::fast_exp2(lo), tc::fast_exp2(hi))), lo, hi);
     return f2_pack(rcp_approx(lo), rcp_approx(hi));
 }
+// sigmoid(r) and sigmoid(i) from one reciprocal: with p = 1 + exp(-r) and q = 1 + exp(-i),
+// 1/p = q/(pq). Right where pq stays below kGatesTop (r + i above about -86): whoever
+// takes it adds pq up in `top`, looks at that (gates_open), and takes the gates one by
+// one where it is more, or a gate that is all but shut would not be: m = 1e-9 for 0
+// moves a state over a long masked stretch.
+constexpr float kGatesTop = 0x1p125f;
+__device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si, f2 &top) {
+    float r0, r1, i0, i1;
+    f2_unpack(f2_mul(r, f2_both(-kLog2e)), r0, r1);
+    f2_unpack(f2_mul(i, f2_both(-kLog2e)), i0, i1);
+    const f2 p = f2_add(f2_both(1.f), f2_pack(tc::fast_exp2(r0), tc::fast_exp2(r1)));
+    const f2 q = f2_add(f2_both(1.f), f2_pack(tc::fast_exp2(i0), tc::fast_exp2(i1)));
+    const f2 pq = f2_mul(p, q);
+    top = f2_add(top, pq);
+    float lo, hi;
+    f2_unpack(pq, lo, hi);
+    const f2 R = f2_pack(rcp_approx(lo), rcp_approx(hi));
+    sr = f2_mul(q, R);
+    si = f2_mul(p, R);
+}
+__device__ __forceinline__ bool gates_open(f2 top) {  // of the warp's; a NaN is not
+    float lo, hi;
+    f2_unpack(top, lo, hi);
+    return __all_sync(0xffffffffu, lo < kGatesTop && hi < kGatesTop);
+}
 // F = 1 - exp(-q) by its series.
 __device__ __forceinline__ f2 forget2(f2 q) {
     f2 p = f2_both(1.f / 120.f);
@@ -162,14 +184,24 @@ __device__ __forceinline__ void decay_from2(f2 v, f2 q, Gate2 &g) {
     g.rm = f2_pack(rsqrt_approx(lo), rsqrt_approx(hi));
     g.m = f2_mul(m2, g.rm);
 }
-template <bool FAST>
-__device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
+// SHARED: the sigmoids by two_sigmoids2.
+template <bool FAST, bool SHARED>
+__device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k, f2 &top) {
     Gate2 g;
-    g.sr = sigmoid2(r);
-    g.si = sigmoid2(i);
+    if (SHARED) {
+        two_sigmoids2(r, i, g.sr, g.si, top);
+    } else {
+        g.sr = sigmoid2(r);
+        g.si = sigmoid2(i);
+    }
     const f2 q = f2_mul(k, g.sr);
     decay_from2<FAST>(decay2<FAST>(q), q, g);
     return g;
+}
+template <bool FAST>
+__device__ __forceinline__ Gate2 gate2(f2 r, f2 i, f2 k) {
+    f2 unused = 0;
+    return gate2<FAST, false>(r, i, k, unused);
 }
 
 }  // namespace gated
