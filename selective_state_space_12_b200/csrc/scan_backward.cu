@@ -352,15 +352,23 @@ __device__ __forceinline__ void spread(const BwdArgs &a, const Place &p, int64_t
         *reinterpret_cast<float4 *>(&s.dt[c][t0]) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
         *reinterpret_cast<float4 *>(&s.dy[c][t0]) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
         if (GRAD) *reinterpret_cast<float4 *>(&fac[c][t0]) = make_float4(f[0], f[1], f[2], f[3]);
-        if (GRAD && ZOH && has) {
-            float least = -s.next_A[c * N], most = least;
+        if (GRAD && ZOH) {
+            // the four lanes of a channel look at a quarter of its A each
+            const float *mine = &s.next_A[c * N + (i / 8) % 4 * (N / 4)];
+            float least = -mine[0], most = least;
 #pragma unroll
-            for (int n = 1; n < N; ++n) {
-                least = fminf(least, -s.next_A[c * N + n]);
-                most = fmaxf(most, -s.next_A[c * N + n]);
+            for (int n = 1; n < N / 4; ++n) {
+                least = fminf(least, -mine[n]);
+                most = fmaxf(most, -mine[n]);
             }
-            if (far_step(fmaxf(fmaxf(v[1][0], v[1][1]), fmaxf(v[1][2], v[1][3])), least, most) ||
-                far_step(fminf(fminf(v[1][0], v[1][1]), fminf(v[1][2], v[1][3])), least, most))
+#pragma unroll
+            for (int o = 8; o < 32; o <<= 1) {
+                least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            }
+            if (has &&
+                (far_step(fmaxf(fmaxf(v[1][0], v[1][1]), fmaxf(v[1][2], v[1][3])), least, most) ||
+                 far_step(fminf(fminf(v[1][0], v[1][1]), fminf(v[1][2], v[1][3])), least, most)))
                 atomicOr(far, 1u << c);
         }
     }
@@ -411,8 +419,9 @@ __device__ __forceinline__ f2 times_decay(f2 v, f2 F) {
 }
 
 // The map of a run of tokens for one thread's four states: end state S from
-// zero, gradient R handed to the left when none comes from the right, product P.
-template <typename T, int N, int CH, bool ALIGNED, bool ZOH, int TOKENS>
+// zero, gradient R handed to the left when none comes from the right, product P
+// (EXACT: of the decays themselves, not of 1 + E: dh0 is of their size).
+template <typename T, int N, int CH, bool ALIGNED, bool ZOH, int TOKENS, bool EXACT>
 __device__ __forceinline__ void run_sums(const Tile<T, N, CH, ALIGNED> &s, int c, int t0, int n0,
                                          const Decay<ZOH> (&A)[2], f2 (&S)[2], f2 (&R)[2],
                                          f2 (&P)[2]) {
@@ -437,7 +446,7 @@ __device__ __forceinline__ void run_sums(const Tile<T, N, CH, ALIGNED> &s, int c
                 f2 e;
                 const f2 F = A[k].at(dt, e);
                 S[k] = move<ZOH>(F, S[k], f2_mul(in, B[k]));
-                P[k] = f2_mul(P[k], e);  // not by 1 + E: dh0 is of the size of the decays
+                P[k] = EXACT ? f2_mul(P[k], e) : times_decay<ZOH>(P[k], F);
                 R[k] = f2_fma(P[k], f2_mul(dy, C[k]), R[k]);
             }
         }
@@ -482,7 +491,7 @@ scan_bwd_sums(const BwdArgs a, const __grid_constant__ Maps maps) {
         Decay<ZOH> A[2];
         f2 S[2], R[2], P[2];
         load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
-        run_sums<T, N, CH, ALIGNED, ZOH, kChunk>(s, c, 0, n0, A, S, R, P);
+        run_sums<T, N, CH, ALIGNED, ZOH, kChunk, true>(s, c, 0, n0, A, S, R, P);
         if (has) {
             const int64_t at = (p.b * a.nc + p.chunk) * a.D + d0 + c;
             store4x(&a.S[at * N + n0], S);
@@ -691,7 +700,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             Decay<ZOH> A[2];
             f2 S[2], R[2], P[2];
             load_A<T, N, CH, ALIGNED, ZOH>(s, c * N + n0, A);
-            run_sums<T, N, CH, ALIGNED, ZOH, kPiece>(s, c, t0, n0, A, S, R, P);
+            run_sums<T, N, CH, ALIGNED, ZOH, kPiece, false>(s, c, t0, n0, A, S, R, P);
             store4x(&s.S[piece][c * N + n0], S);
             store4x(&s.R[piece][c * N + n0], R);
             store4x(&s.P[piece][c * N + n0], P);
@@ -716,6 +725,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             }
         }
         __syncthreads();
+        const unsigned far = ZOH ? s.far : 0;
         float *dx = a.dx + (p.b * a.L + p.t0 + share0) * a.D + d0 + cl;
         float *ddt = a.ddt + (dx - a.dx);
 #pragma unroll 1
@@ -800,7 +810,7 @@ scan_bwd_main(const BwdArgs a, const __grid_constant__ Maps maps) {
             for (int k = 0; k < 2; ++k)
                 if (ZOH) dA[k] = f2_mul(invA[k], dA[k]);
             store4x(&s.P[piece][c * N + n0], dA);
-            if (ZOH && (s.far >> c & 1)) {
+            if (ZOH && (far >> c & 1)) {
                 const float4 v = far_channel<T, N, CH, ALIGNED>(s, piece, c, n0);
                 vA[0] = v.x, vA[1] = v.y, vA[2] = v.z, vA[3] = v.w;
             }
