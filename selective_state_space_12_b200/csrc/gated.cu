@@ -33,12 +33,12 @@
 //    the inputs that the next round of tiles needs are brought to L2 instead.
 //
 // What bounds it: bytes (8 forward and 14 backward a token and channel in bf16, 0.67
-// and 1.17 GB at b8 L2048 D5120) and, nearly as much, issue: about 100 instructions a
+// and 1.17 GB at b8 L2048 D5120) and, nearly as much, issue: about 80 instructions a
 // pair of channels forward and 140 backward, at 45 to 60 % of the issue slots with 18
-// to 36 warps an SM. Measured there, B200, bf16: forward 140 us (4.8 TB/s), backward
-// 271 us (4.3 TB/s), forward with 8-bit copies 223 us and backward from them 332 us.
-// One row of 65536 tokens by 2048 channels, few lanes: 366 and 551 us. Rows that
-// start anywhere (D5121): 181 and 379 us.
+// to 36 warps an SM. Measured there, B200, bf16: forward 141 us (4.8 TB/s), backward
+// 282 us (4.2 TB/s), forward with 8-bit copies 230 us and backward from them 334 us.
+// One row of 65536 tokens by 2048 channels, few lanes: 364 and 565 us. Rows that
+// start anywhere (D5121): 179 and 371 us.
 //
 // A published word is 64 bits, cleared to all ones before the kernel, and is
 // complete once it differs from that: readers poll the data itself, and no
@@ -938,7 +938,7 @@ __device__ __forceinline__ f2 copy_step(const GatedArgs &a, const Tile &t, int w
 // Bytes of shared memory in which sigmoid(i) waits for the gradients. Spilled registers
 // would wait in L2, which these kernels load most: at b8 L2048, D5121 380 us for 459
 // and from copies (D5120) 333 for 415; plain rows, where fewer registers are
-// spilled, take 284 us with it and 271 without.
+// spilled, took 284 us with it and 271 without.
 template <bool ALIGNED, bool CK>
 constexpr int kBackwardKeep = ALIGNED && !CK ? 0 : kRun * kCompute * 8;
 

@@ -39,12 +39,14 @@
 //      and the bias's gradient over batch and chunks. No atomics: every sum has
 //      one order.
 //
-// Measured, B200, bf16, b8 L2048 D5120 N16 with softplus: hold 3730 us (0.36 T state
-// entries a second), of which the sums take 782 us, the chain 167, the main kernel
-// 2730 and the last sums 53; Euler 2860 us (614, 165, 2030, 53). The main kernel
-// issues about 85 instructions for each pair of entries and token in 55 % of its
-// issue slots: 16 warps an SM at 128 registers a thread, whose latencies (exp2,
-// shared memory, the packed arithmetic) they do not quite hide.
+// Measured, B200, bf16, b8 L2048 D5120 N16 with softplus: hold 4080 us (0.33 T state
+// entries a second), of which the sums take 802 us, the chain 168, the main kernel
+// 3071 and the last sums 54; Euler 2860 us (617, 166, 2035, 54). The main kernel with
+// the hold issues about 103 instructions for each pair of entries and token in 58 % of
+// its issue slots: 16 warps an SM at 128 registers a thread, whose latencies (exp2,
+// shared memory, the packed arithmetic) they do not quite hide. (18 of the 103 are what
+// dA takes to keep its bits at small steps: 85 and 2730 us with the two terms that
+// cancel.)
 #include <cudaTypedefs.h>
 #include <math.h>
 
