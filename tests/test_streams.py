@@ -10,13 +10,11 @@ from selective_state_space_12_b200 import ssd as binding
 
 
 class Stream:
-    device = torch.device("cpu")
-
-    def __init__(self, handle):
-        self.cuda_stream = handle
+    def __init__(self, handle, index=0):
+        self.cuda_stream, self.device = handle, torch.device("cuda", index)
 
 
-CALLER, OWN = Stream(1), Stream(2)
+CALLER, OWN, OTHER_GPU = Stream(1), Stream(2), Stream(3, 1)
 
 
 @pytest.fixture
@@ -34,8 +32,11 @@ def now(monkeypatch):
         finally:
             at.pop()
 
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: at[-1])
+    monkeypatch.setattr(torch.cuda, "set_stream", lambda s: at.__setitem__(-1, s))
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(binding, "_current_handle", lambda device: at[-1].cuda_stream)
     return at
 
 
@@ -50,7 +51,7 @@ def test_scratch_comes_from_the_calls_stream(now, monkeypatch):
              lambda s: ssd.ssd_gated_scan_backward_ckpt8(ck, lam, x, stream=s),
              lambda s: ssd.ssd_selective_scan_backward(x, x, A, B, B, None, None, x, stream=s)]
     for call in calls:
-        for s, want in ((OWN, OWN), (CALLER, CALLER), (None, CALLER)):
+        for s, want in ((OWN, OWN), (CALLER, CALLER), (None, CALLER), (OTHER_GPU, OTHER_GPU)):
             with pytest.raises(ValueError, match="CUDA"):  # the tensors are not on a GPU
                 call(s)
             assert taken.pop() is want and now == [CALLER]
