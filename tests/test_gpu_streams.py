@@ -153,3 +153,38 @@ def test_inputs_dropped_after_the_call():
     others = [torch.zeros_like(x) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(y, want) and len(others) == 4
+
+
+def test_a_side_stream_inside_a_capture():
+    """Calls on a stream that a capture has forked to, twice with an empty cache in
+    between, replayed beside eager calls."""
+    import selective_state_space_12_b200 as ssd
+
+    calls = [gated(3)["gated_scan"], gated(4)["gated_scan_backward"],
+             selective(5)["selective_scan_backward"], layer(6)["forward"]]
+    want = [[t.clone() for t in tensors(c())] for c in calls]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph, side = torch.cuda.CUDAGraph(), [torch.cuda.Stream() for _ in calls]
+        with torch.cuda.graph(graph):
+            now = torch.cuda.current_stream()
+            got = []
+            for c, s in zip(calls, side):
+                s.wait_stream(now)
+                got.append(tensors(c(stream=s)))
+            for s in side:
+                now.wait_stream(s)
+        graphs.append((graph, got))
+        torch.cuda.empty_cache()
+    for _ in range(2):
+        for graph, got in graphs:
+            for t in (t for out in got for t in out):
+                t.zero_()
+            graph.replay()
+            eager = tensors(calls[0]())
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(eager, want[0]))
+            for w, g in zip(want, got):
+                assert all(torch.equal(a, b) for a, b in zip(w, g))
+    assert ssd.ssd_device_status() == 0, ssd.ssd_last_error()
