@@ -117,10 +117,11 @@ __device__ __forceinline__ f2 sigmoid2(f2 v) {
     return f2_pack(rcp_approx(lo), rcp_approx(hi));
 }
 // sigmoid(r) and sigmoid(i) from one reciprocal: with p = 1 + exp(-r) and q = 1 + exp(-i),
-// 1/p = q/(pq). Right where pq stays below kGatesTop (r + i above about -86): whoever
-// takes it adds pq up in `top`, looks at that (gates_open), and takes the gates one by
-// one where it is more, or a gate that is all but shut would not be: m = 1e-9 for 0
-// moves a state over a long masked stretch.
+// 1/p = q/(pq). Right where pq stays below kGatesTop (r + i above about -86): beyond,
+// the reciprocal is flushed to 0, and the open gate with the shut one. Whoever takes it
+// adds pq up in `top`, looks at that (gates_open), and takes the gates one by one where
+// it is more. (Bounded exponents instead keep a masked token's m at 1e-9, which moves a
+// state over a long masked stretch.)
 constexpr float kGatesTop = 0x1p125f;
 __device__ __forceinline__ void two_sigmoids2(f2 r, f2 i, f2 &sr, f2 &si, f2 &top) {
     float r0, r1, i0, i1;

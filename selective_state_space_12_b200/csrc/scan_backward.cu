@@ -170,7 +170,7 @@ __device__ __forceinline__ float off_zero(float A) {
 // Steps at which the hold's forms in the main loop lose bits: -z above kFar for one state
 // (they lose z 2^-24 a rounding, 2e-5 in all at kFar), or above kFast for all of a channel's
 // (ddt is then of a's size, and loses 2^-24 / a). Such a channel's dA and ddt are computed a
-// second time: where all are such, b8 L2048 D5120 takes 5710 us for 4180.
+// second time: where all are such, b8 L2048 D5120 takes 5680 us for 4080.
 constexpr float kFar = 96.f, kFast = 4.f;
 // For a step dt of a channel with -A in [least, most].
 __device__ __forceinline__ bool far_step(float dt, float least, float most) {
